@@ -1,0 +1,246 @@
+// Global gradient norm over many tensors, clipping by it, and the clipped Adam step.
+//
+// norm = sqrt(sum of g^2 over every value), c = min(1, max_norm / (norm + 1e-6)), out = c g.  One read of every gradient
+// for the norm, one more read and a write for the clipping, all bound by memory; with many small tensors the
+// launches are what counts.  So a launch takes up to kTable tensors by value in its parameters, cut into chunks of
+// kChunk values: a block finds a chunk's tensor by bisection and works through chunks blockIdx, blockIdx + grid, ...  The
+// norm leaves one partial sum per block; the next kernel's blocks add the partial sums up by themselves, in one fixed order,
+// instead of an extra launch or an atomic whose order would change the bits.
+#include "wide.cuh"
+
+namespace rs {
+namespace {
+
+constexpr int kTable = 400;         // tensors a launch: 32 KB of kernel parameters hold the table
+constexpr int kChunk = 8192;        // values a block takes at a time: 32 a thread
+constexpr int kNormBlocks = kSms * 6;
+
+struct ClipTable {
+    rs_grad_tensor t[kTable];
+    uint32_t start[kTable + 1];     // first chunk of each tensor
+    int n;
+    const float* part;              // clipping: the partial sums, how many, the limit, the norm's place
+    int parts;
+    float max_norm;
+    float* norm;
+};
+
+__device__ __forceinline__ int tensor_of(const ClipTable& T, uint32_t chunk) {
+    int lo = 0, hi = T.n;           // start[lo] <= chunk < start[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (T.start[mid] <= chunk) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// dL/dparam from dL/dact
+__device__ __forceinline__ float chain(int act, float g, float p) {
+    if (act == RS_ACT_EXP) return g * expf(p);
+    if (act == RS_ACT_SIGMOID) {
+        const float a = 1.0f / (1.0f + expf(-p));
+        return g * (a * (1.0f - a));
+    }
+    return g;
+}
+
+template <typename T>
+__device__ __forceinline__ float chunk_squares(const rs_grad_tensor& d, size_t at, int len) {
+    const T* g = static_cast<const T*>(d.d_grad) + at;
+    const float* p = d.activation == RS_ACT_IDENTITY ? nullptr : d.d_param + at;
+    const bool vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kChunk / (256 * 8); ++i) {
+        const int o = (i * 256 + int(threadIdx.x)) * 8;
+        float v[8], u[8];
+        vec ? load8<T, true>(g + o, len - o, v) : load8<T, false>(g + o, len - o, v);
+        if (p) {
+            vec ? load8<float, true>(p + o, len - o, u) : load8<float, false>(p + o, len - o, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = o + j < len ? chain(d.activation, v[j], u[j]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+    return ss;
+}
+
+__global__ void __launch_bounds__(256) k_grad_squares(const __grid_constant__ ClipTable T, float* part) {
+    RS_PDL_ENTER();
+    __shared__ float sm[8];
+    float ss = 0.f;
+    const uint32_t chunks = T.start[T.n];
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const int i = tensor_of(T, k);
+        const rs_grad_tensor& d = T.t[i];
+        const size_t at = size_t(k - T.start[i]) * kChunk;
+        const int len = int(min((unsigned long long)(d.count - at), (unsigned long long)kChunk));
+        ss += d.dtype == RS_F32 ? chunk_squares<float>(d, at, len)
+            : d.dtype == RS_F16 ? chunk_squares<__half>(d, at, len) : chunk_squares<__nv_bfloat16>(d, at, len);
+    }
+    ss = group_sum<32>(ss);
+    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += sm[i];
+        part[blockIdx.x] = ss;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const rs_grad_tensor& d, size_t at, int len, float c) {
+    const T* g = static_cast<const T*>(d.d_grad) + at;
+    T* out = static_cast<T*>(d.d_out) + at;
+    const bool vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+#pragma unroll
+    for (int i = 0; i < kChunk / (256 * 8); ++i) {
+        const int o = (i * 256 + int(threadIdx.x)) * 8;
+        float v[8];
+        vec ? load8<T, true>(g + o, len - o, v) : load8<T, false>(g + o, len - o, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= c;
+        vec ? store8<T, true>(out + o, len - o, v) : store8<T, false>(out + o, len - o, v);
+    }
+}
+
+__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ ClipTable T) {
+    RS_PDL_ENTER();
+    const float norm = norm_of_parts(T.part, T.parts);
+    if (T.norm && blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
+    const float c = clip_factor(T.max_norm, norm);
+    const uint32_t chunks = T.start[T.n];
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+        const int i = tensor_of(T, k);
+        const rs_grad_tensor& d = T.t[i];
+        if (!d.d_out || (c == 1.f && d.d_out == d.d_grad)) continue;
+        const size_t at = size_t(k - T.start[i]) * kChunk;
+        const int len = int(min((unsigned long long)(d.count - at), (unsigned long long)kChunk));
+        if (d.dtype == RS_F32) chunk_scale<float>(d, at, len, c);
+        else if (d.dtype == RS_F16) chunk_scale<__half>(d, at, len, c);
+        else chunk_scale<__nv_bfloat16>(d, at, len, c);
+    }
+}
+
+// The table of tensors [first, first + kTable), empty ones left out; its chunks in *chunks.
+void fill(ClipTable& T, const rs_grad_tensor* t, int n, int first, uint64_t* chunks) {
+    T.n = 0;
+    uint64_t at = 0;
+    for (int i = first; i < std::min(n, first + kTable); ++i) {
+        if (t[i].count == 0) continue;
+        T.t[T.n] = t[i];
+        T.start[T.n++] = uint32_t(at);
+        at += (t[i].count + kChunk - 1) / kChunk;
+    }
+    T.start[T.n] = uint32_t(at);
+    *chunks = at;
+}
+
+int launches(int n) { return std::max(1, ceil_div(n, kTable)); }
+
+// Partial sums of every launch, kNormBlocks each at most; *parts tells how many were written.
+cudaError_t norm_parts(const rs_grad_tensor* t, int n, float* ws, int* parts, cudaStream_t s) {
+    *parts = 0;
+    for (int l = 0; l < launches(n); ++l) {
+        ClipTable T;
+        uint64_t chunks;
+        fill(T, t, n, l * kTable, &chunks);
+        if (chunks == 0) continue;
+        const int blocks = int(std::min<uint64_t>(chunks, kNormBlocks));
+        const cudaError_t e = pdl_launch(k_grad_squares, blocks, 256, 0, s, T, ws + *parts);
+        if (e != cudaSuccess) return e;
+        *parts += blocks;
+    }
+    return cudaSuccess;
+}
+
+int check(const rs_grad_tensor* t, int32_t n, bool outs, const float* d_norm, const void* ws, size_t bytes) {
+    if (n < 0 || (n > 0 && !t) || !ptr_ok(d_norm, 4) || !ptr_ok(ws, 16)) return RS_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i) {
+        const rs_grad_tensor& d = t[i];
+        if (!dtype_ok(d.dtype) || d.activation < RS_ACT_IDENTITY || d.activation > RS_ACT_SIGMOID) return RS_ERR_INVALID_ARG;
+        if (d.count == 0) continue;
+        if (d.count > (size_t(1) << 36)) return RS_ERR_INVALID_ARG;  // a launch's chunk numbers stay within 32 bits
+        const size_t z = dtype_size(d.dtype);
+        if (!ptr_ok(d.d_grad, z) || (outs && d.d_out && !ptr_ok(d.d_out, z))) return RS_ERR_INVALID_ARG;
+        if (d.activation != RS_ACT_IDENTITY && !ptr_ok(d.d_param, 4)) return RS_ERR_INVALID_ARG;
+    }
+    return bytes < rs_grad_norm_workspace_size(n) ? RS_ERR_WORKSPACE : RS_OK;
+}
+
+int clip(const rs_grad_tensor* t, int n, float max_norm, float* d_norm, void* d_workspace, cudaStream_t s) {
+    float* ws = static_cast<float*>(d_workspace);
+    int parts = 0;
+    if (norm_parts(t, n, ws, &parts, s) != cudaSuccess) return RS_ERR_CUDA;
+    bool any = false;
+    for (int i = 0; i < n; ++i) any = any || t[i].d_out;
+    for (int l = 0; l < (any ? launches(n) : 1); ++l) {
+        ClipTable T;
+        uint64_t chunks = 0;
+        if (any) fill(T, t, n, l * kTable, &chunks);
+        else T.n = 0, T.start[0] = 0;
+        if (chunks == 0 && l > 0) continue;
+        T.part = ws;
+        T.parts = parts;
+        T.max_norm = max_norm;
+        T.norm = l == 0 ? d_norm : nullptr;
+        const int blocks = int(std::max<uint64_t>(1, std::min<uint64_t>(chunks, kSms * 8)));
+        if (pdl_launch(k_grad_scale, blocks, 256, 0, s, T) != cudaSuccess) return RS_ERR_CUDA;
+    }
+    return RS_OK;
+}
+
+}  // namespace
+}  // namespace rs
+
+extern "C" {
+
+size_t rs_grad_norm_workspace_size(int32_t n_tensors) {
+    return n_tensors < 0 ? 0 : size_t(rs::launches(n_tensors)) * rs::kNormBlocks * sizeof(float);
+}
+
+int rs_grad_norm(const rs_grad_tensor* tensors, int32_t n_tensors, float* d_norm, void* d_workspace,
+                 size_t workspace_bytes, void* stream) {
+    const int rc = rs::check(tensors, n_tensors, false, d_norm, d_workspace, workspace_bytes);
+    if (rc != RS_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int parts = 0;
+    if (rs::norm_parts(tensors, n_tensors, static_cast<float*>(d_workspace), &parts, s) != cudaSuccess) return RS_ERR_CUDA;
+    rs::ClipTable T;
+    T.n = 0;
+    T.start[0] = 0;
+    T.part = static_cast<const float*>(d_workspace);
+    T.parts = parts;
+    T.max_norm = 1.f;
+    T.norm = d_norm;
+    return rs::pdl_launch(rs::k_grad_scale, 1, 256, 0, s, T) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_norm, float* d_norm, void* d_workspace,
+                 size_t workspace_bytes, void* stream) {
+    if (!(max_norm > 0.f)) return RS_ERR_INVALID_ARG;
+    const int rc = rs::check(tensors, n_tensors, true, d_norm, d_workspace, workspace_bytes);
+    if (rc != RS_OK) return rc;
+    return rs::clip(tensors, n_tensors, max_norm, d_norm, d_workspace, static_cast<cudaStream_t>(stream));
+}
+
+int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
+                         int32_t step, float max_norm, float* d_norm, void* d_workspace, size_t workspace_bytes,
+                         void* stream) {
+    using namespace rs;
+    if (!adam_args_ok(segs, n_segs, beta1, beta2, eps, step) || !(max_norm > 0.f)) return RS_ERR_INVALID_ARG;
+    if (!ptr_ok(d_norm, 4) || !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+    if (workspace_bytes < rs_grad_norm_workspace_size(n_segs)) return RS_ERR_WORKSPACE;
+    rs_grad_tensor t[RS_ADAM_MAX_SEGMENTS];
+    for (int i = 0; i < n_segs; ++i)
+        t[i] = {segs[i].d_grad, nullptr, segs[i].d_param, segs[i].count, RS_F32, segs[i].activation};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* ws = static_cast<float*>(d_workspace);
+    ClipBy by{ws, 0, max_norm, d_norm};
+    if (norm_parts(t, n_segs, ws, &by.parts, s) != cudaSuccess) return RS_ERR_CUDA;
+    return launch_adam(segs, n_segs, beta1, beta2, eps, step, s, &by) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+}  // extern "C"

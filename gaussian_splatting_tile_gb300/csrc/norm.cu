@@ -1,0 +1,326 @@
+// Root-mean-square norm with the residual's addition and an 8-bit output, and its backward.
+//
+// Forward, per row: s = x + r, rstd = 1 / sqrt(mean s^2 + eps), y = s rstd w, then per 128 columns the largest |y|
+// gives a scale and y becomes e4m3.  Everything is bound by memory: x, r in, s and q out, 7 bytes a value in 16 bits.
+// So a row stays in registers between the two sums: TPR threads hold it as runs of eight consecutive values (16 bytes
+// of a 16-bit type), and a block of 128 columns is the run of 16 neighbouring threads, whose maximum takes four shuffles.
+#include "wide.cuh"
+
+namespace rs {
+namespace {
+
+struct NormArgs {
+    int rows, cols;
+    const void* x; size_t xs;
+    const void* r; size_t rs_;
+    const float* w;
+    float eps, inv_cols;
+    void* sum; size_t sums;
+    void* y; size_t ys;
+    uint8_t* q; size_t qs;
+    float* scales;
+    float* rstd;
+};
+
+// Sum over the TPR threads of a row.  All threads of the block call it (TPR > 32 uses barriers).
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* smem) {
+    v = group_sum<(TPR < 32 ? TPR : 32)>(v);
+    if constexpr (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) v += smem[i];
+    }
+    return v;
+}
+
+template <typename T, bool VEC, int TPR, int RUNS>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs a) {
+    RS_PDL_ENTER();
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    __shared__ float smem[32];
+    const int t = threadIdx.x % TPR;
+    const long long row = (long long)blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool in = row < a.rows;
+    const T* x = static_cast<const T*>(a.x) + (in ? row : 0) * a.xs;
+    const T* r = a.r ? static_cast<const T*>(a.r) + (in ? row : 0) * a.rs_ : nullptr;
+    float v[RUNS][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        load8<T, VEC>(x + c, left, v[i]);
+        if (r) {
+            float u[8];
+            load8<T, VEC>(r + c, left, u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] += u[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[i][j], v[i][j], ss);
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, smem) * a.inv_cols + a.eps);
+    if (in && t == 0 && a.rstd) a.rstd[row] = rstd;
+    if (a.sum && in) {
+        T* s = static_cast<T*>(a.sum) + row * a.sums;
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) store8<T, VEC>(s + (i * TPR + t) * 8, a.cols - (i * TPR + t) * 8, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        float w[8];
+        load8<float, VEC>(a.w + c, left, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
+        if (a.y && left > 0) store8<T, VEC>(static_cast<T*>(a.y) + row * a.ys + c, left, v[i]);
+        if (a.q) {
+            float scale, inv;
+            block_scale(group_max<16>(max_abs8(v[i], 0.f)), scale, inv);
+            if (left > 0) {
+                store8_e4m3(a.q + row * a.qs + c, left, v[i], inv);
+                if ((t & 15) == 0) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
+            }
+        }
+    }
+}
+
+template <typename T, bool VEC, int TPR, int RUNS>
+cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
+    constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
+    return pdl_launch(k_rms_norm_fwd<T, VEC, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
+}
+
+template <typename T, bool VEC>
+cudaError_t fwd_width(const NormArgs& a, cudaStream_t s) {
+    const int runs = ceil_div(a.cols, 8);
+    if (runs <= 16) return fwd<T, VEC, 16, 1>(a, s);
+    if (runs <= 32) return fwd<T, VEC, 32, 1>(a, s);
+    if (runs <= 64) return fwd<T, VEC, 32, 2>(a, s);
+    if (runs <= 128) return fwd<T, VEC, 32, 4>(a, s);
+    if (runs <= 256) return fwd<T, VEC, 128, 2>(a, s);
+    if (runs <= 512) return fwd<T, VEC, 256, 2>(a, s);
+    if (runs <= 1024) return fwd<T, VEC, 512, 2>(a, s);
+    return fwd<T, VEC, 512, 4>(a, s);
+}
+
+// ---------------------------------------------------------------- backward
+struct NormBwdArgs {
+    int rows, cols;
+    const void* s; size_t ss;
+    const float* w;
+    const float* rstd;
+    const void* dy; size_t dys;
+    const void* ds; size_t dss;
+    void* dx; size_t dxs;
+    float* part;                    // [blocks][cols]: each block's sum of dy xh, nullptr: not wanted
+    float inv_cols;
+};
+
+// A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its share of
+// dL/dweight stays in registers and leaves once per block.
+template <typename T, bool VEC, int TPR, int RUNS>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdArgs a) {
+    RS_PDL_ENTER();
+    constexpr int kThreads = TPR < 128 ? 128 : TPR;
+    constexpr int kRows = kThreads / TPR;
+    __shared__ float smem[32];
+    __shared__ float comb[kRows > 1 ? kThreads * 8 : 1];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    float w[RUNS][8], dw[RUNS][8];
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+        const int c = (i * TPR + t) * 8;
+        load8<float, VEC>(a.w + c, a.cols - c, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
+    }
+    for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += (long long)gridDim.x * kRows) {
+        const long long row = base + sub;
+        const bool in = row < a.rows;
+        const long long rr = in ? row : 0;
+        const float rstd = in ? a.rstd[rr] : 0.f;
+        const T* s = static_cast<const T*>(a.s) + rr * a.ss;
+        const T* dy = static_cast<const T*>(a.dy) + rr * a.dys;
+        float xh[RUNS][8], tt[RUNS][8];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+            load8<T, VEC>(s + c, left, xh[i]);
+            load8<T, VEC>(dy + c, left, tt[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                xh[i][j] *= rstd;
+                dw[i][j] = fmaf(tt[i][j], xh[i][j], dw[i][j]);
+                tt[i][j] *= w[i][j];
+                dot = fmaf(tt[i][j], xh[i][j], dot);
+            }
+        }
+        const float c1 = row_sum<TPR>(dot, smem) * a.inv_cols;
+        if (in) {
+            const T* ds = a.ds ? static_cast<const T*>(a.ds) + row * a.dss : nullptr;
+            T* dx = static_cast<T*>(a.dx) + row * a.dxs;
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                const int c = (i * TPR + t) * 8, left = a.cols - c;
+                float o[8];
+                if (ds) {
+                    load8<T, VEC>(ds + c, left, o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) o[j] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, tt[i][j] - xh[i][j] * c1, o[j]);
+                store8<T, VEC>(dx + c, left, o);
+            }
+        }
+    }
+    if (!a.part) return;
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+        const int c = (i * TPR + t) * 8;
+        if constexpr (kRows > 1) {
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) comb[threadIdx.x * 8 + j] = dw[i][j];
+            __syncthreads();
+            if (sub == 0)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    for (int k = 1; k < kRows; ++k) dw[i][j] += comb[(k * TPR + t) * 8 + j];
+        }
+        if (sub == 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (c + j < a.cols) a.part[size_t(blockIdx.x) * a.cols + c + j] = dw[i][j];
+    }
+}
+
+// Column sums of part [n][cols] in a fixed order: 32 columns a block, 32 threads a column.
+__global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ part, int n, int cols,
+                                                      float* __restrict__ out) {
+    RS_PDL_ENTER();
+    __shared__ float sm[32][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    float v = 0.f;
+    if (c < cols)
+        for (int i = g; i < n; i += 32) v += part[size_t(i) * cols + c];
+    sm[g][threadIdx.x & 31] = v;
+    __syncthreads();
+    v = group_sum<32>(sm[threadIdx.x & 31][g]);
+    const int oc = blockIdx.x * 32 + g;
+    if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = v;
+}
+
+int bwd_rows_per_block(int cols) { return cols <= 128 ? 8 : cols <= 1024 ? 4 : 1; }
+int bwd_blocks(int rows, int cols) {
+    const int per = cols <= 512 ? 6 : cols <= 1024 ? 4 : cols <= 4096 ? 2 : 1;
+    return std::max(1, std::min(ceil_div(rows, bwd_rows_per_block(cols)), kSms * per));
+}
+
+template <typename T, bool VEC, int TPR, int RUNS>
+cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
+    return pdl_launch(k_rms_norm_bwd<T, VEC, TPR, RUNS>, bwd_blocks(a.rows, a.cols), TPR < 128 ? 128 : TPR, 0, s, a);
+}
+
+template <typename T, bool VEC>
+cudaError_t bwd_width(const NormBwdArgs& a, cudaStream_t s) {
+    const int runs = ceil_div(a.cols, 8);
+    if (runs <= 16) return bwd<T, VEC, 16, 1>(a, s);
+    if (runs <= 32) return bwd<T, VEC, 32, 1>(a, s);
+    if (runs <= 64) return bwd<T, VEC, 32, 2>(a, s);
+    if (runs <= 128) return bwd<T, VEC, 32, 4>(a, s);
+    if (runs <= 256) return bwd<T, VEC, 128, 2>(a, s);
+    if (runs <= 512) return bwd<T, VEC, 256, 2>(a, s);
+    if (runs <= 1024) return bwd<T, VEC, 512, 2>(a, s);
+    return bwd<T, VEC, 512, 4>(a, s);
+}
+
+bool matrix_ok(const void* p, size_t stride, int32_t cols, int32_t dtype) {
+    return ptr_ok(p, dtype_size(dtype)) && stride >= size_t(cols);
+}
+
+}  // namespace
+}  // namespace rs
+
+extern "C" {
+
+int rs_rms_norm_fwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
+                    const void* d_residual, size_t residual_stride, const float* d_weight, float eps, void* d_sum,
+                    size_t sum_stride, void* d_y, size_t y_stride, uint8_t* d_q, size_t q_stride, float* d_scales,
+                    float* d_rstd, void* stream) {
+    using namespace rs;
+    if (rows < 0 || cols < 1 || cols > RS_NORM_MAX_COLS || !dtype_ok(dtype) || !(eps >= 0.f) || !isfinite(eps))
+        return RS_ERR_INVALID_ARG;
+    if (rows == 0) return RS_OK;
+    const size_t z = dtype_size(dtype);
+    if (!matrix_ok(d_x, x_stride, cols, dtype) || !ptr_ok(d_weight, 4)) return RS_ERR_INVALID_ARG;
+    if (d_residual && !matrix_ok(d_residual, residual_stride, cols, dtype)) return RS_ERR_INVALID_ARG;
+    if (d_sum && !matrix_ok(d_sum, sum_stride, cols, dtype)) return RS_ERR_INVALID_ARG;
+    if (d_sum && ((d_sum == d_x && sum_stride != x_stride) || (d_sum == d_residual && sum_stride != residual_stride)))
+        return RS_ERR_INVALID_ARG;
+    if (d_y && !matrix_ok(d_y, y_stride, cols, dtype)) return RS_ERR_INVALID_ARG;
+    if ((d_q == nullptr) != (d_scales == nullptr) || (!d_q && !d_y)) return RS_ERR_INVALID_ARG;
+    if (d_q && (!fp8_rows_ok(d_q, q_stride, cols) || !ptr_ok(d_scales, 4))) return RS_ERR_INVALID_ARG;
+    if (d_rstd && !ptr_ok(d_rstd, 4)) return RS_ERR_INVALID_ARG;
+    const bool vec = ptr_ok(d_weight, 16) && rows16(d_x, x_stride, z) && (!d_residual || rows16(d_residual, residual_stride, z)) &&
+                     (!d_sum || rows16(d_sum, sum_stride, z)) && (!d_y || rows16(d_y, y_stride, z));
+    NormArgs a{rows, cols, d_x, x_stride, d_residual, residual_stride, d_weight, eps, 1.0f / float(cols), d_sum,
+               sum_stride, d_y, y_stride, d_q, q_stride, d_scales, d_rstd};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = with_dtype(dtype, [&](auto v) {
+        using T = decltype(v);
+        return vec ? fwd_width<T, true>(a, s) : fwd_width<T, false>(a, s);
+    });
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+size_t rs_rms_norm_bwd_workspace_size(int32_t rows, int32_t cols) {
+    if (rows < 0 || cols < 1 || cols > RS_NORM_MAX_COLS) return 0;
+    return size_t(rs::bwd_blocks(rows, cols)) * cols * sizeof(float);
+}
+
+int rs_rms_norm_bwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_s, size_t s_stride,
+                    const float* d_weight, const float* d_rstd, const void* d_dL_dy, size_t dy_stride,
+                    const void* d_dL_dsum, size_t dsum_stride, void* d_dL_dx, size_t dx_stride, float* d_dL_dweight,
+                    void* d_workspace, size_t workspace_bytes, void* stream) {
+    using namespace rs;
+    if (rows < 0 || cols < 1 || cols > RS_NORM_MAX_COLS || !dtype_ok(dtype)) return RS_ERR_INVALID_ARG;
+    if (d_dL_dweight && !ptr_ok(d_dL_dweight, 4)) return RS_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        if (!d_dL_dweight) return RS_OK;
+        return cudaMemsetAsync(d_dL_dweight, 0, size_t(cols) * 4, s) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    }
+    const size_t z = dtype_size(dtype);
+    if (!matrix_ok(d_s, s_stride, cols, dtype) || !matrix_ok(d_dL_dy, dy_stride, cols, dtype) ||
+        !matrix_ok(d_dL_dx, dx_stride, cols, dtype) || !ptr_ok(d_weight, 4) || !ptr_ok(d_rstd, 4))
+        return RS_ERR_INVALID_ARG;
+    if (d_dL_dsum && !matrix_ok(d_dL_dsum, dsum_stride, cols, dtype)) return RS_ERR_INVALID_ARG;
+    if ((d_dL_dx == d_dL_dy && dx_stride != dy_stride) || (d_dL_dx == d_dL_dsum && dx_stride != dsum_stride))
+        return RS_ERR_INVALID_ARG;
+    if (d_dL_dweight) {
+        if (!ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+        if (workspace_bytes < rs_rms_norm_bwd_workspace_size(rows, cols)) return RS_ERR_WORKSPACE;
+    }
+    const bool vec = ptr_ok(d_weight, 16) && rows16(d_s, s_stride, z) && rows16(d_dL_dy, dy_stride, z) && rows16(d_dL_dx, dx_stride, z) &&
+                     (!d_dL_dsum || rows16(d_dL_dsum, dsum_stride, z));
+    NormBwdArgs a{rows, cols, d_s, s_stride, d_weight, d_rstd, d_dL_dy, dy_stride, d_dL_dsum, dsum_stride, d_dL_dx,
+                  dx_stride, d_dL_dweight ? static_cast<float*>(d_workspace) : nullptr, 1.0f / float(cols)};
+    cudaError_t e = with_dtype(dtype, [&](auto v) {
+        using T = decltype(v);
+        return vec ? bwd_width<T, true>(a, s) : bwd_width<T, false>(a, s);
+    });
+    if (e == cudaSuccess && d_dL_dweight)
+        e = pdl_launch(k_column_sums, ceil_div(cols, 32), 1024, 0, s, static_cast<const float*>(a.part),
+                       bwd_blocks(rows, cols), cols, d_dL_dweight);
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -8,7 +8,7 @@
 // kernel applies the activation's derivative first and writes the activated value of the updated
 // parameter, which is what the projection reads next.  Per element: read param, grad, m, v;
 // write param, m, v (and the activated value): HBM-bound.
-#include "rs_internal.cuh"
+#include "wide.cuh"
 
 namespace rs {
 namespace {
@@ -22,6 +22,10 @@ struct AdamTable {
     size_t quads[RS_ADAM_MAX_SEGMENTS];
     int n;
     float beta1, beta2, omb1, omb2, eps, rc1, rc2;  // omb = 1 - beta, rc = 1 / (1 - beta^t)
+    const float* part;                              // the clipped step: partial sums of squares,
+    int parts;                                      // how many, the limit, and where the norm goes
+    float max_norm;
+    float* norm;
 };
 
 __device__ __forceinline__ float adam_one(const AdamTable& T, int act, float lr, float& p, float g, float& m,
@@ -40,8 +44,18 @@ __device__ __forceinline__ float adam_one(const AdamTable& T, int act, float lr,
     return act == RS_ACT_EXP ? expf(p) : act == RS_ACT_SIGMOID ? 1.0f / (1.0f + expf(-p)) : p;
 }
 
-__global__ void __launch_bounds__(256) k_adam(AdamTable T) {
+// CLIP: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by itself
+// (a few KB in L2; a launch fewer than a kernel between); a norm that is not finite leaves everything as it is.
+template <bool CLIP>
+__global__ void __launch_bounds__(256) k_adam(const __grid_constant__ AdamTable T) {
     RS_PDL_ENTER();
+    float coef = 1.f;
+    if constexpr (CLIP) {
+        const float norm = norm_of_parts(T.part, T.parts);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
+        if (!isfinite(norm)) return;
+        coef = clip_factor(T.max_norm, norm);
+    }
     const size_t stride = size_t(gridDim.x) * blockDim.x;
     const size_t nq = T.qstart[T.n];
     for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < nq; i += stride) {
@@ -50,7 +64,8 @@ __global__ void __launch_bounds__(256) k_adam(AdamTable T) {
         const rs_adam_segment& S = T.seg[s];
         const size_t k = i - T.qstart[s];
         float4 p = reinterpret_cast<const float4*>(S.d_param)[k];
-        const float4 g = reinterpret_cast<const float4*>(S.d_grad)[k];
+        float4 g = reinterpret_cast<const float4*>(S.d_grad)[k];
+        if constexpr (CLIP) g = make_float4(g.x * coef, g.y * coef, g.z * coef, g.w * coef);
         float4 m = reinterpret_cast<const float4*>(S.d_m)[k];
         float4 v = reinterpret_cast<const float4*>(S.d_v)[k];
         float4 a;
@@ -70,7 +85,7 @@ __global__ void __launch_bounds__(256) k_adam(AdamTable T) {
         const rs_adam_segment& S = T.seg[s];
         const size_t k = 4 * T.quads[s] + (i - T.tstart[s]);
         float p = S.d_param[k], m = S.d_m[k], v = S.d_v[k];
-        const float a = adam_one(T, S.activation, S.lr, p, S.d_grad[k], m, v);
+        const float a = adam_one(T, S.activation, S.lr, p, CLIP ? S.d_grad[k] * coef : S.d_grad[k], m, v);
         S.d_m[k] = m;
         S.d_v[k] = v;
         S.d_param[k] = p;
@@ -95,7 +110,7 @@ __global__ void __launch_bounds__(256) k_densify_stats(int n, const float* __res
 }  // namespace
 
 cudaError_t launch_adam(const rs_adam_segment* segs, int n, double beta1, double beta2, double eps, int step,
-                        cudaStream_t s) {
+                        cudaStream_t s, const ClipBy* clip) {
     AdamTable T{};
     T.n = n;
     for (int i = 0; i < n; ++i) {
@@ -116,9 +131,16 @@ cudaError_t launch_adam(const rs_adam_segment* segs, int n, double beta1, double
     T.rc1 = float(1.0 / (1.0 - std::pow(beta1, double(step))));
     T.rc2 = float(1.0 / (1.0 - std::pow(beta2, double(step))));
     const size_t total = std::max(T.qstart[n], T.tstart[n]);
-    if (total == 0) return cudaSuccess;
-    const unsigned blocks = unsigned(std::min<size_t>((total + 255) / 256, 152 * 16));
-    pdl_launch(k_adam, blocks, 256, 0, s, T);
+    if (total == 0 && !clip) return cudaSuccess;
+    const unsigned blocks = unsigned(std::max<size_t>(1, std::min<size_t>((total + 255) / 256, 152 * 16)));
+    if (clip) {
+        T.part = clip->part;
+        T.parts = clip->parts;
+        T.max_norm = clip->max_norm;
+        T.norm = clip->norm;
+        return pdl_launch(k_adam<true>, blocks, 256, 0, s, T);
+    }
+    pdl_launch(k_adam<false>, blocks, 256, 0, s, T);
     return cudaGetLastError();
 }
 

@@ -60,6 +60,23 @@ bool mlp_ok(const rs_mlp* m) {
 
 }  // namespace
 
+namespace rs {
+
+bool adam_args_ok(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps, int32_t step) {
+    if (!segs || n_segs < 0 || n_segs > RS_ADAM_MAX_SEGMENTS || step < 1) return false;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps > 0.0) || !isfinite(eps)) return false;
+    for (int i = 0; i < n_segs; ++i) {
+        const rs_adam_segment& g = segs[i];
+        if (g.activation < RS_ACT_IDENTITY || g.activation > RS_ACT_SIGMOID || !isfinite(g.lr)) return false;
+        if (g.count == 0) continue;
+        if (!dev_f(g.d_param) || !dev_f(g.d_grad) || !dev_f(g.d_m) || !dev_f(g.d_v)) return false;
+        if (g.d_activated && !aligned(g.d_activated, 4)) return false;
+    }
+    return true;
+}
+
+}  // namespace rs
+
 extern "C" {
 
 const char* rs_error_string(int code) {
@@ -67,7 +84,7 @@ const char* rs_error_string(int code) {
         case RS_OK: return "success";
         case RS_ERR_INVALID_ARG: return "invalid argument (null or misaligned pointer, bad size or parameter)";
         case RS_ERR_CAPACITY: return "entry count exceeds capacity; *n_entries holds the required count";
-        case RS_ERR_WORKSPACE: return "workspace smaller than rs_bin_workspace_size reports";
+        case RS_ERR_WORKSPACE: return "workspace smaller than the call's workspace size function reports";
         case RS_ERR_CUDA: return "CUDA runtime error";
         case RS_ERR_DEVICE_TIMEOUT: return "a bounded wait inside a kernel gave up; the outputs are not valid";
         case RS_ERR_DEVICE_CHECK:
@@ -269,16 +286,7 @@ int rs_l1_loss_grad(size_t count, const float* d_image, const float* d_target, f
 
 int rs_adam_step(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
                  int32_t step, void* stream) {
-    if (!segs || n_segs < 0 || n_segs > RS_ADAM_MAX_SEGMENTS || step < 1) return RS_ERR_INVALID_ARG;
-    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !(eps > 0.0) || !isfinite(eps))
-        return RS_ERR_INVALID_ARG;
-    for (int i = 0; i < n_segs; ++i) {
-        const rs_adam_segment& g = segs[i];
-        if (g.activation < RS_ACT_IDENTITY || g.activation > RS_ACT_SIGMOID || !isfinite(g.lr)) return RS_ERR_INVALID_ARG;
-        if (g.count == 0) continue;
-        if (!dev_f(g.d_param) || !dev_f(g.d_grad) || !dev_f(g.d_m) || !dev_f(g.d_v)) return RS_ERR_INVALID_ARG;
-        if (g.d_activated && !aligned(g.d_activated, 4)) return RS_ERR_INVALID_ARG;
-    }
+    if (!rs::adam_args_ok(segs, n_segs, beta1, beta2, eps, step)) return RS_ERR_INVALID_ARG;
     return cuda_rc(rs::launch_adam(segs, n_segs, beta1, beta2, eps, step, static_cast<cudaStream_t>(stream)));
 }
 
@@ -293,8 +301,9 @@ int rs_densify_stats(int32_t n, const float* d_dL_dmeans2d, const int32_t* d_rad
 
 int rs_device_error(void) {
     const int a = rs::take_device_error(), b = rs::take_projection_error(), c = rs::take_raster_check();
-    if (a < 0 || b < 0 || c < 0) return RS_ERR_CUDA;
-    return c > 0 ? RS_ERR_DEVICE_CHECK : a > 0 || b > 0 ? RS_ERR_DEVICE_TIMEOUT : RS_OK;
+    const int d = rs::take_matmul_error();
+    if (a < 0 || b < 0 || c < 0 || d < 0) return RS_ERR_CUDA;
+    return c > 0 ? RS_ERR_DEVICE_CHECK : a > 0 || b > 0 || d > 0 ? RS_ERR_DEVICE_TIMEOUT : RS_OK;
 }
 
 int rs_l1_dssim_workspace_size(int32_t channels, int32_t height, int32_t width, size_t* bytes) {

@@ -309,8 +309,17 @@ cudaError_t launch_l1_dssim(int C, int H, int W, const float* img, const float* 
                             float* dimg, float* loss, void* ws, cudaStream_t s);
 
 // Fused Adam over parameter groups and the densification statistics.
+bool adam_args_ok(const rs_adam_segment* segs, int32_t n, double beta1, double beta2, double eps, int32_t step);
+int take_matmul_error();  // as take_device_error, of the 8-bit matrix product
+// Partial sums of squares of the gradients (csrc/clip.cu), from which the clipped step forms the norm.
+struct ClipBy {
+    const float* part;
+    int parts;
+    float max_norm;
+    float* norm;
+};
 cudaError_t launch_adam(const rs_adam_segment* segs, int n, double beta1, double beta2, double eps, int step,
-                        cudaStream_t s);
+                        cudaStream_t s, const ClipBy* clip = nullptr);
 cudaError_t launch_densify_stats(int n, const float* dm2, const int* radius, float* accum, float* count,
                                  cudaStream_t s);
 

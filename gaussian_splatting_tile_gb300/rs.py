@@ -149,6 +149,20 @@ def lib():
         L.rs_l1_dssim_loss_grad.argtypes = [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _VP, _VP, ctypes.c_float,
                                             ctypes.c_float, _VP, _VP, _VP, ctypes.c_size_t, _VP]
         L.rs_device_error.argtypes = []
+        i32, sz = ctypes.c_int32, ctypes.c_size_t
+        L.rs_rms_norm_fwd.argtypes = [i32, i32, i32, _VP, sz, _VP, sz, _VP, ctypes.c_float, _VP, sz, _VP, sz, _VP, sz,
+                                      _VP, _VP, _VP]
+        L.rs_rms_norm_bwd_workspace_size.argtypes = [i32, i32]
+        L.rs_rms_norm_bwd.argtypes = [i32, i32, i32, _VP, sz, _VP, _VP, _VP, sz, _VP, sz, _VP, sz, _VP, _VP, sz, _VP]
+        L.rs_quantize_fp8.argtypes = [i32, i32, i32, _VP, sz, _VP, sz, _VP, sz, _VP, _VP, sz, _VP, _VP]
+        L.rs_quantize_fp8_blocks.argtypes = [i32, i32, i32, _VP, sz, _VP, sz, _VP, _VP, sz, _VP, _VP]
+        L.rs_matmul_fp8_workspace_size.argtypes = [i32, i32, i32]
+        L.rs_matmul_fp8.argtypes = [i32, i32, i32, _VP, sz, _VP, _VP, sz, _VP, i32, i32, i32, _VP, sz, _VP, sz, _VP]
+        L.rs_grad_norm_workspace_size.argtypes = [i32]
+        L.rs_grad_norm.argtypes = [_VP, i32, _VP, _VP, sz, _VP]
+        L.rs_grad_clip.argtypes = [_VP, i32, ctypes.c_float, _VP, _VP, sz, _VP]
+        L.rs_adam_step_clipped.argtypes = [ctypes.POINTER(rs_adam_segment), i32, ctypes.c_double, ctypes.c_double,
+                                           ctypes.c_double, i32, ctypes.c_float, _VP, _VP, sz, _VP]
         for ret, name in declared_signatures():
             getattr(L, name).restype = _RESTYPES[ret]
         _lib = L
@@ -559,8 +573,7 @@ class AdamGroup:
     activated: torch.Tensor | None = None
 
 
-def rs_adam_step(groups, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-15,
-                 stream=None):
+def _adam_segments(groups):
     if len(groups) > RS_ADAM_MAX_SEGMENTS:
         raise ValueError(f"at most {RS_ADAM_MAX_SEGMENTS} groups per call")
     arr = (rs_adam_segment * max(1, len(groups)))()
@@ -574,6 +587,12 @@ def rs_adam_step(groups, step: int, beta1: float = 0.9, beta2: float = 0.999, ep
         arr[i].count = k
         arr[i].lr = float(gr.lr)
         arr[i].activation = int(gr.activation)
+    return arr
+
+
+def rs_adam_step(groups, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-15,
+                 stream=None):
+    arr = _adam_segments(groups)
     _check("rs_adam_step", lib().rs_adam_step(arr, len(groups), float(beta1), float(beta2), float(eps), int(step),
                                               _stream(stream)))
 
@@ -672,3 +691,211 @@ def rs_l1_dssim_loss_grad(image: torch.Tensor, target: torch.Tensor, lam: float,
         ctypes.c_float(lam), ctypes.c_float(scale), _ptr(dL_dimage, torch.float32, n, "dL_dimage"),
         _ptr(loss, torch.float32, 1, "loss"), _ptr(workspace, torch.uint8, None, "workspace"),
         int(workspace.numel()), _stream(stream)))
+
+
+# ------------------------------------------------------------------ wide appearance networks
+
+RS_F32, RS_F16, RS_BF16 = 0, 1, 2
+RS_FP8_BLOCK, RS_NORM_MAX_COLS = 128, 16384
+_DTYPES = {torch.float32: RS_F32, torch.float16: RS_F16, torch.bfloat16: RS_BF16}
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _dtype(t, name="tensor") -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return code
+
+
+def _mat(t, name, dtype, rows: int, cols: int):
+    """(pointer, row stride in elements) of a row-major CUDA matrix [rows, cols]; its rows may be apart."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs {(rows, cols)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"{name} must be contiguous along its rows")
+    # a single row's stride is never followed: give one that the alignment rules allow
+    return t.data_ptr(), (s0 if rows > 1 else -(-cols // 16) * 16)
+
+
+def fp8_empty(rows: int, cols: int, device="cuda"):
+    """An 8-bit matrix [rows, cols] with rows on 16-byte boundaries, and its scales [ceil(cols / 128), rows]."""
+    q = torch.empty(rows, max(16, -(-cols // 16) * 16), dtype=torch.uint8, device=device)
+    return (q.view(torch.float8_e4m3fn)[:, :cols],
+            torch.empty(-(-cols // RS_FP8_BLOCK), rows, dtype=torch.float32, device=device))
+
+
+def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """The float32 values of an 8-bit matrix with scales per row or per 128 x 128 block (plain torch, for inspection)."""
+    r, c = q.shape
+    s = scales if scales.shape[1] == r else scales.repeat_interleave(RS_FP8_BLOCK, 1)[:, :r]
+    return q.view(torch.float8_e4m3fn).float() * s.repeat_interleave(RS_FP8_BLOCK, 0)[:c].t()
+
+
+def _scales(t, name, blocks: int, rows: int):
+    p = _ptr(t, torch.float32, None, name)
+    if t is not None and t.shape != (blocks, rows):
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs {(blocks, rows)}")
+    return p
+
+
+def _blocks(n: int) -> int:
+    return -(-n // RS_FP8_BLOCK)
+
+
+def rs_rms_norm_fwd(x, weight, q=None, scales=None, residual=None, sum=None, y=None, rstd=None, eps: float = 1e-6,
+                    stream=None):
+    """x, residual, sum, y: [rows, cols] float32 / float16 / bfloat16 CUDA; weight float32 [cols]; q, scales as
+    fp8_empty(rows, cols) gives them; rstd float32 [rows].  sum, y and rstd are optional outputs."""
+    rows, cols = x.shape
+    dt = x.dtype
+    code = _dtype(x, "x")
+    px, sx = _mat(x, "x", dt, rows, cols)
+    pr, sr = _mat(residual, "residual", dt, rows, cols)
+    ps, ss = _mat(sum, "sum", dt, rows, cols)
+    py, sy = _mat(y, "y", dt, rows, cols)
+    pq, sq = _mat(q, "q", _FP8, rows, cols)
+    _check("rs_rms_norm_fwd", lib().rs_rms_norm_fwd(
+        rows, cols, code, px, sx, pr, sr, _ptr(weight, torch.float32, cols, "weight"), eps, ps, ss, py, sy, pq, sq,
+        _scales(scales, "scales", _blocks(cols), rows), _ptr(rstd, torch.float32, rows, "rstd"), _stream(stream)))
+
+
+def rs_rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().rs_rms_norm_bwd_workspace_size(int(rows), int(cols)))
+
+
+def rs_rms_norm_bwd(s, weight, rstd, dL_dy, dL_dx, dL_dweight, workspace, dL_dsum=None, stream=None):
+    """s: the forward's sum (x without a residual); dL_dx also is the residual's gradient; dL_dweight may be None."""
+    rows, cols = s.shape
+    dt = s.dtype
+    code = _dtype(s, "s")
+    ps, ss = _mat(s, "s", dt, rows, cols)
+    pg, sg = _mat(dL_dy, "dL_dy", dt, rows, cols)
+    pd, sd = _mat(dL_dsum, "dL_dsum", dt, rows, cols)
+    px, sx = _mat(dL_dx, "dL_dx", dt, rows, cols)
+    _check("rs_rms_norm_bwd", lib().rs_rms_norm_bwd(
+        rows, cols, code, ps, ss, _ptr(weight, torch.float32, cols, "weight"), _ptr(rstd, torch.float32, rows, "rstd"),
+        pg, sg, pd, sd, px, sx, _ptr(dL_dweight, torch.float32, cols, "dL_dweight"),
+        _ptr(workspace, torch.uint8, None, "workspace"), 0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def rs_quantize_fp8(x, q=None, scales=None, qt=None, scales_t=None, relu=None, stream=None):
+    """8-bit forms of x [rows, cols]: q, scales as fp8_empty(rows, cols), and / or the transpose qt, scales_t as
+    fp8_empty(cols, rows).  relu: a relu's output; x counts as zero where it is <= 0."""
+    rows, cols = x.shape
+    code = _dtype(x, "x")
+    px, sx = _mat(x, "x", x.dtype, rows, cols)
+    pr, sr = _mat(relu, "relu", x.dtype, rows, cols)
+    pq, sq = _mat(q, "q", _FP8, rows, cols)
+    pt, st = _mat(qt, "qt", _FP8, cols, rows)
+    _check("rs_quantize_fp8", lib().rs_quantize_fp8(
+        rows, cols, code, px, sx, pr, sr, pq, sq, _scales(scales, "scales", _blocks(cols), rows), pt, st,
+        _scales(scales_t, "scales_t", _blocks(rows), cols), _stream(stream)))
+
+
+def rs_quantize_fp8_blocks(x, q=None, scales=None, qt=None, scales_t=None, stream=None):
+    """As rs_quantize_fp8 with one scale per 128 x 128 block: scales [ceil(cols / 128), ceil(rows / 128)], scales_t its
+    transpose."""
+    rows, cols = x.shape
+    code = _dtype(x, "x")
+    px, sx = _mat(x, "x", x.dtype, rows, cols)
+    pq, sq = _mat(q, "q", _FP8, rows, cols)
+    pt, st = _mat(qt, "qt", _FP8, cols, rows)
+    _check("rs_quantize_fp8_blocks", lib().rs_quantize_fp8_blocks(
+        rows, cols, code, px, sx, pq, sq, _scales(scales, "scales", _blocks(cols), _blocks(rows)), pt, st,
+        _scales(scales_t, "scales_t", _blocks(rows), _blocks(cols)), _stream(stream)))
+
+
+def rs_matmul_fp8_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().rs_matmul_fp8_workspace_size(int(m), int(n), int(k)))
+
+
+def rs_matmul_fp8(a, a_scales, b, b_scales, out, workspace=None, relu: bool = False, stream=None):
+    """out [m, n] (float32, float16 or bfloat16) = a [m, k] b [n, k]^T.  a_scales [ceil(k / 128), m]; b_scales per row of b
+    [ceil(k / 128), n] or per 128 x 128 block [ceil(k / 128), ceil(n / 128)]."""
+    m, k = a.shape
+    n = b.shape[0]
+    kb = _blocks(k)
+    pa, sa = _mat(a, "a", _FP8, m, k)
+    pb, sb = _mat(b, "b", _FP8, n, k)
+    po, so = _mat(out, "out", out.dtype, m, n)
+    per_row = b_scales.shape == (kb, n)
+    _check("rs_matmul_fp8", lib().rs_matmul_fp8(
+        m, n, k, pa, sa, _scales(a_scales, "a_scales", kb, m), pb, sb,
+        _scales(b_scales, "b_scales", kb, n if per_row else _blocks(n)), 1 if per_row else RS_FP8_BLOCK, int(relu),
+        _dtype(out, "out"), po, so, _ptr(workspace, torch.uint8, None, "workspace"),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+class rs_grad_tensor(ctypes.Structure):
+    _fields_ = [("d_grad", _VP), ("d_out", _VP), ("d_param", _VP), ("count", ctypes.c_size_t),
+                ("dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+@dataclasses.dataclass
+class GradTensor:
+    """One gradient of rs_grad_norm / rs_grad_clip (float32, float16 or bfloat16 CUDA, contiguous).  out: where the
+    clipped values go (may be grad itself; None: only the norm).  With an activation, param holds the stored float32
+    parameters and the norm counts dL/dparam."""
+    grad: torch.Tensor
+    out: torch.Tensor | None = None
+    param: torch.Tensor | None = None
+    activation: int = RS_ACT_IDENTITY
+
+
+class GradTable:
+    """A list of GradTensor marshalled once, for a loop that clips the same buffers every step."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)  # keeps the buffers alive
+        self.n = len(self.tensors)
+        self.arr = (rs_grad_tensor * max(1, self.n))()
+        for e, g in zip(self.arr, self.tensors):
+            k = int(g.grad.numel())
+            e.dtype = _dtype(g.grad, "grad")
+            e.d_grad = _ptr(g.grad, None, k, "grad")
+            e.d_out = _ptr(g.out, g.grad.dtype, k, "out")
+            e.d_param = _ptr(g.param, torch.float32, k, "param")
+            e.count, e.activation = k, int(g.activation)
+
+
+def _table(tensors) -> GradTable:
+    return tensors if isinstance(tensors, GradTable) else GradTable(tensors)
+
+
+def rs_grad_norm_workspace_size(n_tensors: int = RS_ADAM_MAX_SEGMENTS) -> int:
+    return int(lib().rs_grad_norm_workspace_size(int(n_tensors)))
+
+
+def rs_grad_norm(tensors, norm: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """norm (float32 CUDA [1]) = the global norm of `tensors` (a GradTable or a list of GradTensor)."""
+    t = _table(tensors)
+    _check("rs_grad_norm", lib().rs_grad_norm(t.arr, t.n, _ptr(norm, torch.float32, 1, "norm"),
+                                              _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+                                              _stream(stream)))
+
+
+def rs_grad_clip(tensors, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor, stream=None):
+    """rs_grad_norm, and every tensor's out = grad * min(1, max_norm / (norm + 1e-6))."""
+    t = _table(tensors)
+    _check("rs_grad_clip", lib().rs_grad_clip(t.arr, t.n, float(max_norm), _ptr(norm, torch.float32, 1, "norm"),
+                                              _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+                                              _stream(stream)))
+
+
+def rs_adam_step_clipped(groups, step: int, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor,
+                         beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-15, stream=None):
+    """rs_adam_step on the gradients clipped to the global norm max_norm (nothing waits on the host; a norm that is not
+    finite skips the step)."""
+    arr = _adam_segments(groups)
+    _check("rs_adam_step_clipped", lib().rs_adam_step_clipped(
+        arr, len(groups), float(beta1), float(beta2), float(eps), int(step), float(max_norm),
+        _ptr(norm, torch.float32, 1, "norm"), _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+        _stream(stream)))
