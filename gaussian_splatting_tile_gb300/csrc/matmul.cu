@@ -2,8 +2,13 @@
 //
 //   out[i][j] = sum_b sa[b][i] sb[b][j] sum_{t in block b} a[i][t] b[j][t]
 //
-// The scales change with the block, so a block's products are summed by themselves and added, scaled, to the float32
-// total.
+// The inner sums are e4m3 products on the tensor cores (tcgen05.mma kind::f8f6f4, operands staged in shared memory by
+// TMA, accumulators in tensor memory).  The scales change from block to block, so a block's 128 products are summed by
+// themselves in tensor memory and then added, scaled, to a float32 total that stays in the registers of the threads
+// that read it back: thread = row, so a's scale is one number a thread, and with a scale per 128 rows of b one number a
+// warp -- one fused multiply-add per value and block.
+#include <cuda.h>
+
 #include "wide.cuh"
 
 namespace rs {
@@ -13,64 +18,325 @@ __device__ unsigned int g_matmul_error;  // set when a bounded wait gave up
 
 struct MatmulArgs {
     int m, n, k;
-    const uint8_t* a; size_t as;
-    const float* sa;
-    const uint8_t* b; size_t bs;
-    const float* sb;
-    int b_rows;                 // rows of b that share a scale: 1 or 128
+    const float* sa;            // [blocks][m]
+    const float* sb;            // [blocks][n], or [blocks][ceil(n / 128)]
     int relu;
     void* out; size_t os;
+    int vec;                    // rows of out take 16-byte stores
+    int splits, tiles_n, tiles;
+    float* part;                // splits > 1: [split][tile][column][128 rows]
 };
 
-__device__ __forceinline__ float e4m3_to_f(uint8_t x) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(x)));
-    return __half2float(__ushort_as_half(uint16_t(h)));
+// ---------------------------------------------------------------- tensor cores, TMA, barriers
+constexpr uint32_t kWaitPolls = 1u << 20;  // of at most a microsecond each
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return uint32_t(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
+    const uint32_t addr = smem_u32(b);
+    for (uint32_t i = 0; i < kWaitPolls; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok) : "r"(addr), "r"(parity) : "memory");
+        if (ok) return true;
+    }
+    atomicOr(&g_matmul_error, 1u);
+    return false;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) k_matmul_fp8(MatmulArgs g) {
+// A tile's corner (x: element along the row, y: row); x is a multiple of 128 bytes.
+__device__ __forceinline__ void tma_load(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+
+// Matrix descriptor of a K-major operand in 128-byte swizzled rows (PTX ISA "Matrix Descriptors"): address >> 4, groups of
+// eight rows 1024 bytes apart (bits 32-45), 0b001 at bits 46-48, 128-byte swizzle = 2 at bits 61-63.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(64) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(2) << 61);
+}
+
+// Instruction descriptor of kind::f8f6f4 with e4m3 operands (type 0), both K-major, float32 sums.
+template <int M, int N>
+__host__ __device__ constexpr uint32_t tc_idesc() { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 columns of this warp's 32 lanes; the registers are valid after tc_wait.
+__device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void tc_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));  // no use of them moves above the wait
+}
+
+// ---------------------------------------------------------------- the tile kernel
+// A CTA takes 128 x BN tiles of out (and one of `splits` stretches of the blocks), persistently.  Warp 0 loads, warp 1
+// issues the products, warps 2 to 9 add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on, and one half of the
+// columns.  Tensor memory holds two accumulators of BN columns: the products of block b + 1 run while block b is read.
+template <int BN>
+struct TileSmem {
+    static constexpr int kStages = BN == 256 ? 4 : 6;  // 192 KB of operands either way
+    uint8_t a[kStages][128 * 128];
+    uint8_t b[kStages][BN * 128];
+};
+
+struct Range { int first, last; };
+__device__ __forceinline__ Range split_blocks(int blocks, int splits, int s) {
+    return {int((long long)blocks * s / splits), int((long long)blocks * (s + 1) / splits)};
+}
+
+template <typename T, int BN, bool ROWS>
+__global__ void __launch_bounds__(320, 1) k_matmul_tile(const __grid_constant__ CUtensorMap map_a,
+                                                        const __grid_constant__ CUtensorMap map_b, MatmulArgs g) {
     RS_PDL_ENTER();
-    __shared__ float sa[64][33], sb[64][33];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const long long i0 = (long long)blockIdx.x * 64, j0 = (long long)blockIdx.y * 64;
-    float total[4][4] = {};
-    for (int b = 0; b * kBlock < g.k; ++b) {
-        float part[4][4] = {};
-        for (int t0 = b * kBlock; t0 < min(g.k, (b + 1) * kBlock); t0 += 32) {
-            for (int e = threadIdx.x; e < 64 * 32; e += 256) {
-                const int r = e >> 5, t = t0 + (e & 31);
-                sa[r][e & 31] = i0 + r < g.m && t < g.k ? e4m3_to_f(g.a[(i0 + r) * g.as + t]) : 0.f;
-                sb[r][e & 31] = j0 + r < g.n && t < g.k ? e4m3_to_f(g.b[(j0 + r) * g.bs + t]) : 0.f;
-            }
-            __syncthreads();
-            for (int t = 0; t < 32; ++t)
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) part[y][x] = fmaf(sa[ty + 16 * y][t], sb[tx + 16 * x][t], part[y][x]);
-            __syncthreads();
-        }
-        const int per = g.b_rows == 1 ? g.n : (g.n + kBlock - 1) / kBlock;
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const long long i = i0 + ty + 16 * y, j = j0 + tx + 16 * x;
-                if (i < g.m && j < g.n)
-                    total[y][x] = fmaf(g.sa[size_t(b) * g.m + i] * g.sb[size_t(b) * per + j / g.b_rows], part[y][x],
-                                       total[y][x]);
-            }
+    using Smem = TileSmem<BN>;
+    constexpr int kStages = Smem::kStages, kCols = BN / 2;
+    extern __shared__ uint8_t raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ __align__(16) float sbuf[ROWS ? 8 : 1][2][ROWS ? kCols : 4];  // ROWS: a warp's scales of b
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
+        for (int i = 0; i < 2; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 8);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const long long i = i0 + ty + 16 * y, j = j0 + tx + 16 * x;
-            float v = total[y][x];
-            if (g.relu && v < 0.f) v = 0.f;
-            if (i < g.m && j < g.n) static_cast<T*>(g.out)[i * g.os + j] = from_f<T>(v);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(2 * BN)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_slot;
+    const int blocks = (g.k + kBlock - 1) / kBlock;
+    const int units = g.tiles * g.splits;
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const int tile = u % g.tiles, y = tile / g.tiles_n * 128, x = tile % g.tiles_n * BN;
+                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                for (int b = r.first; b < r.last; ++b, ++it) {
+                    const uint32_t s = it % kStages;
+                    if (!(ok = bar_wait(&empty[s], (it / kStages & 1) ^ 1))) break;
+                    bar_expect(&full[s], (128 + BN) * 128);
+                    tma_load(&map_a, sm.a[s], &full[s], b * kBlock, y);
+                    tma_load(&map_b, sm.b[s], &full[s], b * kBlock, x);
+                }
+            }
+            // no copy and no arrival may outlast the CTA: every stage that was filled is waited for
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
+                if (!ok) bar_wait(&full[i % kStages], i / kStages & 1);
+                else bar_wait(&empty[i % kStages], i / kStages & 1);
+            }
         }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                for (int b = r.first; b < r.last; ++b, ++it) {
+                    const uint32_t s = it % kStages, h = it & 1;
+                    if (!(ok = bar_wait(&full[s], it / kStages & 1) && bar_wait(&acc_empty[h], (it >> 1 & 1) ^ 1))) break;
+                    tc_after();
+                    const uint64_t da = tc_desc(smem_u32(sm.a[s])), db = tc_desc(smem_u32(sm.b[s]));
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)  // 32 bytes of K an instruction
+                        tc_mma(tmem + h * BN, da + 2 * t, db + 2 * t, tc_idesc<128, BN>(), t > 0);
+                    tc_commit(&empty[s]);
+                    tc_commit(&acc_full[h]);
+                }
+            }
+            if (!ok && it > 0) bar_wait(&acc_full[(it - 1) & 1], (it - 1) >> 1 & 1);  // products in flight
+        }
+        __syncwarp();
+    } else {
+        const int half = (warp - 2) >> 2, wrow = (warp & 3) * 32 + lane;  // half of the columns, row of the tile
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + half * kCols;
+        const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;         // b's scales a block
+        uint32_t it = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const int tile = u % g.tiles, split = u / g.tiles;
+            const long long row = (long long)(tile / g.tiles_n) * 128 + wrow;
+            const int col = tile % g.tiles_n * BN + half * kCols;
+            const Range r = split_blocks(blocks, g.splits, split);
+            const bool in = row < g.m && col < g.n;
+            const float* sa = g.sa + row;
+            // b's scales of one block: a number for the warp, or one for each of its columns
+            constexpr int kSb = ROWS ? kCols / 32 : 1;
+            float na = 0.f, nb[kSb];
+            auto load_scales = [&](int b) {
+                na = in ? sa[size_t(b) * g.m] : 0.f;
+#pragma unroll
+                for (int i = 0; i < kSb; ++i) {
+                    const int c = ROWS ? col + 32 * i + lane : col / kBlock;
+                    nb[i] = c < per ? g.sb[size_t(b) * per + c] : 0.f;
+                }
+            };
+            if (r.first < r.last) load_scales(r.first);
+            float acc[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
+            for (int b = r.first; b < r.last; ++b, ++it) {
+                const uint32_t h = it & 1;
+                const float f = ROWS ? na : na * nb[0];
+                float* sb = sbuf[ROWS ? warp - 2 : 0][h];
+                if (ROWS) {
+#pragma unroll
+                    for (int i = 0; i < kSb; ++i) sb[32 * i + lane] = nb[i];
+                    __syncwarp();
+                }
+                if (b + 1 < r.last) load_scales(b + 1);  // a block ahead
+                ok = __all_sync(0xffffffffu, bar_wait(&acc_full[h], it >> 1 & 1));
+                if (!ok) break;
+                tc_after();
+                uint32_t v[2][16];
+                tc_ld16(lanes + h * BN, v[0]);
+#pragma unroll
+                for (int c = 0; c < kCols / 16; ++c) {
+                    tc_wait(v[c & 1]);
+                    if (c + 1 < kCols / 16) tc_ld16(lanes + h * BN + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float p = __uint_as_float(v[c & 1][j]);
+                        acc[16 * c + j] = fmaf(ROWS ? p * sb[16 * c + j] : p, f, acc[16 * c + j]);
+                    }
+                }
+                tc_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&acc_empty[h]);
+            }
+            if (!ok) break;
+            if (g.splits > 1) {
+                float* o = g.part + (size_t(u) * BN + half * kCols) * 128 + wrow;
+#pragma unroll
+                for (int j = 0; j < kCols; ++j) o[size_t(j) * 128] = acc[j];
+            } else if (row < g.m) {
+                T* o = static_cast<T*>(g.out) + row * g.os + col;
+#pragma unroll
+                for (int j = 0; j < kCols; j += 8) {
+                    float w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = g.relu && acc[j + i] < 0.f ? 0.f : acc[j + i];
+                    if (g.vec) store8<T, true>(o + j, g.n - col - j, w);
+                    else store8<T, false>(o + j, g.n - col - j, w);
+                }
+            }
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+}
+
+// out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row reads
+// 128 consecutive floats a warp group, and the values leave through shared memory along out's rows.
+template <typename T>
+__global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
+    RS_PDL_ENTER();
+    __shared__ float sm[8][129];
+    const int groups = bn / 8, tile = blockIdx.x / groups, c0 = blockIdx.x % groups * 8;
+    const int row = threadIdx.x & 127, cc = (threadIdx.x >> 7) * 4;
+    const float* p = g.part + (size_t(tile) * bn + c0 + cc) * 128 + row;
+    const size_t step = size_t(g.tiles) * bn * 128;
+    float v[4] = {};
+    for (int s = 0; s < g.splits; ++s, p += step)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += p[j * 128];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sm[cc + j][row] = g.relu && v[j] < 0.f ? 0.f : v[j];
+    __syncthreads();
+    const int c = threadIdx.x & 7;
+    const long long col = (long long)(tile % g.tiles_n) * bn + c0 + c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 32 + int(threadIdx.x >> 3);
+        const long long gr = (long long)(tile / g.tiles_n) * 128 + r;
+        if (gr < g.m && col < g.n) static_cast<T*>(g.out)[gr * g.os + col] = from_f<T>(sm[c][r]);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+struct Plan {
+    int bn, splits, tiles_n, tiles;
+    size_t workspace() const { return splits > 1 ? size_t(splits) * tiles * bn * 128 * sizeof(float) : 0; }
+};
+
+Plan plan_matmul(int m, int n, int k) {
+    Plan p;
+    p.bn = n > 128 ? 256 : 128;
+    p.tiles_n = ceil_div(n, p.bn);
+    const long long tiles = (long long)ceil_div(m, 128) * p.tiles_n;
+    p.tiles = int(std::min<long long>(tiles, 0x7fffffff));
+    const int blocks = ceil_div(k, kBlock);
+    p.splits = tiles >= kSms ? 1 : std::max(1, std::min(kSms / p.tiles, blocks / 8));
+    return p;
+}
+
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+EncodeTiled encode_tiled() {
+    static const EncodeTiled f = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// A [rows][cols] matrix of bytes, read in boxes of 128 columns and `box` rows; what lies outside reads as zero.
+bool encode(CUtensorMap* map, const uint8_t* p, size_t stride, int rows, int cols, int box) {
+    const EncodeTiled f = encode_tiled();
+    if (!f) return false;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride)};
+    const cuuint32_t boxes[2] = {128, cuuint32_t(box)}, steps[2] = {1, 1};
+    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, boxes, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int BN, bool ROWS>
+cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
+    constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
+    const cudaError_t e = cudaFuncSetAttribute(k_matmul_tile<T, BN, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return pdl_launch(k_matmul_tile<T, BN, ROWS>, std::min(kSms, g.tiles * g.splits), 320, smem, s, a, b, g);
 }
 
 }  // namespace
@@ -88,7 +354,9 @@ int take_matmul_error() {
 
 extern "C" {
 
-size_t rs_matmul_fp8_workspace_size(int32_t, int32_t, int32_t) { return 0; }
+size_t rs_matmul_fp8_workspace_size(int32_t m, int32_t n, int32_t k) {
+    return m <= 0 || n <= 0 || k <= 0 ? 0 : rs::plan_matmul(m, n, k).workspace();
+}
 
 int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride, const float* d_a_scales,
                   const uint8_t* d_b, size_t b_stride, const float* d_b_scales, int32_t b_scale_rows, int32_t relu,
@@ -98,18 +366,32 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     if (m < 0 || n < 0 || k < 0 || !dtype_ok(out_dtype) || (b_scale_rows != 1 && b_scale_rows != kBlock))
         return RS_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return RS_OK;
-    if (!ptr_ok(d_out, dtype_size(out_dtype)) || out_stride < size_t(n)) return RS_ERR_INVALID_ARG;
-    if (k > 0 && (!fp8_rows_ok(d_a, a_stride, k) || !fp8_rows_ok(d_b, b_stride, k) || !ptr_ok(d_a_scales, 4) ||
-                  !ptr_ok(d_b_scales, 4)))
+    const size_t z = dtype_size(out_dtype);
+    if (!ptr_ok(d_out, z) || out_stride < size_t(n)) return RS_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k == 0)
+        return cudaMemset2DAsync(d_out, out_stride * z, 0, n * z, m, s) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    if (!fp8_rows_ok(d_a, a_stride, k) || !fp8_rows_ok(d_b, b_stride, k) || !ptr_ok(d_a_scales, 4) ||
+        !ptr_ok(d_b_scales, 4) || a_stride >= (size_t(1) << 40) || b_stride >= (size_t(1) << 40))
         return RS_ERR_INVALID_ARG;
-    const size_t need = rs_matmul_fp8_workspace_size(m, n, k);
-    if (need > 0 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
-    if (workspace_bytes < need) return RS_ERR_WORKSPACE;
-    MatmulArgs g{m, n, k, d_a, a_stride, d_a_scales, d_b, b_stride, d_b_scales, b_scale_rows, relu, d_out, out_stride};
-    const cudaError_t e = with_dtype(out_dtype, [&](auto v) {
-        return pdl_launch(k_matmul_fp8<decltype(v)>, dim3(ceil_div(m, 64), ceil_div(n, 64)), 256, 0,
-                          static_cast<cudaStream_t>(stream), g);
+    if ((long long)ceil_div(m, 128) * ceil_div(n, 128) > 0x3fffffff) return RS_ERR_INVALID_ARG;
+    const Plan p = plan_matmul(m, n, k);
+    if (p.splits > 1 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+    if (p.splits > 1 && workspace_bytes < p.workspace()) return RS_ERR_WORKSPACE;
+    CUtensorMap ma, mb;
+    if (!encode(&ma, d_a, a_stride, m, k, 128) || !encode(&mb, d_b, b_stride, n, k, p.bn)) return RS_ERR_CUDA;
+    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z),
+                 p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
+    cudaError_t e = with_dtype(out_dtype, [&](auto v) {
+        using T = decltype(v);
+        if (p.bn == 256)
+            return b_scale_rows == 1 ? launch_tile<T, 256, true>(ma, mb, g, s) : launch_tile<T, 256, false>(ma, mb, g, s);
+        return b_scale_rows == 1 ? launch_tile<T, 128, true>(ma, mb, g, s) : launch_tile<T, 128, false>(ma, mb, g, s);
     });
+    if (e == cudaSuccess && p.splits > 1)
+        e = with_dtype(out_dtype, [&](auto v) {
+            return pdl_launch(k_matmul_join<decltype(v)>, unsigned(p.tiles) * (p.bn / 8), 256, 0, s, g, p.bn);
+        });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
