@@ -2,8 +2,8 @@
 //
 // norm = sqrt(sum of g^2 over every value), c = min(1, max_norm / (norm + 1e-6)), out = c g.  One read of every gradient
 // for the norm, one more read and a write for the clipping, all bound by memory; with many small tensors the
-// launches are what counts.  So a launch takes up to kTable tensors by value in its parameters, cut into chunks of
-// kChunk values: a block finds a chunk's tensor by bisection and works through chunks blockIdx, blockIdx + grid, ...  The
+// launches are what counts.  So a launch takes up to kTable tensors by value in its parameters (a table of kSmallTable where
+// that is enough: the parameters are copied at every launch), cut into chunks of kChunk values: a block finds a chunk's tensor by bisection and works through chunks blockIdx, blockIdx + grid, ...  The
 // norm leaves one partial sum per block; the next kernel's blocks add the partial sums up by themselves, in one fixed order,
 // instead of an extra launch or an atomic whose order would change the bits.
 #include "wide.cuh"
@@ -12,12 +12,14 @@ namespace rs {
 namespace {
 
 constexpr int kTable = 400;         // tensors a launch: 32 KB of kernel parameters hold the table
+constexpr int kSmallTable = 48;
 constexpr int kChunk = 8192;        // values a block takes at a time: 32 a thread
 constexpr int kNormBlocks = kSms * 6;
 
+template <int N>
 struct ClipTable {
-    rs_grad_tensor t[kTable];
-    uint32_t start[kTable + 1];     // first chunk of each tensor
+    rs_grad_tensor t[N];
+    uint32_t start[N + 1];          // first chunk of each tensor
     int n;
     const float* part;              // clipping: the partial sums, how many, the limit, the norm's place
     int parts;
@@ -25,7 +27,8 @@ struct ClipTable {
     float* norm;
 };
 
-__device__ __forceinline__ int tensor_of(const ClipTable& T, uint32_t chunk) {
+template <int N>
+__device__ __forceinline__ int tensor_of(const ClipTable<N>& T, uint32_t chunk) {
     int lo = 0, hi = T.n;           // start[lo] <= chunk < start[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -66,7 +69,8 @@ __device__ __forceinline__ float chunk_squares(const rs_grad_tensor& d, size_t a
     return ss;
 }
 
-__global__ void __launch_bounds__(256) k_grad_squares(const __grid_constant__ ClipTable T, float* part) {
+template <int N>
+__global__ void __launch_bounds__(256) k_grad_squares(const __grid_constant__ ClipTable<N> T, float* part) {
     RS_PDL_ENTER();
     __shared__ float sm[8];
     float ss = 0.f;
@@ -106,7 +110,8 @@ __device__ __forceinline__ void chunk_scale(const rs_grad_tensor& d, size_t at, 
     }
 }
 
-__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ ClipTable T) {
+template <int N>
+__global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ ClipTable<N> T) {
     RS_PDL_ENTER();
     const float norm = norm_of_parts(T.part, T.parts);
     if (T.norm && blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
@@ -124,34 +129,58 @@ __global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ Clip
     }
 }
 
-// The table of tensors [first, first + kTable), empty ones left out; its chunks in *chunks.
-void fill(ClipTable& T, const rs_grad_tensor* t, int n, int first, uint64_t* chunks) {
+// The table of tensors [first, first + N), empty ones left out; returns its chunks.
+template <int N>
+uint64_t fill(ClipTable<N>& T, const rs_grad_tensor* t, int n, int first) {
     T.n = 0;
     uint64_t at = 0;
-    for (int i = first; i < std::min(n, first + kTable); ++i) {
+    for (int i = first; i < std::min(n, first + N); ++i) {
         if (t[i].count == 0) continue;
         T.t[T.n] = t[i];
         T.start[T.n++] = uint32_t(at);
         at += (t[i].count + kChunk - 1) / kChunk;
     }
     T.start[T.n] = uint32_t(at);
-    *chunks = at;
+    return at;
 }
 
 int launches(int n) { return std::max(1, ceil_div(n, kTable)); }
 
 // Partial sums of every launch, kNormBlocks each at most; *parts tells how many were written.
-cudaError_t norm_parts(const rs_grad_tensor* t, int n, float* ws, int* parts, cudaStream_t s) {
+template <int N>
+cudaError_t norm_parts_t(const rs_grad_tensor* t, int n, float* ws, int* parts, cudaStream_t s) {
     *parts = 0;
-    for (int l = 0; l < launches(n); ++l) {
-        ClipTable T;
-        uint64_t chunks;
-        fill(T, t, n, l * kTable, &chunks);
+    for (int first = 0; first < n; first += N) {
+        ClipTable<N> T;
+        const uint64_t chunks = fill(T, t, n, first);
         if (chunks == 0) continue;
         const int blocks = int(std::min<uint64_t>(chunks, kNormBlocks));
-        const cudaError_t e = pdl_launch(k_grad_squares, blocks, 256, 0, s, T, ws + *parts);
+        const cudaError_t e = pdl_launch(k_grad_squares<N>, blocks, 256, 0, s, T, ws + *parts);
         if (e != cudaSuccess) return e;
         *parts += blocks;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t norm_parts(const rs_grad_tensor* t, int n, float* ws, int* parts, cudaStream_t s) {
+    return n <= kSmallTable ? norm_parts_t<kSmallTable>(t, n, ws, parts, s) : norm_parts_t<kTable>(t, n, ws, parts, s);
+}
+
+// The norm from its partial sums, and the tensors scaled by it (n = 0: only the norm).
+template <int N>
+cudaError_t scale_by(const rs_grad_tensor* t, int n, float max_norm, float* d_norm, const float* ws, int parts,
+                     cudaStream_t s) {
+    for (int first = 0; first == 0 || first < n; first += N) {
+        ClipTable<N> T;
+        const uint64_t chunks = fill(T, t, n, first);
+        if (chunks == 0 && first > 0) continue;
+        T.part = ws;
+        T.parts = parts;
+        T.max_norm = max_norm;
+        T.norm = first == 0 ? d_norm : nullptr;
+        const int blocks = int(std::max<uint64_t>(1, std::min<uint64_t>(chunks, kSms * 8)));
+        const cudaError_t e = pdl_launch(k_grad_scale<N>, blocks, 256, 0, s, T);
+        if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -170,28 +199,6 @@ int check(const rs_grad_tensor* t, int32_t n, bool outs, const float* d_norm, co
     return bytes < rs_grad_norm_workspace_size(n) ? RS_ERR_WORKSPACE : RS_OK;
 }
 
-int clip(const rs_grad_tensor* t, int n, float max_norm, float* d_norm, void* d_workspace, cudaStream_t s) {
-    float* ws = static_cast<float*>(d_workspace);
-    int parts = 0;
-    if (norm_parts(t, n, ws, &parts, s) != cudaSuccess) return RS_ERR_CUDA;
-    bool any = false;
-    for (int i = 0; i < n; ++i) any = any || t[i].d_out;
-    for (int l = 0; l < (any ? launches(n) : 1); ++l) {
-        ClipTable T;
-        uint64_t chunks = 0;
-        if (any) fill(T, t, n, l * kTable, &chunks);
-        else T.n = 0, T.start[0] = 0;
-        if (chunks == 0 && l > 0) continue;
-        T.part = ws;
-        T.parts = parts;
-        T.max_norm = max_norm;
-        T.norm = l == 0 ? d_norm : nullptr;
-        const int blocks = int(std::max<uint64_t>(1, std::min<uint64_t>(chunks, kSms * 8)));
-        if (pdl_launch(k_grad_scale, blocks, 256, 0, s, T) != cudaSuccess) return RS_ERR_CUDA;
-    }
-    return RS_OK;
-}
-
 }  // namespace
 }  // namespace rs
 
@@ -206,16 +213,10 @@ int rs_grad_norm(const rs_grad_tensor* tensors, int32_t n_tensors, float* d_norm
     const int rc = rs::check(tensors, n_tensors, false, d_norm, d_workspace, workspace_bytes);
     if (rc != RS_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* ws = static_cast<float*>(d_workspace);
     int parts = 0;
-    if (rs::norm_parts(tensors, n_tensors, static_cast<float*>(d_workspace), &parts, s) != cudaSuccess) return RS_ERR_CUDA;
-    rs::ClipTable T;
-    T.n = 0;
-    T.start[0] = 0;
-    T.part = static_cast<const float*>(d_workspace);
-    T.parts = parts;
-    T.max_norm = 1.f;
-    T.norm = d_norm;
-    return rs::pdl_launch(rs::k_grad_scale, 1, 256, 0, s, T) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    if (rs::norm_parts(tensors, n_tensors, ws, &parts, s) != cudaSuccess) return RS_ERR_CUDA;
+    return rs::scale_by<rs::kSmallTable>(nullptr, 0, 1.f, d_norm, ws, parts, s) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
 int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_norm, float* d_norm, void* d_workspace,
@@ -223,7 +224,16 @@ int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_nor
     if (!(max_norm > 0.f)) return RS_ERR_INVALID_ARG;
     const int rc = rs::check(tensors, n_tensors, true, d_norm, d_workspace, workspace_bytes);
     if (rc != RS_OK) return rc;
-    return rs::clip(tensors, n_tensors, max_norm, d_norm, d_workspace, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    float* ws = static_cast<float*>(d_workspace);
+    int parts = 0;
+    if (rs::norm_parts(tensors, n_tensors, ws, &parts, s) != cudaSuccess) return RS_ERR_CUDA;
+    bool any = false;
+    for (int i = 0; i < n_tensors; ++i) any = any || tensors[i].d_out;
+    const int n = any ? n_tensors : 0;
+    const cudaError_t e = n <= rs::kSmallTable ? rs::scale_by<rs::kSmallTable>(tensors, n, max_norm, d_norm, ws, parts, s)
+                                               : rs::scale_by<rs::kTable>(tensors, n, max_norm, d_norm, ws, parts, s);
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
 int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,

@@ -178,9 +178,13 @@ def _check(fn: str, code: int):
         raise RsError(fn, code, error_string(code))
 
 
+# the current stream's handle without building a Stream object (3 us of a small call's 13), where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+
+
 def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -714,7 +718,7 @@ def _mat(t, name, dtype, rows: int, cols: int):
         return None, 0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtype if isinstance(dtype, tuple) else t.dtype != dtype:
+    if t.dtype is not dtype and (dtype is not _FP8 or t.dtype not in _FP8):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} is {tuple(t.shape)}, needs {(rows, cols)}")
@@ -722,7 +726,16 @@ def _mat(t, name, dtype, rows: int, cols: int):
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
     # a single row's stride is never followed: give one that the alignment rules allow
-    return t.data_ptr(), (s0 if rows > 1 else -(-cols // 16) * 16)
+    return t.data_ptr(), (s0 if rows > 1 else (cols + 15) // 16 * 16)
+
+
+def _vec(t, dtype, numel: int, name: str):
+    """Pointer of a contiguous CUDA tensor of at least `numel` elements."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
+        return _ptr(t, dtype, numel, name)  # says what is wrong
+    return t.data_ptr()
 
 
 def fp8_empty(rows: int, cols: int, device="cuda"):
@@ -740,7 +753,7 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
 
 
 def _scales(t, name, blocks: int, rows: int):
-    p = _ptr(t, torch.float32, None, name)
+    p = _vec(t, torch.float32, 0, name)
     if t is not None and t.shape != (blocks, rows):
         raise ValueError(f"{name} is {tuple(t.shape)}, needs {(blocks, rows)}")
     return p
@@ -763,8 +776,8 @@ def rs_rms_norm_fwd(x, weight, q=None, scales=None, residual=None, sum=None, y=N
     py, sy = _mat(y, "y", dt, rows, cols)
     pq, sq = _mat(q, "q", _FP8, rows, cols)
     _check("rs_rms_norm_fwd", lib().rs_rms_norm_fwd(
-        rows, cols, code, px, sx, pr, sr, _ptr(weight, torch.float32, cols, "weight"), eps, ps, ss, py, sy, pq, sq,
-        _scales(scales, "scales", _blocks(cols), rows), _ptr(rstd, torch.float32, rows, "rstd"), _stream(stream)))
+        rows, cols, code, px, sx, pr, sr, _vec(weight, torch.float32, cols, "weight"), eps, ps, ss, py, sy, pq, sq,
+        _scales(scales, "scales", _blocks(cols), rows), _vec(rstd, torch.float32, rows, "rstd"), _stream(stream)))
 
 
 def rs_rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
@@ -781,9 +794,9 @@ def rs_rms_norm_bwd(s, weight, rstd, dL_dy, dL_dx, dL_dweight, workspace, dL_dsu
     pd, sd = _mat(dL_dsum, "dL_dsum", dt, rows, cols)
     px, sx = _mat(dL_dx, "dL_dx", dt, rows, cols)
     _check("rs_rms_norm_bwd", lib().rs_rms_norm_bwd(
-        rows, cols, code, ps, ss, _ptr(weight, torch.float32, cols, "weight"), _ptr(rstd, torch.float32, rows, "rstd"),
-        pg, sg, pd, sd, px, sx, _ptr(dL_dweight, torch.float32, cols, "dL_dweight"),
-        _ptr(workspace, torch.uint8, None, "workspace"), 0 if workspace is None else workspace.numel(), _stream(stream)))
+        rows, cols, code, ps, ss, _vec(weight, torch.float32, cols, "weight"), _vec(rstd, torch.float32, rows, "rstd"),
+        pg, sg, pd, sd, px, sx, _vec(dL_dweight, torch.float32, cols, "dL_dweight"),
+        _vec(workspace, torch.uint8, 0, "workspace"), 0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
 def rs_quantize_fp8(x, q=None, scales=None, qt=None, scales_t=None, relu=None, stream=None):
@@ -830,7 +843,7 @@ def rs_matmul_fp8(a, a_scales, b, b_scales, out, workspace=None, relu: bool = Fa
     _check("rs_matmul_fp8", lib().rs_matmul_fp8(
         m, n, k, pa, sa, _scales(a_scales, "a_scales", kb, m), pb, sb,
         _scales(b_scales, "b_scales", kb, n if per_row else _blocks(n)), 1 if per_row else RS_FP8_BLOCK, int(relu),
-        _dtype(out, "out"), po, so, _ptr(workspace, torch.uint8, None, "workspace"),
+        _dtype(out, "out"), po, so, _vec(workspace, torch.uint8, 0, "workspace"),
         0 if workspace is None else workspace.numel(), _stream(stream)))
 
 
@@ -877,16 +890,16 @@ def rs_grad_norm_workspace_size(n_tensors: int = RS_ADAM_MAX_SEGMENTS) -> int:
 def rs_grad_norm(tensors, norm: torch.Tensor, workspace: torch.Tensor, stream=None):
     """norm (float32 CUDA [1]) = the global norm of `tensors` (a GradTable or a list of GradTensor)."""
     t = _table(tensors)
-    _check("rs_grad_norm", lib().rs_grad_norm(t.arr, t.n, _ptr(norm, torch.float32, 1, "norm"),
-                                              _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+    _check("rs_grad_norm", lib().rs_grad_norm(t.arr, t.n, _vec(norm, torch.float32, 1, "norm"),
+                                              _vec(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
                                               _stream(stream)))
 
 
 def rs_grad_clip(tensors, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor, stream=None):
     """rs_grad_norm, and every tensor's out = grad * min(1, max_norm / (norm + 1e-6))."""
     t = _table(tensors)
-    _check("rs_grad_clip", lib().rs_grad_clip(t.arr, t.n, float(max_norm), _ptr(norm, torch.float32, 1, "norm"),
-                                              _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+    _check("rs_grad_clip", lib().rs_grad_clip(t.arr, t.n, float(max_norm), _vec(norm, torch.float32, 1, "norm"),
+                                              _vec(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
                                               _stream(stream)))
 
 
@@ -897,5 +910,5 @@ def rs_adam_step_clipped(groups, step: int, max_norm: float, norm: torch.Tensor,
     arr = _adam_segments(groups)
     _check("rs_adam_step_clipped", lib().rs_adam_step_clipped(
         arr, len(groups), float(beta1), float(beta2), float(eps), int(step), float(max_norm),
-        _ptr(norm, torch.float32, 1, "norm"), _ptr(workspace, torch.uint8, None, "workspace"), workspace.numel(),
+        _vec(norm, torch.float32, 1, "norm"), _vec(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
         _stream(stream)))
