@@ -263,6 +263,161 @@ __global__ void __launch_bounds__(320, 1) k_matmul_tile(const __grid_constant__ 
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
 }
 
+// ---------------------------------------------------------------- few rows
+// With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
+// (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that every SM
+// reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its CTAs' sums
+// through distributed shared memory, rank by rank, each CTA finishing some of the columns.
+template <int NT>
+struct RowsSmem {
+    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = 128 / NT, kMaxStages = 8;
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+template <typename T, int NT, bool ROWS>
+__global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUtensorMap map_a,
+                                                     const __grid_constant__ CUtensorMap map_b, MatmulArgs g, int stages) {
+    RS_PDL_ENTER();
+    constexpr int kStage = RowsSmem<NT>::kStage, kAcc = RowsSmem<NT>::kAcc, kMax = RowsSmem<NT>::kMaxStages;
+    extern __shared__ uint8_t raw[];
+    uint8_t* ops = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    __shared__ uint64_t full[kMax], empty[kMax], acc_full[kAcc], acc_empty[kAcc];
+    __shared__ uint32_t tmem_slot;
+    __shared__ __align__(16) float sbuf[4][2][NT];  // a warp's copy of a's scales of one block
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % g.splits, tile = blockIdx.x / g.splits, n0 = tile * 128;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
+        for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 4);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(128)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_slot;
+    const Range r = split_blocks((g.k + kBlock - 1) / kBlock, g.splits, rank);
+    const int count = r.last - r.first;
+    const int wrow = (warp & 3) * 32 + lane;
+    float acc[NT];
+    bool ok = true;
+    if (warp == 0) {
+        if (lane == 0) {
+            int it = 0;
+            for (; it < count; ++it) {
+                const int s = it % stages;
+                if (!(ok = bar_wait(&empty[s], (it / stages & 1) ^ 1))) break;
+                bar_expect(&full[s], kStage);
+                tma_load(&map_b, ops + s * kStage, &full[s], (r.first + it) * kBlock, n0);
+                tma_load(&map_a, ops + s * kStage + 128 * 128, &full[s], (r.first + it) * kBlock, 0);
+            }
+            for (int i = max(0, it - stages); i < it; ++i)  // no copy and no arrival may outlast the CTA
+                bar_wait(ok ? &empty[i % stages] : &full[i % stages], i / stages & 1);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            int it = 0;
+            for (; it < count; ++it) {
+                const int s = it % stages, h = it % kAcc;
+                if (!(ok = bar_wait(&full[s], it / stages & 1) && bar_wait(&acc_empty[h], (it / kAcc & 1) ^ 1))) break;
+                tc_after();
+                const uint64_t da = tc_desc(smem_u32(ops + s * kStage)), db = tc_desc(smem_u32(ops + s * kStage + 128 * 128));
+#pragma unroll
+                for (int t = 0; t < 4; ++t) tc_mma(tmem + h * NT, da + 2 * t, db + 2 * t, tc_idesc<128, NT>(), t > 0);
+                tc_commit(&empty[s]);
+                tc_commit(&acc_full[h]);
+            }
+            if (!ok && it > 0) bar_wait(&acc_full[(it - 1) % kAcc], (it - 1) / kAcc & 1);  // products in flight
+        }
+        __syncwarp();
+    } else {
+        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16);
+        const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock, sc = ROWS ? n0 + wrow : tile;
+        constexpr int kSa = (NT + 31) / 32;
+        float nb = 0.f, na[kSa];
+        auto load_scales = [&](int b) {
+            nb = sc < per ? g.sb[size_t(b) * per + sc] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kSa; ++i) na[i] = 32 * i + lane < g.m ? g.sa[size_t(b) * g.m + 32 * i + lane] : 0.f;
+        };
+        if (count > 0) load_scales(r.first);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[j] = 0.f;
+        for (int it = 0; it < count; ++it) {
+            const int h = it % kAcc;
+            const float f = nb;
+            float* sa = sbuf[warp - 2][it & 1];
+#pragma unroll
+            for (int i = 0; i < kSa; ++i)
+                if (32 * i + lane < NT) sa[32 * i + lane] = na[i];
+            __syncwarp();
+            if (it + 1 < count) load_scales(r.first + it + 1);
+            ok = __all_sync(0xffffffffu, bar_wait(&acc_full[h], it / kAcc & 1));
+            if (!ok) break;
+            tc_after();
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                uint32_t v[16];
+                tc_ld16(lanes + h * NT + 16 * c, v);
+                tc_wait(v);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[j]) * sa[16 * c + j], f, acc[16 * c + j]);
+            }
+            tc_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&acc_empty[h]);
+        }
+    }
+    const int n = n0 + wrow;
+    auto store = [&](int j, float v) {
+        if (g.relu && v < 0.f) v = 0.f;
+        static_cast<T*>(g.out)[size_t(j) * g.os + n] = from_f<T>(v);
+    };
+    // every role is done with the operands' memory after this barrier: the sums take their place
+    const bool all = __syncthreads_and(ok);
+    if (g.splits == 1) {
+        if (warp >= 2 && all && n < g.n) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                if (j < g.m) store(j, acc[j]);
+        }
+    } else {
+        float* red = reinterpret_cast<float*>(ops);
+        if (warp >= 2) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) red[j * 128 + wrow] = all ? acc[j] : __int_as_float(0x7fc00000);
+        }
+        cluster_sync();
+        if (warp >= 2 && n < g.n) {
+            for (int j = rank; j < g.m; j += g.splits) {
+                const uint32_t at = smem_u32(red + j * 128 + wrow);
+                float v = 0.f;
+                for (int s = 0; s < g.splits; ++s) {
+                    uint32_t there;
+                    float x;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(s));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
+                    v += x;
+                }
+                store(j, v);
+            }
+        }
+        cluster_sync();  // no CTA's memory goes while another reads it
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(128) : "memory");
+}
+
 // out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row reads
 // 128 consecutive floats a warp group, and the values leave through shared memory along out's rows.
 template <typename T>
@@ -292,17 +447,25 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
 
 // ---------------------------------------------------------------- host side
 struct Plan {
+    int rows;      // 16, 32 or 64: few rows, that many columns of products; 0: the tile kernel
     int bn, splits, tiles_n, tiles;
-    size_t workspace() const { return splits > 1 ? size_t(splits) * tiles * bn * 128 * sizeof(float) : 0; }
+    size_t workspace() const { return rows == 0 && splits > 1 ? size_t(splits) * tiles * bn * 128 * sizeof(float) : 0; }
 };
 
 Plan plan_matmul(int m, int n, int k) {
-    Plan p;
+    Plan p{};
+    const int blocks = ceil_div(k, kBlock);
+    if (m <= 64) {
+        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+        p.bn = 128;
+        p.tiles_n = p.tiles = ceil_div(n, 128);
+        for (p.splits = 1; p.splits < 8 && p.tiles * p.splits * 2 <= 2 * kSms && blocks >= p.splits * 4;) p.splits *= 2;
+        return p;
+    }
     p.bn = n > 128 ? 256 : 128;
     p.tiles_n = ceil_div(n, p.bn);
     const long long tiles = (long long)ceil_div(m, 128) * p.tiles_n;
     p.tiles = int(std::min<long long>(tiles, 0x7fffffff));
-    const int blocks = ceil_div(k, kBlock);
     p.splits = tiles >= kSms ? 1 : std::max(1, std::min(kSms / p.tiles, blocks / 8));
     return p;
 }
@@ -337,6 +500,29 @@ cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Matmul
     const cudaError_t e = cudaFuncSetAttribute(k_matmul_tile<T, BN, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return pdl_launch(k_matmul_tile<T, BN, ROWS>, std::min(kSms, g.tiles * g.splits), 320, smem, s, a, b, g);
+}
+
+template <typename T, int NT, bool ROWS>
+cudaError_t launch_rows(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
+    using Smem = RowsSmem<NT>;
+    const int per = ceil_div(ceil_div(g.k, kBlock), g.splits), stages = std::min(per, Smem::kMaxStages);
+    const int smem = std::max(stages * Smem::kStage, NT * 128 * 4) + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_matmul_rows<T, NT, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = unsigned(g.tiles) * g.splits;
+    cfg.blockDim = 192;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = g.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_matmul_rows<T, NT, ROWS>, a, b, g, stages);
 }
 
 }  // namespace
@@ -376,19 +562,24 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
         return RS_ERR_INVALID_ARG;
     if ((long long)ceil_div(m, 128) * ceil_div(n, 128) > 0x3fffffff) return RS_ERR_INVALID_ARG;
     const Plan p = plan_matmul(m, n, k);
-    if (p.splits > 1 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
-    if (p.splits > 1 && workspace_bytes < p.workspace()) return RS_ERR_WORKSPACE;
+    const size_t need = p.workspace();
+    if (need > 0 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return RS_ERR_WORKSPACE;
     CUtensorMap ma, mb;
-    if (!encode(&ma, d_a, a_stride, m, k, 128) || !encode(&mb, d_b, b_stride, n, k, p.bn)) return RS_ERR_CUDA;
+    if (!encode(&ma, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, d_b, b_stride, n, k, p.bn)) return RS_ERR_CUDA;
     MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z),
                  p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
+        const bool per_row = b_scale_rows == 1;
+        if (p.rows == 16) return per_row ? launch_rows<T, 16, true>(ma, mb, g, s) : launch_rows<T, 16, false>(ma, mb, g, s);
+        if (p.rows == 32) return per_row ? launch_rows<T, 32, true>(ma, mb, g, s) : launch_rows<T, 32, false>(ma, mb, g, s);
+        if (p.rows == 64) return per_row ? launch_rows<T, 64, true>(ma, mb, g, s) : launch_rows<T, 64, false>(ma, mb, g, s);
         if (p.bn == 256)
             return b_scale_rows == 1 ? launch_tile<T, 256, true>(ma, mb, g, s) : launch_tile<T, 256, false>(ma, mb, g, s);
         return b_scale_rows == 1 ? launch_tile<T, 128, true>(ma, mb, g, s) : launch_tile<T, 128, false>(ma, mb, g, s);
     });
-    if (e == cudaSuccess && p.splits > 1)
+    if (e == cudaSuccess && need > 0)
         e = with_dtype(out_dtype, [&](auto v) {
             return pdl_launch(k_matmul_join<decltype(v)>, unsigned(p.tiles) * (p.bn / 8), 256, 0, s, g, p.bn);
         });
