@@ -41,6 +41,21 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint64_t* b) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
 }
+// Arrival at a barrier of another CTA of the cluster (address from cluster_addr).  It says that tensor memory has been
+// read, nothing that this thread has stored: a release at the cluster's scope would wait for all of the thread's memory
+// operations each time (measured: half the product's speed).
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The address of `p`'s counterpart in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     const uint32_t addr = smem_u32(b);
     for (uint32_t i = 0; i < kWaitPolls; ++i) {
@@ -58,6 +73,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
 __device__ __forceinline__ void tma_load(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+
+// The same by one CTA of a pair, into its own memory, counted at a barrier of either (address from cluster_addr).
+__device__ __forceinline__ void tma_load_pair(const CUtensorMap* map, void* dst, uint32_t bar, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
 // Matrix descriptor of a K-major operand in 128-byte swizzled rows (PTX ISA "Matrix Descriptors"): address >> 4, groups of
@@ -78,6 +99,15 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// The same of a pair of CTAs: operands at the same places of both, the sums' upper 128 rows in the second's tensor memory.
+__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+                 ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {  // arrives at both CTAs' barriers
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -94,15 +124,51 @@ __device__ __forceinline__ void tc_wait(uint32_t (&r)[16]) {
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));  // no use of them moves above the wait
 }
 
+// Two floats in one register pair: a product or a multiply-add of both is one instruction (f32x2).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pack2(uint32_t a, uint32_t b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------- the tile kernel
-// A CTA takes 128 x BN tiles of out (and one of `splits` stretches of the blocks), persistently.  Warp 0 loads, warp 1
-// issues the products, warps 2 to 9 add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on, and one half of the
-// columns.  Tensor memory holds two accumulators of BN columns: the products of block b + 1 run while block b is read.
+// A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA holds
+// 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is fetched and
+// stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warps 4 to 19 of both add
+// the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a quarter of the columns.  Tensor memory holds
+// kAcc accumulators of BN columns: the products of the next blocks run while a block is read.
+constexpr int kTileThreads = 640;
+constexpr int kPairs = kSms / 2;
+// Registers a thread before and after the split between warps 0-3 and the rest: 128 x 32 + 512 x 112 = 640 x 96.
+constexpr int kRegsLaunch = 96, kRegsFew = 32, kRegsMany = 112;
+static_assert(128 * kRegsFew + 512 * kRegsMany <= kTileThreads * kRegsLaunch, "the launch's registers");
+
 template <int BN>
 struct TileSmem {
-    static constexpr int kStages = BN == 256 ? 4 : 6;  // 192 KB of operands either way
+    static constexpr int kStages = BN == 256 ? 4 : 6, kAcc = 512 / BN;
     uint8_t a[kStages][128 * 128];
-    uint8_t b[kStages][BN * 128];
+    uint8_t b[kStages][BN / 2 * 128];
+    uint8_t stage[16][32 * 128];     // a warp's way out: 32 rows of 128 bytes
 };
 
 struct Range { int first, last; };
@@ -110,90 +176,115 @@ __device__ __forceinline__ Range split_blocks(int blocks, int splits, int s) {
     return {int((long long)blocks * s / splits), int((long long)blocks * (s + 1) / splits)};
 }
 
+// A warp's 32 rows x WORDS 16-byte words of results (thread = row) to out, through shared memory so that
+// the stores run along the rows.  The words of row r are placed at word ^ (r mod 8): no two of eight neighbours share a bank.
+template <typename T, int WORDS>
+__device__ __forceinline__ void store_rows(uint8_t* st, const uint4 (&w)[8], T* o, size_t os, long long rows, int cols,
+                                           bool vec, int lane) {
+    constexpr int kPer = 16 / sizeof(T);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = w[i];
+    __syncwarp();
+    if (vec && cols >= WORDS * kPer) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            const int r = i * (32 / WORDS) + lane / WORDS, c = lane % WORDS;
+            if (r < rows)
+                *reinterpret_cast<uint4*>(o + r * os + c * kPer) =
+                    *reinterpret_cast<const uint4*>(st + r * 128 + ((c ^ (r & 7)) << 4));
+        }
+    } else {
+        for (int r = 0; r < 32 && r < rows; ++r)
+            for (int c = lane; c < WORDS * kPer && c < cols; c += 32)
+                o[r * os + c] = *reinterpret_cast<const T*>(st + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(T));
+    }
+}
+
 template <typename T, int BN, bool ROWS>
-__global__ void __launch_bounds__(320, 1) k_matmul_tile(const __grid_constant__ CUtensorMap map_a,
-                                                        const __grid_constant__ CUtensorMap map_b, MatmulArgs g) {
+__global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_constant__ CUtensorMap map_a,
+                                                                 const __grid_constant__ CUtensorMap map_b, MatmulArgs g) {
     RS_PDL_ENTER();
     using Smem = TileSmem<BN>;
-    constexpr int kStages = Smem::kStages, kCols = BN / 2;
+    constexpr int kStages = Smem::kStages, kAcc = Smem::kAcc, kCols = BN / 4;
     extern __shared__ uint8_t raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2];
+    __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float sbuf[ROWS ? 8 : 1][2][ROWS ? kCols : 4];  // ROWS: a warp's scales of b
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) float sbuf[ROWS ? 16 : 1][2][ROWS ? kCols : 4];  // ROWS: a warp's scales of b
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
-        for (int i = 0; i < 2; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 8);
+        for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 32);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(2 * BN)
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
                      : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_before();
     __syncthreads();
+    cluster_sync();  // the other CTA's barriers are set up before anything arrives there
     tc_after();
     const uint32_t tmem = tmem_slot;
     const int blocks = (g.k + kBlock - 1) / kBlock;
-    const int units = g.tiles * g.splits;
-    if (warp == 0) {
-        if (lane == 0) {
+    const int units = g.tiles * g.splits, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+        if (warp == 0 && lane == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const int tile = u % g.tiles, y = tile / g.tiles_n * 128, x = tile % g.tiles_n * BN;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const int tile = u % g.tiles, y = (tile / g.tiles_n * 2 + rank) * 128,
+                          x = tile % g.tiles_n * BN + rank * (BN / 2);
                 const Range r = split_blocks(blocks, g.splits, u / g.tiles);
                 for (int b = r.first; b < r.last; ++b, ++it) {
                     const uint32_t s = it % kStages;
                     if (!(ok = bar_wait(&empty[s], (it / kStages & 1) ^ 1))) break;
-                    bar_expect(&full[s], (128 + BN) * 128);
-                    tma_load(&map_a, sm.a[s], &full[s], b * kBlock, y);
-                    tma_load(&map_b, sm.b[s], &full[s], b * kBlock, x);
+                    // the first CTA's barrier counts both CTAs' copies
+                    if (rank == 0) bar_expect(&full[s], 2 * (128 + BN / 2) * 128);
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    tma_load_pair(&map_a, sm.a[s], bar, b * kBlock, y);
+                    tma_load_pair(&map_b, sm.b[s], bar, b * kBlock, x);
                 }
             }
-            // no copy and no arrival may outlast the CTA: every stage that was filled is waited for
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
-                if (!ok) bar_wait(&full[i % kStages], i / kStages & 1);
-                else bar_wait(&empty[i % kStages], i / kStages & 1);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
+            // no copy and no arrival may outlast the CTA: a stage's products follow its copies
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) bar_wait(&empty[i % kStages], i / kStages & 1);
+        } else if (warp == 1 && lane == 0 && rank == 0) {
             uint32_t it = 0;
             bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            for (int u = pair; u < units && ok; u += pairs) {
                 const Range r = split_blocks(blocks, g.splits, u / g.tiles);
                 for (int b = r.first; b < r.last; ++b, ++it) {
-                    const uint32_t s = it % kStages, h = it & 1;
-                    if (!(ok = bar_wait(&full[s], it / kStages & 1) && bar_wait(&acc_empty[h], (it >> 1 & 1) ^ 1))) break;
+                    const uint32_t s = it % kStages, h = it % kAcc;
+                    if (!(ok = bar_wait(&full[s], it / kStages & 1) && bar_wait(&acc_empty[h], (it / kAcc & 1) ^ 1))) break;
                     tc_after();
                     const uint64_t da = tc_desc(smem_u32(sm.a[s])), db = tc_desc(smem_u32(sm.b[s]));
 #pragma unroll
                     for (int t = 0; t < 4; ++t)  // 32 bytes of K an instruction
-                        tc_mma(tmem + h * BN, da + 2 * t, db + 2 * t, tc_idesc<128, BN>(), t > 0);
-                    tc_commit(&empty[s]);
-                    tc_commit(&acc_full[h]);
+                        tc_mma_pair(tmem + h * BN, da + 2 * t, db + 2 * t, tc_idesc<256, BN>(), t > 0);
+                    tc_commit_pair(&empty[s]);
+                    tc_commit_pair(&acc_full[h]);
                 }
             }
-            if (!ok && it > 0) bar_wait(&acc_full[(it - 1) & 1], (it - 1) >> 1 & 1);  // products in flight
+            if (!ok && it > 0) bar_wait(&acc_full[(it - 1) % kAcc], (it - 1) / kAcc & 1);  // products in flight
         }
         __syncwarp();
     } else {
-        const int half = (warp - 2) >> 2, wrow = (warp & 3) * 32 + lane;  // half of the columns, row of the tile
-        const uint32_t lanes = tmem + (uint32_t((warp & 3) * 32) << 16) + half * kCols;
-        const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;         // b's scales a block
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
+        const int w16 = warp - 4, quarter = w16 >> 2, wrow = (w16 & 3) * 32;   // columns and rows of the tile
+        const uint32_t lanes = tmem + (uint32_t(wrow) << 16) + quarter * kCols;
+        const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;             // b's scales a block
         uint32_t it = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const int tile = u % g.tiles, split = u / g.tiles;
-            const long long row = (long long)(tile / g.tiles_n) * 128 + wrow;
-            const int col = tile % g.tiles_n * BN + half * kCols;
-            const Range r = split_blocks(blocks, g.splits, split);
-            const bool in = row < g.m && col < g.n;
-            const float* sa = g.sa + row;
+        for (int u = pair; u < units; u += pairs) {
+            const int tile = u % g.tiles;
+            const long long row0 = (long long)(tile / g.tiles_n * 2 + rank) * 128 + wrow;
+            const int col = tile % g.tiles_n * BN + quarter * kCols;
+            const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+            const bool in = row0 + lane < g.m && col < g.n;
+            const float* sa = g.sa + row0 + lane;
             // b's scales of one block: a number for the warp, or one for each of its columns
             constexpr int kSb = ROWS ? kCols / 32 : 1;
             float na = 0.f, nb[kSb];
@@ -206,20 +297,21 @@ __global__ void __launch_bounds__(320, 1) k_matmul_tile(const __grid_constant__ 
                 }
             };
             if (r.first < r.last) load_scales(r.first);
-            float acc[kCols];
+            uint64_t acc[kCols / 2];
 #pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] = 0.f;
+            for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
             for (int b = r.first; b < r.last; ++b, ++it) {
-                const uint32_t h = it & 1;
+                const uint32_t h = it % kAcc;
                 const float f = ROWS ? na : na * nb[0];
-                float* sb = sbuf[ROWS ? warp - 2 : 0][h];
+                const uint64_t ff = pack2(f, f);
+                float* sb = sbuf[ROWS ? w16 : 0][it & 1];
                 if (ROWS) {
 #pragma unroll
                     for (int i = 0; i < kSb; ++i) sb[32 * i + lane] = nb[i];
                     __syncwarp();
                 }
                 if (b + 1 < r.last) load_scales(b + 1);  // a block ahead
-                ok = __all_sync(0xffffffffu, bar_wait(&acc_full[h], it >> 1 & 1));
+                ok = __all_sync(0xffffffffu, bar_wait(&acc_full[h], it / kAcc & 1));
                 if (!ok) break;
                 tc_after();
                 uint32_t v[2][16];
@@ -229,53 +321,63 @@ __global__ void __launch_bounds__(320, 1) k_matmul_tile(const __grid_constant__ 
                     tc_wait(v[c & 1]);
                     if (c + 1 < kCols / 16) tc_ld16(lanes + h * BN + 16 * (c + 1), v[(c + 1) & 1]);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float p = __uint_as_float(v[c & 1][j]);
-                        acc[16 * c + j] = fmaf(ROWS ? p * sb[16 * c + j] : p, f, acc[16 * c + j]);
+                    for (int j = 0; j < 16; j += 2) {
+                        uint64_t p = pack2(v[c & 1][j], v[c & 1][j + 1]);
+                        if (ROWS) {
+                            const float2 s2 = *reinterpret_cast<const float2*>(sb + 16 * c + j);
+                            p = mul2(p, pack2(s2.x, s2.y));
+                        }
+                        acc[8 * c + j / 2] = fma2(p, ff, acc[8 * c + j / 2]);
                     }
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(&acc_empty[h]);
+                if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[h], 0));
             }
             if (!ok) break;
             if (g.splits > 1) {
-                float* o = g.part + (size_t(u) * BN + half * kCols) * 128 + wrow;
+                float* o = g.part + ((size_t(u) * 2 + rank) * BN + quarter * kCols) * 128 + wrow + lane;
 #pragma unroll
-                for (int j = 0; j < kCols; ++j) o[size_t(j) * 128] = acc[j];
-            } else if (row < g.m) {
-                T* o = static_cast<T*>(g.out) + row * g.os + col;
+                for (int j = 0; j < kCols / 2; ++j) {
+                    const float2 x = unpack2(acc[j]);
+                    o[size_t(2 * j) * 128] = x.x;
+                    o[size_t(2 * j + 1) * 128] = x.y;
+                }
+            } else if (col < g.n) {
+                constexpr int kOnce = 128 / sizeof(T) < kCols ? 128 / sizeof(T) : kCols;  // columns a pass: 128 bytes at most
 #pragma unroll
-                for (int j = 0; j < kCols; j += 8) {
-                    float w[8];
+                for (int c = 0; c < kCols; c += kOnce) {
+                    uint4 w[8];
+                    T* wt = reinterpret_cast<T*>(w);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = g.relu && acc[j + i] < 0.f ? 0.f : acc[j + i];
-                    if (g.vec) store8<T, true>(o + j, g.n - col - j, w);
-                    else store8<T, false>(o + j, g.n - col - j, w);
+                    for (int j = 0; j < kOnce; j += 2) {
+                        const float2 x = unpack2(acc[(c + j) / 2]);
+                        wt[j] = from_f<T>(g.relu && x.x < 0.f ? 0.f : x.x);
+                        wt[j + 1] = from_f<T>(g.relu && x.y < 0.f ? 0.f : x.y);
+                    }
+                    store_rows<T, kOnce * sizeof(T) / 16>(sm.stage[w16], w, static_cast<T*>(g.out) + row0 * g.os + col + c, g.os,
+                                                          g.m - row0, g.n - col - c, g.vec, lane);
                 }
             }
         }
     }
     tc_before();
     __syncthreads();
+    cluster_sync();  // neither CTA's memory goes while the other's products or arrivals use it
     tc_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * BN) : "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // ---------------------------------------------------------------- few rows
-// With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
+// With at most 128 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
 // (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that every SM
 // reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its CTAs' sums
 // through distributed shared memory, rank by rank, each CTA finishing some of the columns.
 template <int NT>
 struct RowsSmem {
-    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = 128 / NT, kMaxStages = 8;
+    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = NT == 128 ? 2 : 128 / NT, kMaxStages = NT == 128 ? 6 : 8;
+    static constexpr int kTmem = kAcc * NT;  // columns
 };
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 
 template <typename T, int NT, bool ROWS>
 __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUtensorMap map_a,
@@ -295,7 +397,7 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(128)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(RowsSmem<NT>::kTmem)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -398,13 +500,10 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
         cluster_sync();
         if (warp >= 2 && n < g.n) {
             for (int j = rank; j < g.m; j += g.splits) {
-                const uint32_t at = smem_u32(red + j * 128 + wrow);
                 float v = 0.f;
                 for (int s = 0; s < g.splits; ++s) {
-                    uint32_t there;
                     float x;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(at), "r"(s));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr(red + j * 128 + wrow, s)) : "memory");
                     v += x;
                 }
                 store(j, v);
@@ -415,7 +514,7 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(128) : "memory");
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(RowsSmem<NT>::kTmem) : "memory");
 }
 
 // out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row reads
@@ -424,10 +523,10 @@ template <typename T>
 __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
     RS_PDL_ENTER();
     __shared__ float sm[8][129];
-    const int groups = bn / 8, tile = blockIdx.x / groups, c0 = blockIdx.x % groups * 8;
+    const int groups = bn / 8, half = blockIdx.x / groups, tile = half >> 1, c0 = blockIdx.x % groups * 8;
     const int row = threadIdx.x & 127, cc = (threadIdx.x >> 7) * 4;
-    const float* p = g.part + (size_t(tile) * bn + c0 + cc) * 128 + row;
-    const size_t step = size_t(g.tiles) * bn * 128;
+    const float* p = g.part + (size_t(half) * bn + c0 + cc) * 128 + row;
+    const size_t step = size_t(g.tiles) * 2 * bn * 128;
     float v[4] = {};
     for (int s = 0; s < g.splits; ++s, p += step)
 #pragma unroll
@@ -440,23 +539,23 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 32 + int(threadIdx.x >> 3);
-        const long long gr = (long long)(tile / g.tiles_n) * 128 + r;
+        const long long gr = (long long)(tile / g.tiles_n * 2 + (half & 1)) * 128 + r;
         if (gr < g.m && col < g.n) static_cast<T*>(g.out)[gr * g.os + col] = from_f<T>(sm[c][r]);
     }
 }
 
 // ---------------------------------------------------------------- host side
 struct Plan {
-    int rows;      // 16, 32 or 64: few rows, that many columns of products; 0: the tile kernel
+    int rows;      // 16, 32, 64 or 128: few rows, that many columns of products; 0: the tile kernel
     int bn, splits, tiles_n, tiles;
-    size_t workspace() const { return rows == 0 && splits > 1 ? size_t(splits) * tiles * bn * 128 * sizeof(float) : 0; }
+    size_t workspace() const { return rows == 0 && splits > 1 ? size_t(splits) * tiles * 2 * bn * 128 * sizeof(float) : 0; }
 };
 
 Plan plan_matmul(int m, int n, int k) {
     Plan p{};
     const int blocks = ceil_div(k, kBlock);
-    if (m <= 64) {
-        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
+    if (m <= 128) {
+        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
         p.bn = 128;
         p.tiles_n = p.tiles = ceil_div(n, 128);
         for (p.splits = 1; p.splits < 8 && p.tiles * p.splits * 2 <= 2 * kSms && blocks >= p.splits * 4;) p.splits *= 2;
@@ -464,9 +563,9 @@ Plan plan_matmul(int m, int n, int k) {
     }
     p.bn = n > 128 ? 256 : 128;
     p.tiles_n = ceil_div(n, p.bn);
-    const long long tiles = (long long)ceil_div(m, 128) * p.tiles_n;
+    const long long tiles = (long long)ceil_div(m, 256) * p.tiles_n;
     p.tiles = int(std::min<long long>(tiles, 0x7fffffff));
-    p.splits = tiles >= kSms ? 1 : std::max(1, std::min(kSms / p.tiles, blocks / 8));
+    p.splits = tiles >= kPairs ? 1 : std::max(1, std::min(kPairs / p.tiles, blocks / 8));
     return p;
 }
 
@@ -494,12 +593,38 @@ bool encode(CUtensorMap* map, const uint8_t* p, size_t stride, int rows, int col
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// With programmatic stream serialization, in clusters of `cluster` CTAs.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned grid, unsigned block, int smem, cudaStream_t s,
+                            Args&&... args) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 template <typename T, int BN, bool ROWS>
 cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
     constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
-    const cudaError_t e = cudaFuncSetAttribute(k_matmul_tile<T, BN, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    return pdl_launch(k_matmul_tile<T, BN, ROWS>, std::min(kSms, g.tiles * g.splits), 320, smem, s, a, b, g);
+    // the kernel's register split counts on what it is launched with
+    static const bool enough = [] {
+        cudaFuncAttributes f{};
+        return cudaFuncGetAttributes(&f, k_matmul_tile<T, BN, ROWS>) == cudaSuccess && f.numRegs >= kRegsLaunch;
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+    return launch_clusters(k_matmul_tile<T, BN, ROWS>, 2, 2u * std::min(kPairs, g.tiles * g.splits), kTileThreads, smem, s, a, b, g);
 }
 
 template <typename T, int NT, bool ROWS>
@@ -507,22 +632,7 @@ cudaError_t launch_rows(const CUtensorMap& a, const CUtensorMap& b, const Matmul
     using Smem = RowsSmem<NT>;
     const int per = ceil_div(ceil_div(g.k, kBlock), g.splits), stages = std::min(per, Smem::kMaxStages);
     const int smem = std::max(stages * Smem::kStage, NT * 128 * 4) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_matmul_rows<T, NT, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = unsigned(g.tiles) * g.splits;
-    cfg.blockDim = 192;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = g.splits;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_matmul_rows<T, NT, ROWS>, a, b, g, stages);
+    return launch_clusters(k_matmul_rows<T, NT, ROWS>, g.splits, unsigned(g.tiles) * g.splits, 192, smem, s, a, b, g, stages);
 }
 
 }  // namespace
@@ -566,7 +676,7 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     if (need > 0 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
     if (workspace_bytes < need) return RS_ERR_WORKSPACE;
     CUtensorMap ma, mb;
-    if (!encode(&ma, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, d_b, b_stride, n, k, p.bn)) return RS_ERR_CUDA;
+    if (!encode(&ma, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2)) return RS_ERR_CUDA;
     MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z),
                  p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
@@ -574,6 +684,7 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
         const bool per_row = b_scale_rows == 1;
         if (p.rows == 16) return per_row ? launch_rows<T, 16, true>(ma, mb, g, s) : launch_rows<T, 16, false>(ma, mb, g, s);
         if (p.rows == 32) return per_row ? launch_rows<T, 32, true>(ma, mb, g, s) : launch_rows<T, 32, false>(ma, mb, g, s);
+        if (p.rows == 128) return per_row ? launch_rows<T, 128, true>(ma, mb, g, s) : launch_rows<T, 128, false>(ma, mb, g, s);
         if (p.rows == 64) return per_row ? launch_rows<T, 64, true>(ma, mb, g, s) : launch_rows<T, 64, false>(ma, mb, g, s);
         if (p.bn == 256)
             return b_scale_rows == 1 ? launch_tile<T, 256, true>(ma, mb, g, s) : launch_tile<T, 256, false>(ma, mb, g, s);
@@ -581,7 +692,7 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     });
     if (e == cudaSuccess && need > 0)
         e = with_dtype(out_dtype, [&](auto v) {
-            return pdl_launch(k_matmul_join<decltype(v)>, unsigned(p.tiles) * (p.bn / 8), 256, 0, s, g, p.bn);
+            return pdl_launch(k_matmul_join<decltype(v)>, unsigned(p.tiles) * 2 * (p.bn / 8), 256, 0, s, g, p.bn);
         });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
