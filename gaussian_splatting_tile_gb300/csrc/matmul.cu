@@ -56,8 +56,14 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
-    const uint32_t addr = smem_u32(b);
+__device__ __forceinline__ bool bar_test(uint32_t addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok) : "r"(addr), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t addr, uint32_t parity) {
+    if (bar_test(addr, parity)) return true;
     for (uint32_t i = 0; i < kWaitPolls; ++i) {
         uint32_t ok;
         asm volatile(
@@ -68,6 +74,8 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) {
     atomicOr(&g_matmul_error, 1u);
     return false;
 }
+
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) { return bar_wait(smem_u32(b), parity); }
 
 // A tile's corner (x: element along the row, y: row); x is a multiple of 128 bytes.
 __device__ __forceinline__ void tma_load(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y) {
@@ -108,6 +116,13 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {  // arrives at b
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
+// True in one lane of a converged warp.  The loops that feed the tensor cores run in all lanes and let one act: what they
+// compute is then the same in every lane by construction, as those instructions' operands have to be.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -122,6 +137,10 @@ __device__ __forceinline__ void tc_wait(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) asm volatile("" : "+r"(r[i]));  // no use of them moves above the wait
+}
+
+__device__ __forceinline__ void copy4(float* dst, const float* src) {  // asynchronously
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // Two floats in one register pair: a product or a multiply-add of both is one instruction (f32x2).
@@ -155,20 +174,21 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA holds
 // 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is fetched and
 // stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warps 4 to 19 of both add
-// the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a quarter of the columns.  Tensor memory holds
+// the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a half of the columns.  Tensor memory holds
 // kAcc accumulators of BN columns: the products of the next blocks run while a block is read.
-constexpr int kTileThreads = 640;
+constexpr int kSumWarps = 8;
+constexpr int kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPairs = kSms / 2;
-// Registers a thread before and after the split between warps 0-3 and the rest: 128 x 32 + 512 x 112 = 640 x 96.
-constexpr int kRegsLaunch = 96, kRegsFew = 32, kRegsMany = 112;
-static_assert(128 * kRegsFew + 512 * kRegsMany <= kTileThreads * kRegsLaunch, "the launch's registers");
+// Registers a thread before and after the split between warps 0-3 and the rest: 128 x 40 + 256 x 232 = 384 x 168.
+constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
+static_assert(128 * kRegsFew + 32 * kSumWarps * kRegsMany <= kTileThreads * kRegsLaunch, "the launch's registers");
 
 template <int BN>
 struct TileSmem {
     static constexpr int kStages = BN == 256 ? 4 : 6, kAcc = 512 / BN;
     uint8_t a[kStages][128 * 128];
     uint8_t b[kStages][BN / 2 * 128];
-    uint8_t stage[16][32 * 128];     // a warp's way out: 32 rows of 128 bytes
+    uint8_t stage[kSumWarps][2][32 * 128];  // a warp's way out: twice 32 rows of 128 bytes
 };
 
 struct Range { int first, last; };
@@ -176,46 +196,63 @@ __device__ __forceinline__ Range split_blocks(int blocks, int splits, int s) {
     return {int((long long)blocks * s / splits), int((long long)blocks * (s + 1) / splits)};
 }
 
-// A warp's 32 rows x WORDS 16-byte words of results (thread = row) to out, through shared memory so that
-// the stores run along the rows.  The words of row r are placed at word ^ (r mod 8): no two of eight neighbours share a bank.
-template <typename T, int WORDS>
-__device__ __forceinline__ void store_rows(uint8_t* st, const uint4 (&w)[8], T* o, size_t os, long long rows, int cols,
-                                           bool vec, int lane) {
+// max(x, 0), a NaN kept.
+__device__ __forceinline__ float relu(float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pair_of(float2 x);
+template <>
+__device__ __forceinline__ uint32_t pair_of<__half>(float2 x) {
+    const __half2 h = __float22half2_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pair_of<__nv_bfloat16>(float2 x) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(x);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A warp's 32 rows x 128 bytes of results (thread = row, eight 16-byte words) in shared memory, the words of row r at
+// word ^ (r mod 8): the 128-byte swizzle of the tensor map that takes them out, and no two of eight neighbours share a bank.
+__device__ __forceinline__ void stage_rows(uint8_t* st, const uint4 (&w)[8], int lane) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = w[i];
+}
+// From there to rows of out that TMA cannot write (not on 16-byte boundaries), one value a lane.
+template <typename T>
+__device__ __forceinline__ void copy_rows(const uint8_t* st, T* o, size_t os, long long rows, int cols, int lane) {
     constexpr int kPer = 16 / sizeof(T);
-    __syncwarp();
+    for (int r = 0; r < 32 && r < rows; ++r)
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = w[i];
-    __syncwarp();
-    if (vec && cols >= WORDS * kPer) {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            const int r = i * (32 / WORDS) + lane / WORDS, c = lane % WORDS;
-            if (r < rows)
-                *reinterpret_cast<uint4*>(o + r * os + c * kPer) =
-                    *reinterpret_cast<const uint4*>(st + r * 128 + ((c ^ (r & 7)) << 4));
-        }
-    } else {
-        for (int r = 0; r < 32 && r < rows; ++r)
-            for (int c = lane; c < WORDS * kPer && c < cols; c += 32)
+        for (int c = lane; c < 8 * kPer; c += 32)
+            if (c < cols)
                 o[r * os + c] = *reinterpret_cast<const T*>(st + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(T));
-    }
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
 template <typename T, int BN, bool ROWS>
 __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_constant__ CUtensorMap map_a,
-                                                                 const __grid_constant__ CUtensorMap map_b, MatmulArgs g) {
+                                                                 const __grid_constant__ CUtensorMap map_b,
+                                                                 const __grid_constant__ CUtensorMap map_out, MatmulArgs g) {
     RS_PDL_ENTER();
     using Smem = TileSmem<BN>;
-    constexpr int kStages = Smem::kStages, kAcc = Smem::kAcc, kCols = BN / 4;
+    constexpr int kStages = Smem::kStages, kAcc = Smem::kAcc, kCols = BN / (kSumWarps / 4);
     extern __shared__ uint8_t raw[];
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
     __shared__ uint32_t tmem_slot;
-    __shared__ __align__(16) float sbuf[ROWS ? 16 : 1][2][ROWS ? kCols : 4];  // ROWS: a warp's scales of b
+    // A warp's scales of four blocks: a's, one a row, then b's, one a column (ROWS) or the same one for every lane.
+    __shared__ __align__(16) float scales[kSumWarps][4][32 + (ROWS ? kCols : 32)];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
-        for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 32);
+        for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 2 * kSumWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -232,40 +269,50 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
     const int units = g.tiles * g.splits, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
-        if (warp == 0 && lane == 0) {
-            uint32_t it = 0;
+        if (warp == 0) {
+            const uint32_t bar0 = cluster_addr(full, 0);  // the first CTA's barriers count both CTAs' copies
+            uint32_t s = 0, phase = 1, it = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
                 const int tile = u % g.tiles, y = (tile / g.tiles_n * 2 + rank) * 128,
                           x = tile % g.tiles_n * BN + rank * (BN / 2);
                 const Range r = split_blocks(blocks, g.splits, u / g.tiles);
                 for (int b = r.first; b < r.last; ++b, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!(ok = bar_wait(&empty[s], (it / kStages & 1) ^ 1))) break;
-                    // the first CTA's barrier counts both CTAs' copies
-                    if (rank == 0) bar_expect(&full[s], 2 * (128 + BN / 2) * 128);
-                    const uint32_t bar = cluster_addr(&full[s], 0);
-                    tma_load_pair(&map_a, sm.a[s], bar, b * kBlock, y);
-                    tma_load_pair(&map_b, sm.b[s], bar, b * kBlock, x);
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], phase)))) break;
+                    if (elect_one()) {
+                        if (rank == 0) bar_expect(&full[s], 2 * (128 + BN / 2) * 128);
+                        tma_load_pair(&map_a, sm.a[s], bar0 + s * 8, b * kBlock, y);
+                        tma_load_pair(&map_b, sm.b[s], bar0 + s * 8, b * kBlock, x);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) s = 0, phase ^= 1;
                 }
             }
             // no copy and no arrival may outlast the CTA: a stage's products follow its copies
             for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) bar_wait(&empty[i % kStages], i / kStages & 1);
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            uint32_t it = 0;
-            bool ok = true;
+        } else if (warp == 1 && rank == 0) {
+            const uint64_t da0 = tc_desc(smem_u32(sm.a[0])), db0 = tc_desc(smem_u32(sm.b[0]));
+            uint32_t s = 0, phase = 0, h = 0, acc_phase = 1, it = 0;
+            bool ok = true, ready = false;
             for (int u = pair; u < units && ok; u += pairs) {
                 const Range r = split_blocks(blocks, g.splits, u / g.tiles);
                 for (int b = r.first; b < r.last; ++b, ++it) {
-                    const uint32_t s = it % kStages, h = it % kAcc;
-                    if (!(ok = bar_wait(&full[s], it / kStages & 1) && bar_wait(&acc_empty[h], (it / kAcc & 1) ^ 1))) break;
+                    ok = (ready || bar_wait(&full[s], phase)) && bar_wait(&acc_empty[h], acc_phase);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
                     tc_after();
-                    const uint64_t da = tc_desc(smem_u32(sm.a[s])), db = tc_desc(smem_u32(sm.b[s]));
+                    if (elect_one()) {
+                        const uint64_t da = da0 + s * (sizeof(sm.a[0]) >> 4), db = db0 + s * (sizeof(sm.b[0]) >> 4);
+                        const uint32_t d = tmem + h * BN;
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)  // 32 bytes of K an instruction
-                        tc_mma_pair(tmem + h * BN, da + 2 * t, db + 2 * t, tc_idesc<256, BN>(), t > 0);
-                    tc_commit_pair(&empty[s]);
-                    tc_commit_pair(&acc_full[h]);
+                        for (int t = 0; t < 4; ++t)  // 32 bytes of K an instruction
+                            tc_mma_pair(d, da + 2 * t, db + 2 * t, tc_idesc<256, BN>(), t > 0);
+                        tc_commit_pair(&acc_full[h]);
+                        tc_commit_pair(&empty[s]);
+                    }
+                    __syncwarp();
+                    if (++s == kStages) s = 0, phase ^= 1;
+                    if (++h == kAcc) h = 0, acc_phase ^= 1;
+                    ready = __all_sync(0xffffffffu, bar_test(smem_u32(&full[s]), phase));  // while the products run
                 }
             }
             if (!ok && it > 0) bar_wait(&acc_full[(it - 1) % kAcc], (it - 1) / kAcc & 1);  // products in flight
@@ -273,70 +320,81 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
-        const int w16 = warp - 4, quarter = w16 >> 2, wrow = (w16 & 3) * 32;   // columns and rows of the tile
-        const uint32_t lanes = tmem + (uint32_t(wrow) << 16) + quarter * kCols;
+        const int w8 = warp - 4, half = w8 >> 2, wrow = (w8 & 3) * 32;   // columns and rows of the tile
+        const uint32_t lanes = tmem + (uint32_t(wrow) << 16) + half * kCols;
         const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;             // b's scales a block
-        uint32_t it = 0;
+        const uint32_t full0 = smem_u32(acc_full), empty0 = cluster_addr(acc_empty, 0);
+        uint32_t h = 0, phase = 0;  // the accumulator to read next
+        int passes = 0;             // of results through the two buffers
         bool ok = true;
         for (int u = pair; u < units; u += pairs) {
             const int tile = u % g.tiles;
             const long long row0 = (long long)(tile / g.tiles_n * 2 + rank) * 128 + wrow;
-            const int col = tile % g.tiles_n * BN + quarter * kCols;
+            const int col = tile % g.tiles_n * BN + half * kCols;
             const Range r = split_blocks(blocks, g.splits, u / g.tiles);
-            const bool in = row0 + lane < g.m && col < g.n;
-            const float* sa = g.sa + row0 + lane;
-            // b's scales of one block: a number for the warp, or one for each of its columns
-            constexpr int kSb = ROWS ? kCols / 32 : 1;
-            float na = 0.f, nb[kSb];
-            auto load_scales = [&](int b) {
-                na = in ? sa[size_t(b) * g.m] : 0.f;
+            // The scales are copied to shared memory three blocks ahead (a load from L2 takes longer than a block).  Rows and
+            // columns outside the matrices take the last one's: what comes of them is not stored.
+            const int count = r.last - r.first;
+            const float* pa = g.sa + size_t(r.first) * g.m + min(row0 + lane, (long long)g.m - 1);
+            const float* pb = g.sb + size_t(r.first) * per;
+            float (*sc)[32 + (ROWS ? kCols : 32)] = scales[w8];
+            auto copy_scales = [&](int b) {  // of the stretch's block b, if there is one
+                if (b < count) {
+                    copy4(&sc[b & 3][lane], pa + size_t(b) * g.m);
+                    if (ROWS) {
 #pragma unroll
-                for (int i = 0; i < kSb; ++i) {
-                    const int c = ROWS ? col + 32 * i + lane : col / kBlock;
-                    nb[i] = c < per ? g.sb[size_t(b) * per + c] : 0.f;
+                        for (int i = 0; i < kCols; i += 32)
+                            copy4(&sc[b & 3][32 + i + lane], pb + size_t(b) * per + min(col + i + lane, per - 1));
+                    } else {
+                        copy4(&sc[b & 3][32 + lane], pb + size_t(b) * per + min(col / kBlock, per - 1));
+                    }
                 }
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
-            if (r.first < r.last) load_scales(r.first);
+            __syncwarp();  // every lane is done with the last tile's scales
+#pragma unroll
+            for (int i = 0; i < 3; ++i) copy_scales(i);
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-            for (int b = r.first; b < r.last; ++b, ++it) {
-                const uint32_t h = it % kAcc;
-                const float f = ROWS ? na : na * nb[0];
+            for (int b = 0; b < count; ++b) {
+                asm volatile("cp.async.wait_group 2;" ::: "memory");
+                __syncwarp();  // all lanes' copies; and every lane is done with block b - 1, whose place block b + 3 takes
+                const float f = ROWS ? sc[b & 3][lane] : sc[b & 3][lane] * sc[b & 3][32 + lane];
                 const uint64_t ff = pack2(f, f);
-                float* sb = sbuf[ROWS ? w16 : 0][it & 1];
-                if (ROWS) {
-#pragma unroll
-                    for (int i = 0; i < kSb; ++i) sb[32 * i + lane] = nb[i];
-                    __syncwarp();
-                }
-                if (b + 1 < r.last) load_scales(b + 1);  // a block ahead
-                ok = __all_sync(0xffffffffu, bar_wait(&acc_full[h], it / kAcc & 1));
-                if (!ok) break;
+                copy_scales(b + 3);
+                // a wait that gave up ends the waiting, not the loop: what is added from then on is not stored
+                ok = ok && __all_sync(0xffffffffu, bar_wait(full0 + h * 8, phase));
                 tc_after();
                 uint32_t v[2][16];
                 tc_ld16(lanes + h * BN, v[0]);
 #pragma unroll
                 for (int c = 0; c < kCols / 16; ++c) {
                     tc_wait(v[c & 1]);
-                    if (c + 1 < kCols / 16) tc_ld16(lanes + h * BN + 16 * (c + 1), v[(c + 1) & 1]);
+                    if (c + 1 < kCols / 16) {
+                        tc_ld16(lanes + h * BN + 16 * (c + 1), v[(c + 1) & 1]);
+                    } else {  // all of it has been read
+                        tc_before();
+                        __syncwarp();
+                        if (lane == 0) bar_arrive_cluster(empty0 + h * 8);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        uint64_t p = pack2(v[c & 1][j], v[c & 1][j + 1]);
+                    for (int j = 0; j < 16; j += 4) {
+                        uint64_t p = pack2(v[c & 1][j], v[c & 1][j + 1]), q = pack2(v[c & 1][j + 2], v[c & 1][j + 3]);
                         if (ROWS) {
-                            const float2 s2 = *reinterpret_cast<const float2*>(sb + 16 * c + j);
-                            p = mul2(p, pack2(s2.x, s2.y));
+                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&sc[b & 3][32 + 16 * c + j]);
+                            p = mul2(p, s4.x);
+                            q = mul2(q, s4.y);
                         }
                         acc[8 * c + j / 2] = fma2(p, ff, acc[8 * c + j / 2]);
+                        acc[8 * c + j / 2 + 1] = fma2(q, ff, acc[8 * c + j / 2 + 1]);
                     }
                 }
-                tc_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive_cluster(cluster_addr(&acc_empty[h], 0));
+                if (++h == kAcc) h = 0, phase ^= 1;
             }
             if (!ok) break;
             if (g.splits > 1) {
-                float* o = g.part + ((size_t(u) * 2 + rank) * BN + quarter * kCols) * 128 + wrow + lane;
+                float* o = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + wrow + lane;
 #pragma unroll
                 for (int j = 0; j < kCols / 2; ++j) {
                     const float2 x = unpack2(acc[j]);
@@ -344,22 +402,42 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                     o[size_t(2 * j + 1) * 128] = x.y;
                 }
             } else if (col < g.n) {
-                constexpr int kOnce = 128 / sizeof(T) < kCols ? 128 / sizeof(T) : kCols;  // columns a pass: 128 bytes at most
+                constexpr int kOnce = 128 / sizeof(T);  // columns a pass
+                static_assert(kCols % (2 * kOnce) == 0 || kCols == kOnce, "passes take the two buffers in turn");
 #pragma unroll
                 for (int c = 0; c < kCols; c += kOnce) {
                     uint4 w[8];
-                    T* wt = reinterpret_cast<T*>(w);
+                    uint32_t* ww = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
                     for (int j = 0; j < kOnce; j += 2) {
-                        const float2 x = unpack2(acc[(c + j) / 2]);
-                        wt[j] = from_f<T>(g.relu && x.x < 0.f ? 0.f : x.x);
-                        wt[j + 1] = from_f<T>(g.relu && x.y < 0.f ? 0.f : x.y);
+                        float2 x = unpack2(acc[(c + j) / 2]);
+                        if (g.relu) x = make_float2(relu(x.x), relu(x.y));
+                        if constexpr (sizeof(T) == 4) ww[j] = __float_as_uint(x.x), ww[j + 1] = __float_as_uint(x.y);
+                        else ww[j / 2] = pair_of<T>(x);
                     }
-                    store_rows<T, kOnce * sizeof(T) / 16>(sm.stage[w16], w, static_cast<T*>(g.out) + row0 * g.os + col + c, g.os,
-                                                          g.m - row0, g.n - col - c, g.vec, lane);
+                    uint8_t* st = sm.stage[w8][passes++ & 1];
+                    if (g.vec) {
+                        // the copy before the last has left this buffer; the last may still run
+                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                        __syncwarp();
+                        stage_rows(st, w, lane);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (row0 < g.m && col + c < g.n) tma_store(&map_out, st, col + c, int(row0));
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // one a pass, for the wait above
+                        }
+                    } else {
+                        __syncwarp();
+                        stage_rows(st, w, lane);
+                        __syncwarp();
+                        copy_rows(st, static_cast<T*>(g.out) + row0 * g.os + col + c, g.os, g.m - row0, g.n - col - c, lane);
+                    }
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // no copy outlasts the CTA
+        __syncwarp();
     }
     tc_before();
     __syncthreads();
@@ -480,7 +558,7 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
     }
     const int n = n0 + wrow;
     auto store = [&](int j, float v) {
-        if (g.relu && v < 0.f) v = 0.f;
+        if (g.relu) v = relu(v);
         static_cast<T*>(g.out)[size_t(j) * g.os + n] = from_f<T>(v);
     };
     // every role is done with the operands' memory after this barrier: the sums take their place
@@ -532,7 +610,7 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] += p[j * 128];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sm[cc + j][row] = g.relu && v[j] < 0.f ? 0.f : v[j];
+    for (int j = 0; j < 4; ++j) sm[cc + j][row] = g.relu ? relu(v[j]) : v[j];
     __syncthreads();
     const int c = threadIdx.x & 7;
     const long long col = (long long)(tile % g.tiles_n) * bn + c0 + c;
@@ -582,13 +660,14 @@ EncodeTiled encode_tiled() {
     return f;
 }
 
-// A [rows][cols] matrix of bytes, read in boxes of 128 columns and `box` rows; what lies outside reads as zero.
-bool encode(CUtensorMap* map, const uint8_t* p, size_t stride, int rows, int cols, int box) {
+// A [rows][cols] matrix, moved in boxes of 128 bytes of a row and `box` rows; what lies outside reads as zero and is not
+// written.
+bool encode(CUtensorMap* map, CUtensorMapDataType type, size_t size, const void* p, size_t stride, int rows, int cols, int box) {
     const EncodeTiled f = encode_tiled();
     if (!f) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride)};
-    const cuuint32_t boxes[2] = {128, cuuint32_t(box)}, steps[2] = {1, 1};
-    return f(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p), dims, strides, boxes, steps,
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride * size)};
+    const cuuint32_t boxes[2] = {cuuint32_t(128 / size), cuuint32_t(box)}, steps[2] = {1, 1};
+    return f(map, type, 2, const_cast<void*>(p), dims, strides, boxes, steps,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -617,6 +696,9 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned gri
 
 template <typename T, int BN, bool ROWS>
 cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
+    CUtensorMap out{};
+    constexpr CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    if (g.vec && g.splits == 1 && !encode(&out, type, sizeof(T), g.out, g.os, g.m, g.n, 32)) return cudaErrorUnknown;
     constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
     // the kernel's register split counts on what it is launched with
     static const bool enough = [] {
@@ -624,7 +706,7 @@ cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Matmul
         return cudaFuncGetAttributes(&f, k_matmul_tile<T, BN, ROWS>) == cudaSuccess && f.numRegs >= kRegsLaunch;
     }();
     if (!enough) return cudaErrorInvalidConfiguration;
-    return launch_clusters(k_matmul_tile<T, BN, ROWS>, 2, 2u * std::min(kPairs, g.tiles * g.splits), kTileThreads, smem, s, a, b, g);
+    return launch_clusters(k_matmul_tile<T, BN, ROWS>, 2, 2u * std::min(kPairs, g.tiles * g.splits), kTileThreads, smem, s, a, b, out, g);
 }
 
 template <typename T, int NT, bool ROWS>
@@ -676,8 +758,9 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     if (need > 0 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
     if (workspace_bytes < need) return RS_ERR_WORKSPACE;
     CUtensorMap ma, mb;
-    if (!encode(&ma, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2)) return RS_ERR_CUDA;
-    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z),
+    constexpr CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (!encode(&ma, bytes, 1, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, bytes, 1, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2)) return RS_ERR_CUDA;
+    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40),
                  p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
