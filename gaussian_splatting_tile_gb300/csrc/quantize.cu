@@ -19,32 +19,75 @@ struct QuantArgs {
     int ctiles, rtiles;
 };
 
+// Where the transposed tile keeps the eight bytes of column c, rows 8 u to 8 u + 7: the sixteen threads that write the same u
+// of sixteen columns eight apart, and the eight that read a column's sixteen-byte words, all hit different banks.
+__device__ __forceinline__ int tile_unit(int c, int u) { return c * 16 + (u ^ ((c >> 3) & 15)); }
+
+// The 8 x 8 values of one thread, scaled by column (inv[j]), to the transposed bytes.
+template <typename T>
+__device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<T> (&v)[8], const float (&inv)[8], uint2* tile,
+                                                 int tx, int ty, int c0, long long r0) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        float x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 w = v[i].pair(j / 2);
+            x[i] = w.x * inv[j];
+            y[i] = w.y * inv[j + 1];
+        }
+        tile[tile_unit(tx * 8 + j, ty)] = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
+        tile[tile_unit(tx * 8 + j + 1, ty)] = make_uint2(e4m3x4(y[0], y[1], y[2], y[3]), e4m3x4(y[4], y[5], y[6], y[7]));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int tc = p * 32 + int(threadIdx.x >> 3), k = int(threadIdx.x & 7), tr = k * 16;
+        if (c0 + tc >= a.cols || r0 + tr >= a.rows) continue;
+        uint8_t* o = a.qt + size_t(c0 + tc) * a.qts + r0 + tr;
+        const uint2 lo = tile[tile_unit(tc, 2 * k)], hi = tile[tile_unit(tc, 2 * k + 1)];
+        const uint4 w = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        const long long rest = a.rows - (r0 + tr);
+        if (rest >= 16) {
+            *reinterpret_cast<uint4*>(o) = w;
+        } else {
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < rest) o[i] = uint8_t(ws[i >> 2] >> (8 * (i & 3)));
+        }
+    }
+}
+
 template <typename T, bool VEC, bool BLOCKS>
-__global__ void __launch_bounds__(256) k_quantize(QuantArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_quantize(QuantArgs a) {
     RS_PDL_ENTER();
-    __shared__ float cmax[16][kBlock + 4];
-    __shared__ __align__(16) uint8_t tile[kBlock][kBlock + 16];  // the transposed bytes
+    __shared__ float cmax[16][kBlock];
+    __shared__ __align__(16) uint2 tile[kBlock * 16];  // the transposed bytes
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int ct = blockIdx.x % a.ctiles, rt = blockIdx.x / a.ctiles;  // neighbours share the rows
     const int c0 = ct * kBlock, c = c0 + tx * 8;
     const long long r0 = (long long)rt * kBlock, r = r0 + ty * 8;
     const int left = a.cols - c;
-    float v[8][8];
+    Run8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool in = r + i < a.rows;
-        load8<T, VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0, v[i]);
-        if (a.relu) {
-            float u[8];
-            load8<T, VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0, u);
+        v[i].template load<VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
+    }
+    if (a.relu) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = u[j] <= 0.f ? 0.f : v[i][j];
+        for (int i = 0; i < 8; ++i) {
+            const bool in = r + i < a.rows;
+            Run8<T> u;
+            u.template load<VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0);
+            v[i].mask(u);
         }
     }
     if constexpr (BLOCKS) {
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max_abs8(v[i], m);
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, max_abs8(v[i]));
         m = group_max<32>(m);
         if ((threadIdx.x & 31) == 0) cmax[0][threadIdx.x >> 5] = m;
         __syncthreads();
@@ -56,31 +99,46 @@ __global__ void __launch_bounds__(256) k_quantize(QuantArgs a) {
             if (a.q) a.scales[size_t(ct) * a.rtiles + rt] = scale;
             if (a.qt) a.scales_t[size_t(rt) * a.ctiles + ct] = scale;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-            if (a.q && r + i < a.rows && left > 0) store8_e4m3(a.q + (r + i) * a.qs + c, left, v[i], 1.f);
-        }
-    } else {
         if (a.q) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float scale, inv;
-                block_scale(group_max<16>(max_abs8(v[i], 0.f)), scale, inv);
-                if (r + i < a.rows && left > 0) {
-                    store8_e4m3(a.q + (r + i) * a.qs + c, left, v[i], inv);
-                    if (tx == 0) a.scales[size_t(ct) * a.rows + r + i] = scale;
+            for (int i = 0; i < 8; ++i)
+                if (r + i < a.rows && left > 0) store8_e4m3(a.q + (r + i) * a.qs + c, left, v[i], inv);
+        }
+        const float invs[8] = {inv, inv, inv, inv, inv, inv, inv, inv};
+        if (a.qt) store_transposed(a, v, invs, tile, tx, ty, c0, r0);
+    } else {
+        if (a.q) {
+            // The eight rows' maxima over the sixteen threads beside each other: every exchange halves the rows that a thread
+            // goes on with, so that thread tx ends with row (tx >> 1 & 7) and forms that row's two quotients alone.
+            float m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = max_abs8(v[i]);
+#pragma unroll
+            for (int o = 8, n = 4; n; o >>= 1, n >>= 1)
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const bool upper = tx & o;
+                    const float other = __shfl_xor_sync(0xffffffffu, upper ? m[i] : m[i + n], o);
+                    m[i] = fmaxf(upper ? m[i + n] : m[i], other);
                 }
+            float scale, inv;
+            block_scale(fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1)), scale, inv);
+            const int mine = (tx & 8 ? 4 : 0) + (tx & 4 ? 2 : 0) + (tx & 2 ? 1 : 0);
+            if (!(tx & 1) && r + mine < a.rows) a.scales[size_t(ct) * a.rows + r + mine] = scale;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int from = (i & 4 ? 8 : 0) + (i & 2 ? 4 : 0) + (i & 1 ? 2 : 0);
+                const float k = __shfl_sync(0xffffffffu, inv, from, 16);
+                if (r + i < a.rows && left > 0) store8_e4m3(a.q + (r + i) * a.qs + c, left, v[i], k);
             }
         }
         if (!a.qt) return;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float m = 0.f;
+        for (int p = 0; p < 4; ++p) {
+            typename Run8<T>::Max m;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i][j]));
-            cmax[ty][tx * 8 + j] = m;
+            for (int i = 0; i < 8; ++i) v[i].max_into(m, p);
+            *reinterpret_cast<float2*>(&cmax[ty][tx * 8 + 2 * p]) = Run8<T>::wide(m);
         }
         __syncthreads();
         if (threadIdx.x < kBlock) {
@@ -92,32 +150,10 @@ __global__ void __launch_bounds__(256) k_quantize(QuantArgs a) {
             cmax[0][threadIdx.x] = inv;  // this column of row 0 is read by this thread alone
         }
         __syncthreads();
+        float invs[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float inv = cmax[0][tx * 8 + j];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i][j] *= inv;
-        }
-    }
-    if (!a.qt) return;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const uint32_t lo = e4m3x4(v[0][j], v[1][j], v[2][j], v[3][j]);
-        const uint32_t hi = e4m3x4(v[4][j], v[5][j], v[6][j], v[7][j]);
-        *reinterpret_cast<uint2*>(&tile[tx * 8 + j][ty * 8]) = make_uint2(lo, hi);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const int tc = p * 32 + int(threadIdx.x >> 3), tr = int(threadIdx.x & 7) * 16;
-        if (c0 + tc >= a.cols || r0 + tr >= a.rows) continue;
-        uint8_t* o = a.qt + size_t(c0 + tc) * a.qts + r0 + tr;
-        const long long rest = a.rows - (r0 + tr);
-        if (rest >= 16) {
-            *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(&tile[tc][tr]);
-        } else {
-            for (int i = 0; i < rest; ++i) o[i] = tile[tc][tr + i];
-        }
+        for (int j = 0; j < 8; ++j) invs[j] = cmax[0][tx * 8 + j];
+        store_transposed(a, v, invs, tile, tx, ty, c0, r0);
     }
 }
 

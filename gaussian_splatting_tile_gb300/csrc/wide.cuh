@@ -63,6 +63,65 @@ __device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
         if (i < left) p[i] = from_f<T>(v[i]);
 }
 
+// Eight consecutive values as they are stored: 16-bit types stay packed in four registers, where a maximum of
+// magnitudes is exact, and are widened where they are used.
+template <typename T>
+struct Run8 {
+    float v[8];
+    __device__ __forceinline__ float2 pair(int p) const { return make_float2(v[2 * p], v[2 * p + 1]); }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* p, int left) { load8<T, VEC>(p, left, v); }
+    // zero where u <= 0
+    __device__ __forceinline__ void mask(const Run8& u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = u.v[i] <= 0.f ? 0.f : v[i];
+    }
+    // m = max(m, |values|), pair by pair
+    struct Max { float x = 0.f, y = 0.f; };
+    __device__ __forceinline__ void max_into(Max& m, int p) const {
+        m.x = fmaxf(m.x, fabsf(v[2 * p]));
+        m.y = fmaxf(m.y, fabsf(v[2 * p + 1]));
+    }
+    static __device__ __forceinline__ float2 wide(const Max& m) { return make_float2(m.x, m.y); }
+};
+
+template <typename T, typename T2>
+struct PackedRun8 {
+    uint4 w;
+    __device__ __forceinline__ uint32_t word(int p) const { return p == 0 ? w.x : p == 1 ? w.y : p == 2 ? w.z : w.w; }
+    __device__ __forceinline__ float2 pair(int p) const {
+        const uint32_t x = word(p);
+        const T2 h = *reinterpret_cast<const T2*>(&x);
+        return make_float2(to_f(h.x), to_f(h.y));
+    }
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T* p, int left) {
+        if (VEC && left >= 8) {
+            w = *reinterpret_cast<const uint4*>(p);
+        } else {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+            uint32_t h[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = i < left ? q[i] : 0;
+            w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+    }
+    static __device__ __forceinline__ uint32_t kept(uint32_t x, uint32_t u) {
+        return x & ~__hle2_mask(*reinterpret_cast<const T2*>(&u), T2{T(0.f), T(0.f)});
+    }
+    __device__ __forceinline__ void mask(const PackedRun8& u) {
+        w = make_uint4(kept(w.x, u.w.x), kept(w.y, u.w.y), kept(w.z, u.w.z), kept(w.w, u.w.w));
+    }
+    struct Max { T2 h = {T(0.f), T(0.f)}; };
+    __device__ __forceinline__ void max_into(Max& m, int p) const {
+        const uint32_t x = word(p) & 0x7fff7fffu;
+        m.h = __hmax2(m.h, *reinterpret_cast<const T2*>(&x));
+    }
+    static __device__ __forceinline__ float2 wide(const Max& m) { return make_float2(to_f(m.h.x), to_f(m.h.y)); }
+};
+template <> struct Run8<__half> : PackedRun8<__half, __half2> {};
+template <> struct Run8<__nv_bfloat16> : PackedRun8<__nv_bfloat16, __nv_bfloat162> {};
+
 // Four floats as e4m3 bytes, lowest first (round to nearest even; finite values past 448 become 448, NaN stays).
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
@@ -71,10 +130,8 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     return uint32_t(lo) | (uint32_t(hi) << 16);
 }
 
-// Eight scaled values as bytes.  A row starts on a 16-byte boundary and runs of eight on multiples of 8.
-__device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const float (&v)[8], float inv) {
-    const uint32_t lo = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    const uint32_t hi = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+// Up to eight bytes of a row.  A row starts on a 16-byte boundary and runs of eight on multiples of 8.
+__device__ __forceinline__ void store8_bytes(uint8_t* p, int left, uint32_t lo, uint32_t hi) {
     if (left >= 8) {
         *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
         return;
@@ -82,6 +139,17 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const float (&
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (i < left) p[i] = uint8_t((i < 4 ? lo : hi) >> (8 * (i & 3)));
+}
+
+// Eight values, scaled, as bytes.
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const float (&v)[8], float inv) {
+    store8_bytes(p, left, e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                 e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+template <typename T>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const Run8<T>& v, float inv) {
+    const float2 a = v.pair(0), b = v.pair(1), c = v.pair(2), d = v.pair(3);
+    store8_bytes(p, left, e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv), e4m3x4(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
 }
 
 // A block's scale and the factor its values are multiplied by, from its largest magnitude.  Both are correctly rounded
@@ -96,6 +164,15 @@ __device__ __forceinline__ float max_abs8(const float (&v)[8], float m) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
     return m;
+}
+
+template <typename T>
+__device__ __forceinline__ float max_abs8(const Run8<T>& v) {
+    typename Run8<T>::Max m;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) v.max_into(m, p);
+    const float2 w = Run8<T>::wide(m);
+    return fmaxf(w.x, w.y);
 }
 
 template <int W>
