@@ -202,19 +202,6 @@ __device__ __forceinline__ float relu(float x) {
     asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
     return r;
 }
-template <typename T>
-__device__ __forceinline__ uint32_t pair_of(float2 x);
-template <>
-__device__ __forceinline__ uint32_t pair_of<__half>(float2 x) {
-    const __half2 h = __float22half2_rn(x);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pair_of<__nv_bfloat16>(float2 x) {
-    const __nv_bfloat162 h = __float22bfloat162_rn(x);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A warp's 32 rows x 128 bytes of results (thread = row, eight 16-byte words) in shared memory, the words of row r at
 // word ^ (r mod 8): the 128-byte swizzle of the tensor map that takes them out, and no two of eight neighbours share a bank.
 __device__ __forceinline__ void stage_rows(uint8_t* st, const uint4 (&w)[8], int lane) {
@@ -413,7 +400,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                         float2 x = unpack2(acc[(c + j) / 2]);
                         if (g.relu) x = make_float2(relu(x.x), relu(x.y));
                         if constexpr (sizeof(T) == 4) ww[j] = __float_as_uint(x.x), ww[j + 1] = __float_as_uint(x.y);
-                        else ww[j / 2] = pair_of<T>(x);
+                        else ww[j / 2] = pack_pair(x.x, x.y, T());
                     }
                     uint8_t* st = sm.stage[w8][passes++ & 1];
                     if (g.vec) {

@@ -32,8 +32,9 @@ __device__ __forceinline__ float row_sum(float v, float* smem) {
         if ((threadIdx.x & 31) == 0) smem[threadIdx.x >> 5] = v;
         __syncthreads();
         v = 0.f;
+        const float* mine = smem + threadIdx.x / TPR * kWarps;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) v += smem[i];
+        for (int i = 0; i < kWarps; ++i) v += mine[i];
     }
     return v;
 }
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
 #pragma unroll
         for (int i = 0; i < RUNS; ++i) store8<T, VEC>(s + (i * TPR + t) * 8, a.cols - (i * TPR + t) * 8, v[i]);
     }
+    float top[RUNS];
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
         const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
@@ -78,14 +80,21 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
         if (a.y && left > 0) store8<T, VEC>(static_cast<T*>(a.y) + row * a.ys + c, left, v[i]);
-        if (a.q) {
-            float scale, inv;
-            block_scale(group_max<16>(max_abs8(v[i], 0.f)), scale, inv);
-            if (left > 0) {
-                store8_e4m3(a.q + row * a.qs + c, left, v[i], inv);
-                if ((t & 15) == 0) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
-            }
-        }
+        top[i] = group_max<16>(max_abs8(v[i], 0.f));
+    }
+    if (!a.q) return;
+    // thread i of the sixteen that share a block's columns forms run i's two quotients, and passes them on
+    const int of = t & 15;
+    float mine = top[0], scale, inv;
+#pragma unroll
+    for (int i = 1; i < RUNS; ++i) mine = of == i ? top[i] : mine;
+    block_scale(mine, scale, inv);
+#pragma unroll
+    for (int i = 0; i < RUNS; ++i) {
+        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        const float k = __shfl_sync(0xffffffffu, inv, i, 16);
+        if (of == i && c - of * 8 < a.cols && in) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
+        if (left > 0) store8_e4m3(a.q + row * a.qs + c, left, v[i], k);
     }
 }
 
@@ -131,14 +140,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdA
     __shared__ float smem[32];
     __shared__ float comb[kRows > 1 ? kThreads * 8 : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    float w[RUNS][8], dw[RUNS][8];
+    float dw[RUNS][8];
 #pragma unroll
-    for (int i = 0; i < RUNS; ++i) {
-        const int c = (i * TPR + t) * 8;
-        load8<float, VEC>(a.w + c, a.cols - c, w[i]);
+    for (int i = 0; i < RUNS; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    }
     for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += (long long)gridDim.x * kRows) {
         const long long row = base + sub;
         const bool in = row < a.rows;
@@ -146,37 +152,47 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdA
         const float rstd = in ? a.rstd[rr] : 0.f;
         const T* s = static_cast<const T*>(a.s) + rr * a.ss;
         const T* dy = static_cast<const T*>(a.dy) + rr * a.dys;
-        float xh[RUNS][8], tt[RUNS][8];
-        float dot = 0.f;
+        const T* ds = a.ds ? static_cast<const T*>(a.ds) + rr * a.dss : nullptr;
+        // everything that the row needs is asked for at once; s, dy and ds wait as they are stored
+        Run8<T> sv[RUNS], gv[RUNS], dv[RUNS];
 #pragma unroll
         for (int i = 0; i < RUNS; ++i) {
             const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
-            load8<T, VEC>(s + c, left, xh[i]);
-            load8<T, VEC>(dy + c, left, tt[i]);
+            sv[i].template load<VEC>(s + c, left);
+            gv[i].template load<VEC>(dy + c, left);
+            if (ds) dv[i].template load<VEC>(ds + c, left);
+        }
+        float dot = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                xh[i][j] *= rstd;
-                dw[i][j] = fmaf(tt[i][j], xh[i][j], dw[i][j]);
-                tt[i][j] *= w[i][j];
-                dot = fmaf(tt[i][j], xh[i][j], dot);
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = (i * TPR + t) * 8;
+            float w[8];
+            load8<float, VEC>(a.w + c, a.cols - c, w);  // from L1: registers for it would cost a block of the SM
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2 x = sv[i].pair(p), g = gv[i].pair(p);
+                const float x0 = x.x * rstd, x1 = x.y * rstd;
+                dw[i][2 * p] = fmaf(g.x, x0, dw[i][2 * p]);
+                dw[i][2 * p + 1] = fmaf(g.y, x1, dw[i][2 * p + 1]);
+                dot = fmaf(g.x * w[2 * p], x0, dot);
+                dot = fmaf(g.y * w[2 * p + 1], x1, dot);
             }
         }
         const float c1 = row_sum<TPR>(dot, smem) * a.inv_cols;
         if (in) {
-            const T* ds = a.ds ? static_cast<const T*>(a.ds) + row * a.dss : nullptr;
             T* dx = static_cast<T*>(a.dx) + row * a.dxs;
 #pragma unroll
             for (int i = 0; i < RUNS; ++i) {
                 const int c = (i * TPR + t) * 8, left = a.cols - c;
-                float o[8];
-                if (ds) {
-                    load8<T, VEC>(ds + c, left, o);
-                } else {
+                float o[8], w[8];
+                load8<float, VEC>(a.w + c, left, w);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = 0.f;
+                for (int p = 0; p < 4; ++p) {
+                    const float2 x = sv[i].pair(p), g = gv[i].pair(p);
+                    const float2 d = ds ? dv[i].pair(p) : make_float2(0.f, 0.f);
+                    o[2 * p] = fmaf(rstd, g.x * w[2 * p] - x.x * rstd * c1, d.x);
+                    o[2 * p + 1] = fmaf(rstd, g.y * w[2 * p + 1] - x.y * rstd * c1, d.y);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = fmaf(rstd, tt[i][j] - xh[i][j] * c1, o[j]);
                 store8<T, VEC>(dx + c, left, o);
             }
         }
@@ -218,10 +234,15 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = v;
 }
 
-int bwd_rows_per_block(int cols) { return cols <= 128 ? 8 : cols <= 1024 ? 4 : 1; }
+// Threads a row and blocks an SM for a width.  One run a thread as far as that goes: its registers (the share of
+// dL/dweight among them) then leave room for many rows in flight.
+int bwd_threads(int cols) {
+    const int runs = ceil_div(cols, 8);
+    return runs <= 16 ? 16 : runs <= 32 ? 32 : runs <= 64 ? 64 : runs <= 128 ? 128 : runs <= 256 ? 256 : 512;
+}
 int bwd_blocks(int rows, int cols) {
-    const int per = cols <= 512 ? 6 : cols <= 1024 ? 4 : cols <= 4096 ? 2 : 1;
-    return std::max(1, std::min(ceil_div(rows, bwd_rows_per_block(cols)), kSms * per));
+    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1, per = t <= 128 ? 8 : t == 256 ? 4 : 2;
+    return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * per));
 }
 
 template <typename T, bool VEC, int TPR, int RUNS>
@@ -231,15 +252,15 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
 
 template <typename T, bool VEC>
 cudaError_t bwd_width(const NormBwdArgs& a, cudaStream_t s) {
-    const int runs = ceil_div(a.cols, 8);
-    if (runs <= 16) return bwd<T, VEC, 16, 1>(a, s);
-    if (runs <= 32) return bwd<T, VEC, 32, 1>(a, s);
-    if (runs <= 64) return bwd<T, VEC, 32, 2>(a, s);
-    if (runs <= 128) return bwd<T, VEC, 32, 4>(a, s);
-    if (runs <= 256) return bwd<T, VEC, 128, 2>(a, s);
-    if (runs <= 512) return bwd<T, VEC, 256, 2>(a, s);
-    if (runs <= 1024) return bwd<T, VEC, 512, 2>(a, s);
-    return bwd<T, VEC, 512, 4>(a, s);
+    switch (bwd_threads(a.cols)) {
+        case 16: return bwd<T, VEC, 16, 1>(a, s);
+        case 32: return bwd<T, VEC, 32, 1>(a, s);
+        case 64: return bwd<T, VEC, 64, 1>(a, s);
+        case 128: return bwd<T, VEC, 128, 1>(a, s);
+        case 256: return bwd<T, VEC, 256, 1>(a, s);
+    }
+    if (a.cols <= 4096) return bwd<T, VEC, 512, 1>(a, s);
+    return a.cols <= 8192 ? bwd<T, VEC, 512, 2>(a, s) : bwd<T, VEC, 512, 4>(a, s);
 }
 
 bool matrix_ok(const void* p, size_t stride, int32_t cols, int32_t dtype) {

@@ -22,55 +22,24 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// Eight consecutive values at `p`, of which the first `left` exist (the others read as zero).  VEC: p is aligned to
-// 16 bytes; a whole run is then one or two 16-byte accesses.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
-    if (VEC && left >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            const T* h = reinterpret_cast<const T*>(&w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = to_f(h[i]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_f(p[i]) : 0.f;
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
-    if (VEC && left >= 8) {
-        if constexpr (sizeof(T) == 4) {
-            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            uint4 w;
-            T* h = reinterpret_cast<T*>(&w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = from_f<T>(v[i]);
-            *reinterpret_cast<uint4*>(p) = w;
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < left) p[i] = from_f<T>(v[i]);
-}
-
-// Eight consecutive values as they are stored: 16-bit types stay packed in four registers, where a maximum of
+// Eight consecutive values as they are stored, of which the first `left` exist (the others read as zero).  VEC: the place
+// is aligned to 16 bytes, and a whole run is one or two 16-byte accesses.  16-bit types stay packed in four registers, where a maximum of
 // magnitudes is exact, and are widened where they are used.
 template <typename T>
 struct Run8 {
     float v[8];
     __device__ __forceinline__ float2 pair(int p) const { return make_float2(v[2 * p], v[2 * p + 1]); }
     template <bool VEC>
-    __device__ __forceinline__ void load(const T* p, int left) { load8<T, VEC>(p, left, v); }
+    __device__ __forceinline__ void load(const T* p, int left) {
+        if (VEC && left >= 8) {
+            const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
+        }
+    }
     // zero where u <= 0
     __device__ __forceinline__ void mask(const Run8& u) {
 #pragma unroll
@@ -128,6 +97,45 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return uint32_t(lo) | (uint32_t(hi) << 16);
+}
+
+// The same as floats.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+    Run8<T> r;
+    r.template load<VEC>(p, left);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 w = r.pair(i);
+        v[2 * i] = w.x;
+        v[2 * i + 1] = w.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack_pair(float a, float b, __half) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_pair(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
+    if (VEC && left >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack_pair(v[0], v[1], T()), pack_pair(v[2], v[3], T()),
+                                                      pack_pair(v[4], v[5], T()), pack_pair(v[6], v[7], T()));
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < left) p[i] = from_f<T>(v[i]);
 }
 
 // Up to eight bytes of a row.  A row starts on a 16-byte boundary and runs of eight on multiples of 8.
