@@ -14,7 +14,7 @@ namespace {
 constexpr int kTable = 400;         // tensors a launch: 32 KB of kernel parameters hold the table
 constexpr int kSmallTable = 48;
 constexpr int kChunk = 8192;        // values a block takes at a time: 32 a thread
-constexpr int kNormBlocks = kSms * 6;
+constexpr int kNormBlocks = kSms * 8;
 
 template <int N>
 struct ClipTable {
@@ -47,26 +47,48 @@ __device__ __forceinline__ float chain(int act, float g, float p) {
     return g;
 }
 
+constexpr int kRuns = kChunk / (256 * 8);  // runs of eight a thread
+
+template <typename T, bool VEC>
+__device__ __forceinline__ float chunk_squares_t(const T* g, const float* p, int act, int len) {
+    Run8<T> v[kRuns];  // all of the chunk is asked for before any of it is used
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        const int o = (i * 256 + int(threadIdx.x)) * 8;
+        v[i].template load<VEC>(g + o, len - o);
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        if (!p) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 x = v[i].pair(k);
+                ss = fmaf(x.x, x.x, ss);
+                ss = fmaf(x.y, x.y, ss);
+            }
+        } else {
+            const int o = (i * 256 + int(threadIdx.x)) * 8;
+            float u[8];
+            load8<float, VEC>(p + o, len - o, u);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 x = v[i].pair(k);  // past the end: a gradient of zero
+                const float a = chain(act, x.x, u[2 * k]), b = chain(act, x.y, u[2 * k + 1]);
+                ss = fmaf(a, a, ss);
+                ss = fmaf(b, b, ss);
+            }
+        }
+    }
+    return ss;
+}
+
 template <typename T>
 __device__ __forceinline__ float chunk_squares(const rs_grad_tensor& d, size_t at, int len) {
     const T* g = static_cast<const T*>(d.d_grad) + at;
     const float* p = d.activation == RS_ACT_IDENTITY ? nullptr : d.d_param + at;
     const bool vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < kChunk / (256 * 8); ++i) {
-        const int o = (i * 256 + int(threadIdx.x)) * 8;
-        float v[8], u[8];
-        vec ? load8<T, true>(g + o, len - o, v) : load8<T, false>(g + o, len - o, v);
-        if (p) {
-            vec ? load8<float, true>(p + o, len - o, u) : load8<float, false>(p + o, len - o, u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = o + j < len ? chain(d.activation, v[j], u[j]) : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-    }
-    return ss;
+    return vec ? chunk_squares_t<T, true>(g, p, d.activation, len) : chunk_squares_t<T, false>(g, p, d.activation, len);
 }
 
 template <int N>
@@ -94,20 +116,34 @@ __global__ void __launch_bounds__(256) k_grad_squares(const __grid_constant__ Cl
     }
 }
 
+template <typename T, bool VEC>
+__device__ __forceinline__ void chunk_scale_t(const T* g, T* out, int len, float c) {
+    Run8<T> r[kRuns];
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        const int o = (i * 256 + int(threadIdx.x)) * 8;
+        r[i].template load<VEC>(g + o, len - o);
+    }
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+        const int o = (i * 256 + int(threadIdx.x)) * 8;
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 x = r[i].pair(k);
+            v[2 * k] = x.x * c;
+            v[2 * k + 1] = x.y * c;
+        }
+        store8<T, VEC>(out + o, len - o, v);
+    }
+}
+
 template <typename T>
 __device__ __forceinline__ void chunk_scale(const rs_grad_tensor& d, size_t at, int len, float c) {
     const T* g = static_cast<const T*>(d.d_grad) + at;
     T* out = static_cast<T*>(d.d_out) + at;
     const bool vec = reinterpret_cast<uintptr_t>(g) % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
-#pragma unroll
-    for (int i = 0; i < kChunk / (256 * 8); ++i) {
-        const int o = (i * 256 + int(threadIdx.x)) * 8;
-        float v[8];
-        vec ? load8<T, true>(g + o, len - o, v) : load8<T, false>(g + o, len - o, v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= c;
-        vec ? store8<T, true>(out + o, len - o, v) : store8<T, false>(out + o, len - o, v);
-    }
+    vec ? chunk_scale_t<T, true>(g, out, len, c) : chunk_scale_t<T, false>(g, out, len, c);
 }
 
 template <int N>
@@ -117,7 +153,8 @@ __global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ Clip
     if (T.norm && blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
     const float c = clip_factor(T.max_norm, norm);
     const uint32_t chunks = T.start[T.n];
-    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
+    for (uint32_t from = blockIdx.x; from < chunks; from += gridDim.x) {
+        const uint32_t k = chunks - 1 - from;  // the norm's pass ended there: L2 still has it
         const int i = tensor_of(T, k);
         const rs_grad_tensor& d = T.t[i];
         if (!d.d_out || (c == 1.f && d.d_out == d.d_grad)) continue;

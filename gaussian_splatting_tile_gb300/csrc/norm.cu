@@ -110,7 +110,7 @@ cudaError_t fwd_width(const NormArgs& a, cudaStream_t s) {
     if (runs <= 16) return fwd<T, VEC, 16, 1>(a, s);
     if (runs <= 32) return fwd<T, VEC, 32, 1>(a, s);
     if (runs <= 64) return fwd<T, VEC, 32, 2>(a, s);
-    if (runs <= 128) return fwd<T, VEC, 32, 4>(a, s);
+    if (runs <= 128) return fwd<T, VEC, 64, 2>(a, s);
     if (runs <= 256) return fwd<T, VEC, 128, 2>(a, s);
     if (runs <= 512) return fwd<T, VEC, 256, 2>(a, s);
     if (runs <= 1024) return fwd<T, VEC, 512, 2>(a, s);

@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(256) k_adam(const __grid_constant__ AdamTable 
     }
     const size_t stride = size_t(gridDim.x) * blockDim.x;
     const size_t nq = T.qstart[T.n];
-    for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < nq; i += stride) {
+    for (size_t from = size_t(blockIdx.x) * blockDim.x + threadIdx.x; from < nq; from += stride) {
+        const size_t i = CLIP ? nq - 1 - from : from;  // the norm's pass ended at the end: L2 still has those gradients
         int s = 0;
         while (s + 1 < T.n && i >= T.qstart[s + 1]) ++s;
         const rs_adam_segment& S = T.seg[s];
