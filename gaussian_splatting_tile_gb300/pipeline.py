@@ -274,6 +274,133 @@ class AppearanceStep:
         return F, self.backward(stream=stream)
 
 
+class _Linear:
+    """A linear layer's float32 weights [out, in] with their 8-bit form per 128 x 128 block, both ways round."""
+
+    def __init__(self, w: torch.Tensor):
+        self.w, self.dw = w, torch.empty_like(w)
+        o, i = w.shape
+        ob, ib = -(-o // rs.RS_FP8_BLOCK), -(-i // rs.RS_FP8_BLOCK)
+        self.q, self.qt = rs.fp8_empty(o, i, w.device)[0], rs.fp8_empty(i, o, w.device)[0]
+        self.s = torch.empty(ib, ob, dtype=torch.float32, device=w.device)
+        self.st = torch.empty(ob, ib, dtype=torch.float32, device=w.device)
+        self.refresh()
+
+    def refresh(self, stream=None):
+        rs.rs_quantize_fp8_blocks(self.w, self.q, self.s, self.qt, self.st, stream=stream)
+
+
+class WideAppearance:
+    """A residual appearance network wider than rs_mlp allows: per Gaussian, features [width] -> colour [3],
+
+        h_0 = features;  r_b = relu(norm_b(h_b) W1_b^T) W2_b^T,  h_{b+1} = h_b + r_b;  colour = sigmoid(norm(h_B) Wo^T)
+
+    with root-mean-square norms, every product on 8-bit operands (float32 sums, `dtype` activations) and float32 master
+    weights.  `forward` gives the planar colours that rs_project reads when sh_degree is -1, `backward` takes
+    the colours' gradient that rs_rasterize_bwd returns, and `step` is one Adam step over all parameters (and the caller's own
+    groups) with their gradients clipped to a global norm; nothing in the three waits on the host."""
+
+    def __init__(self, features: torch.Tensor, hidden: int, blocks: int = 2, dtype=torch.bfloat16, seed: int = 0):
+        n, c = features.shape
+        if 3 * blocks + 3 > rs.RS_ADAM_MAX_SEGMENTS:
+            raise ValueError(f"at most {(rs.RS_ADAM_MAX_SEGMENTS - 3) // 3} blocks")
+        self.n, self.width, self.hidden, self.dtype = int(n), int(c), int(hidden), dtype
+        self.device = dev = features.device
+        g = torch.Generator(dev).manual_seed(seed)
+        rand = lambda o, i: torch.randn(o, i, device=dev, generator=g) / i ** 0.5
+        self.features, self.dfeatures = features, torch.empty_like(features)
+        self.norms = [torch.ones(c, device=dev) for _ in range(blocks + 1)]
+        self.dnorms = [torch.empty(c, device=dev) for _ in range(blocks + 1)]
+        self.up = [_Linear(rand(hidden, c)) for _ in range(blocks)]
+        self.down = [_Linear(rand(c, hidden)) for _ in range(blocks)]
+        self.head = _Linear(rand(3, c))
+        e = lambda r, k, d=dtype: torch.empty(r, k, dtype=d, device=dev)
+        # kept for the backward: each norm's input sum, output and statistic, each relu's output
+        self.h = [e(n, c) for _ in range(blocks + 1)]
+        self.y = [e(n, c) for _ in range(blocks + 1)]
+        self.rstd = [torch.empty(n, dtype=torch.float32, device=dev) for _ in range(blocks + 1)]
+        self.u = [e(n, hidden) for _ in range(blocks)]
+        # scratch: 8-bit operands by rows and by columns, gradients, results of products
+        self.qc, self.qct = rs.fp8_empty(n, c, dev), rs.fp8_empty(c, n, dev)
+        self.qh, self.qht = rs.fp8_empty(n, hidden, dev), rs.fp8_empty(hidden, n, dev)
+        self.q3, self.q3t = rs.fp8_empty(n, 3, dev), rs.fp8_empty(3, n, dev)
+        self.r, self.dh, self.dy, self.du = e(n, c), e(n, c), e(n, c), e(n, hidden)
+        self.z = torch.empty(n, 3, dtype=torch.float32, device=dev)
+        self.colors = torch.empty(3, n, dtype=torch.float32, device=dev)
+        sizes = [(n, hidden, c), (n, c, hidden), (n, 3, c), (n, c, 3), (hidden, c, n), (c, hidden, n), (3, c, n)]
+        need = max([rs.rs_matmul_fp8_workspace_size(*s) for s in sizes] +
+                   [rs.rs_rms_norm_bwd_workspace_size(n, c), rs.rs_grad_norm_workspace_size(rs.RS_ADAM_MAX_SEGMENTS)])
+        self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.moments = None
+        self.steps = 0
+
+    def _product(self, a, b, b_scales, out, relu=False):
+        rs.rs_matmul_fp8(*a, b, b_scales, out, self.workspace, relu=relu)
+
+    def forward(self, stream=None) -> torch.Tensor:
+        """colours [3, n] (planar) of the features and weights as they are."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            x, residual = self.h[0], None
+            x.copy_(self.features)
+            for b in range(len(self.up) + 1):
+                rs.rs_rms_norm_fwd(x, self.norms[b], *self.qc, residual=residual, sum=self.h[b] if b else None,
+                                   y=self.y[b], rstd=self.rstd[b])
+                if b == len(self.up):
+                    break
+                self._product(self.qc, self.up[b].q, self.up[b].s, self.u[b], relu=True)
+                rs.rs_quantize_fp8(self.u[b], *self.qh)
+                self._product(self.qh, self.down[b].q, self.down[b].s, self.r)
+                x, residual = self.h[b], self.r
+            self._product(self.qc, self.head.q, self.head.s, self.z)
+            torch.sigmoid(self.z.t(), out=self.colors)
+        return self.colors
+
+    def _weight_grad(self, grad_t, x, scratch_t, layer):
+        """layer.dw = grad^T x, both in 8 bits by columns."""
+        rs.rs_quantize_fp8(x, qt=scratch_t[0], scales_t=scratch_t[1])
+        self._product(grad_t, *scratch_t, layer.dw)
+
+    def backward(self, dL_dcolors: torch.Tensor, stream=None):
+        """Gradients of every weight (dnorms, the layers' dw) and of the features from dL/dcolours [3, n]."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            dz = (dL_dcolors * self.colors * (1 - self.colors)).t().contiguous()
+            last = len(self.up)
+            rs.rs_quantize_fp8(dz, *self.q3, *self.q3t)
+            self._weight_grad(self.q3t, self.y[last], self.qct, self.head)
+            self._product(self.q3, self.head.qt, self.head.st, self.dy)
+            rs.rs_rms_norm_bwd(self.h[last], self.norms[last], self.rstd[last], self.dy, self.dh, self.dnorms[last],
+                               self.workspace)
+            for b in reversed(range(last)):
+                # dh is the gradient of h_{b+1} = h_b + r_b: of r_b as it is, of h_b with what comes through the block
+                rs.rs_quantize_fp8(self.dh, *self.qc, *self.qct)
+                self._weight_grad(self.qct, self.u[b], self.qht, self.down[b])
+                self._product(self.qc, self.down[b].qt, self.down[b].st, self.du)
+                rs.rs_quantize_fp8(self.du, *self.qh, *self.qht, relu=self.u[b])
+                self._weight_grad(self.qht, self.y[b], self.qct, self.up[b])
+                self._product(self.qh, self.up[b].qt, self.up[b].st, self.dy)
+                rs.rs_rms_norm_bwd(self.h[b], self.norms[b], self.rstd[b], self.dy, self.dh, self.dnorms[b],
+                                   self.workspace, dL_dsum=self.dh)
+            self.dfeatures.copy_(self.dh)
+
+    def parameters(self):
+        """(parameter, gradient) of every group: the features, the norms, the layers."""
+        return ([(self.features, self.dfeatures)] + list(zip(self.norms, self.dnorms)) +
+                [(l.w, l.dw) for l in (*self.up, *self.down, self.head)])
+
+    def step(self, max_norm: float, lr: float = 1e-3, groups=(), stream=None):
+        """One clipped Adam step over the network and `groups` (rs.AdamGroup, e.g. the geometry's); the norm before
+        clipping is in self.norm."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
+            if self.moments is None:
+                self.moments = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _ in self.parameters()]
+            own = [rs.AdamGroup(p, g, m, v, lr) for (p, g), (m, v) in zip(self.parameters(), self.moments)]
+            self.steps += 1
+            rs.rs_adam_step_clipped([*own, *groups], self.steps, max_norm, self.norm, self.workspace)
+            for layer in (*self.up, *self.down, self.head):
+                layer.refresh()
+
+
 class AppearanceGraph:
     """One view of the training-shaped step (MLP colours, render, L1 loss, render backward, MLP
     backward) captured as a single CUDA graph, like FrameGraph: the camera is fixed, the
