@@ -59,8 +59,11 @@ __device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<
     }
 }
 
-template <typename T, bool VEC, bool BLOCKS>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_quantize(QuantArgs a) {
+// 16-bit values leave registers for three blocks an SM; with a mask beside x two, so that both tiles are in flight at once.
+enum Form { kRowsCols, kRowsColsRelu, kBlocks };
+template <typename T, bool VEC, Form FORM>
+__global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ? 2 : 3) k_quantize(QuantArgs a) {
+    constexpr bool BLOCKS = FORM == kBlocks;
     RS_PDL_ENTER();
     __shared__ float cmax[16][kBlock];
     __shared__ __align__(16) uint2 tile[kBlock * 16];  // the transposed bytes
@@ -75,14 +78,15 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 ? 2 : 3) k_quantize(QuantA
         const bool in = r + i < a.rows;
         v[i].template load<VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
     }
-    if (a.relu) {
+    if constexpr (FORM == kRowsColsRelu) {
+        Run8<T> u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const bool in = r + i < a.rows;
-            Run8<T> u;
-            u.template load<VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0);
-            v[i].mask(u);
+            u[i].template load<VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0);
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].mask(u[i]);
     }
     if constexpr (BLOCKS) {
         float m = 0.f;
@@ -175,11 +179,10 @@ int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s) {
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         const unsigned g = unsigned(a.ctiles) * a.rtiles;
-        if (blocks)
-            return vec ? pdl_launch(k_quantize<T, true, true>, g, 256, 0, s, a)
-                       : pdl_launch(k_quantize<T, false, true>, g, 256, 0, s, a);
-        return vec ? pdl_launch(k_quantize<T, true, false>, g, 256, 0, s, a)
-                   : pdl_launch(k_quantize<T, false, false>, g, 256, 0, s, a);
+        const auto launch = [&](auto kernel) { return pdl_launch(kernel, g, 256, 0, s, a); };
+        if (blocks) return vec ? launch(k_quantize<T, true, kBlocks>) : launch(k_quantize<T, false, kBlocks>);
+        if (a.relu) return vec ? launch(k_quantize<T, true, kRowsColsRelu>) : launch(k_quantize<T, false, kRowsColsRelu>);
+        return vec ? launch(k_quantize<T, true, kRowsCols>) : launch(k_quantize<T, false, kRowsCols>);
     });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }

@@ -712,17 +712,21 @@ def _dtype(t, name="tensor") -> int:
     return code
 
 
-def _mat(t, name, dtype, rows: int, cols: int):
-    """(pointer, row stride in elements) of a row-major CUDA matrix [rows, cols]; its rows may be apart."""
+def _mat(t, name, dtype, shape):
+    """(pointer, row stride in elements) of a row-major CUDA matrix of `shape` (rows, columns); its rows may be apart."""
     if t is None:
         return None, 0
+    # the common case in one line: these checks are most of a small call's time
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and shape[0] > 1:
+        return t.data_ptr(), shape[1]
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype and (dtype is not _FP8 or t.dtype not in _FP8):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name} is {tuple(t.shape)}, needs {(rows, cols)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, needs {tuple(shape)}")
     s0, s1 = t.stride()
+    rows, cols = shape
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
     # a single row's stride is never followed: give one that the alignment rules allow
@@ -733,9 +737,9 @@ def _vec(t, dtype, numel: int, name: str):
     """Pointer of a contiguous CUDA tensor of at least `numel` elements."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dtype or not t.is_contiguous() or t.numel() < numel:
-        return _ptr(t, dtype, numel, name)  # says what is wrong
-    return t.data_ptr()
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
+        return t.data_ptr()
+    return _ptr(t, dtype, numel, name)  # says what is wrong
 
 
 def fp8_empty(rows: int, cols: int, device="cuda"):
@@ -767,14 +771,14 @@ def rs_rms_norm_fwd(x, weight, q=None, scales=None, residual=None, sum=None, y=N
                     stream=None):
     """x, residual, sum, y: [rows, cols] float32 / float16 / bfloat16 CUDA; weight float32 [cols]; q, scales as
     fp8_empty(rows, cols) gives them; rstd float32 [rows].  sum, y and rstd are optional outputs."""
-    rows, cols = x.shape
+    shape = rows, cols = x.shape
     dt = x.dtype
     code = _dtype(x, "x")
-    px, sx = _mat(x, "x", dt, rows, cols)
-    pr, sr = _mat(residual, "residual", dt, rows, cols)
-    ps, ss = _mat(sum, "sum", dt, rows, cols)
-    py, sy = _mat(y, "y", dt, rows, cols)
-    pq, sq = _mat(q, "q", _FP8, rows, cols)
+    px, sx = _mat(x, "x", dt, shape)
+    pr, sr = _mat(residual, "residual", dt, shape)
+    ps, ss = _mat(sum, "sum", dt, shape)
+    py, sy = _mat(y, "y", dt, shape)
+    pq, sq = _mat(q, "q", _FP8, shape)
     _check("rs_rms_norm_fwd", lib().rs_rms_norm_fwd(
         rows, cols, code, px, sx, pr, sr, _vec(weight, torch.float32, cols, "weight"), eps, ps, ss, py, sy, pq, sq,
         _scales(scales, "scales", _blocks(cols), rows), _vec(rstd, torch.float32, rows, "rstd"), _stream(stream)))
@@ -786,13 +790,13 @@ def rs_rms_norm_bwd_workspace_size(rows: int, cols: int) -> int:
 
 def rs_rms_norm_bwd(s, weight, rstd, dL_dy, dL_dx, dL_dweight, workspace, dL_dsum=None, stream=None):
     """s: the forward's sum (x without a residual); dL_dx also is the residual's gradient; dL_dweight may be None."""
-    rows, cols = s.shape
+    shape = rows, cols = s.shape
     dt = s.dtype
     code = _dtype(s, "s")
-    ps, ss = _mat(s, "s", dt, rows, cols)
-    pg, sg = _mat(dL_dy, "dL_dy", dt, rows, cols)
-    pd, sd = _mat(dL_dsum, "dL_dsum", dt, rows, cols)
-    px, sx = _mat(dL_dx, "dL_dx", dt, rows, cols)
+    ps, ss = _mat(s, "s", dt, shape)
+    pg, sg = _mat(dL_dy, "dL_dy", dt, shape)
+    pd, sd = _mat(dL_dsum, "dL_dsum", dt, shape)
+    px, sx = _mat(dL_dx, "dL_dx", dt, shape)
     _check("rs_rms_norm_bwd", lib().rs_rms_norm_bwd(
         rows, cols, code, ps, ss, _vec(weight, torch.float32, cols, "weight"), _vec(rstd, torch.float32, rows, "rstd"),
         pg, sg, pd, sd, px, sx, _vec(dL_dweight, torch.float32, cols, "dL_dweight"),
@@ -802,12 +806,12 @@ def rs_rms_norm_bwd(s, weight, rstd, dL_dy, dL_dx, dL_dweight, workspace, dL_dsu
 def rs_quantize_fp8(x, q=None, scales=None, qt=None, scales_t=None, relu=None, stream=None):
     """8-bit forms of x [rows, cols]: q, scales as fp8_empty(rows, cols), and / or the transpose qt, scales_t as
     fp8_empty(cols, rows).  relu: a relu's output; x counts as zero where it is <= 0."""
-    rows, cols = x.shape
+    shape = rows, cols = x.shape
     code = _dtype(x, "x")
-    px, sx = _mat(x, "x", x.dtype, rows, cols)
-    pr, sr = _mat(relu, "relu", x.dtype, rows, cols)
-    pq, sq = _mat(q, "q", _FP8, rows, cols)
-    pt, st = _mat(qt, "qt", _FP8, cols, rows)
+    px, sx = _mat(x, "x", x.dtype, shape)
+    pr, sr = _mat(relu, "relu", x.dtype, shape)
+    pq, sq = _mat(q, "q", _FP8, shape)
+    pt, st = _mat(qt, "qt", _FP8, (cols, rows))
     _check("rs_quantize_fp8", lib().rs_quantize_fp8(
         rows, cols, code, px, sx, pr, sr, pq, sq, _scales(scales, "scales", _blocks(cols), rows), pt, st,
         _scales(scales_t, "scales_t", _blocks(rows), cols), _stream(stream)))
@@ -816,11 +820,11 @@ def rs_quantize_fp8(x, q=None, scales=None, qt=None, scales_t=None, relu=None, s
 def rs_quantize_fp8_blocks(x, q=None, scales=None, qt=None, scales_t=None, stream=None):
     """As rs_quantize_fp8 with one scale per 128 x 128 block: scales [ceil(cols / 128), ceil(rows / 128)], scales_t its
     transpose."""
-    rows, cols = x.shape
+    shape = rows, cols = x.shape
     code = _dtype(x, "x")
-    px, sx = _mat(x, "x", x.dtype, rows, cols)
-    pq, sq = _mat(q, "q", _FP8, rows, cols)
-    pt, st = _mat(qt, "qt", _FP8, cols, rows)
+    px, sx = _mat(x, "x", x.dtype, shape)
+    pq, sq = _mat(q, "q", _FP8, shape)
+    pt, st = _mat(qt, "qt", _FP8, (cols, rows))
     _check("rs_quantize_fp8_blocks", lib().rs_quantize_fp8_blocks(
         rows, cols, code, px, sx, pq, sq, _scales(scales, "scales", _blocks(cols), _blocks(rows)), pt, st,
         _scales(scales_t, "scales_t", _blocks(rows), _blocks(cols)), _stream(stream)))
@@ -836,9 +840,9 @@ def rs_matmul_fp8(a, a_scales, b, b_scales, out, workspace=None, relu: bool = Fa
     m, k = a.shape
     n = b.shape[0]
     kb = _blocks(k)
-    pa, sa = _mat(a, "a", _FP8, m, k)
-    pb, sb = _mat(b, "b", _FP8, n, k)
-    po, so = _mat(out, "out", out.dtype, m, n)
+    pa, sa = _mat(a, "a", _FP8, (m, k))
+    pb, sb = _mat(b, "b", _FP8, (n, k))
+    po, so = _mat(out, "out", out.dtype, (m, n))
     per_row = b_scales.shape == (kb, n)
     _check("rs_matmul_fp8", lib().rs_matmul_fp8(
         m, n, k, pa, sa, _scales(a_scales, "a_scales", kb, m), pb, sb,
