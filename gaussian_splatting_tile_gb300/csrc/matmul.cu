@@ -38,8 +38,8 @@ __device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
 __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint64_t* b) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+__device__ __forceinline__ void bar_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Arrival at a barrier of another CTA of the cluster (address from cluster_addr).  It says that tensor memory has been
 // read, nothing that this thread has stored: a release at the cluster's scope would wait for all of the thread's memory
@@ -234,12 +234,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
     __shared__ uint32_t tmem_slot;
-    // A warp's scales of four blocks: a's, one a row, then b's, one a column (ROWS) or the same one for every lane.
-    __shared__ __align__(16) float scales[kSumWarps][4][32 + (ROWS ? kCols : 32)];
+    // The scales of kRing blocks: a's of the CTA's rows, then b's of the tile's columns (ROWS) or of its halves.
+    constexpr int kRing = 8, kScales = 128 + (ROWS ? BN : 4);
+    __shared__ __align__(16) float scales[kRing][kScales];
+    __shared__ uint64_t sc_full[kRing], sc_empty[kRing];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
         for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 2 * kSumWarps);
+        for (int i = 0; i < kRing; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -303,54 +306,64 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                 }
             }
             if (!ok && it > 0) bar_wait(&acc_full[(it - 1) % kAcc], (it - 1) / kAcc & 1);  // products in flight
+        } else if (warp == 2) {
+            // The scales, up to kRing blocks ahead of their use and on into the next tiles: a load takes longer than a block.
+            // Rows and columns outside the matrices take the last one's: what comes of them is not stored.
+            const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;  // b's scales a block
+            uint32_t slot = 0, phase = 1;
+            bool ok = true;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const int tile = u % g.tiles, x = tile % g.tiles_n * BN;
+                const long long y = (long long)(tile / g.tiles_n * 2 + rank) * 128 + lane;
+                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                const float* pa = g.sa + size_t(r.first) * g.m;
+                const float* pb = g.sb + size_t(r.first) * per;
+                for (int b = r.first; b < r.last; ++b, pa += g.m, pb += per) {
+                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&sc_empty[slot], phase)))) break;
+                    float* to = scales[slot];
+#pragma unroll
+                    for (int i = 0; i < 128; i += 32) copy4(to + i + lane, pa + min(y + i, (long long)g.m - 1));
+                    if (ROWS) {
+#pragma unroll
+                        for (int i = 0; i < BN; i += 32) copy4(to + 128 + i + lane, pb + min(x + i + lane, per - 1));
+                    } else if (lane < 2) {
+                        copy4(to + 128 + lane, pb + min((x + lane * kCols) / kBlock, per - 1));
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[slot])) : "memory");
+                    if (++slot == kRing) slot = 0, phase ^= 1;
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsMany));
         const int w8 = warp - 4, half = w8 >> 2, wrow = (w8 & 3) * 32;   // columns and rows of the tile
         const uint32_t lanes = tmem + (uint32_t(wrow) << 16) + half * kCols;
-        const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;             // b's scales a block
         const uint32_t full0 = smem_u32(acc_full), empty0 = cluster_addr(acc_empty, 0);
-        uint32_t h = 0, phase = 0;  // the accumulator to read next
-        int passes = 0;             // of results through the two buffers
+        const uint32_t sc_full0 = smem_u32(sc_full), sc_empty0 = smem_u32(sc_empty);
+        uint32_t h = 0, phase = 0;         // the accumulator to read next
+        uint32_t slot = 0, sc_phase = 0;   // and the scales
         bool ok = true;
         for (int u = pair; u < units; u += pairs) {
             const int tile = u % g.tiles;
             const long long row0 = (long long)(tile / g.tiles_n * 2 + rank) * 128 + wrow;
             const int col = tile % g.tiles_n * BN + half * kCols;
             const Range r = split_blocks(blocks, g.splits, u / g.tiles);
-            // The scales are copied to shared memory three blocks ahead (a load from L2 takes longer than a block).  Rows and
-            // columns outside the matrices take the last one's: what comes of them is not stored.
-            const int count = r.last - r.first;
-            const float* pa = g.sa + size_t(r.first) * g.m + min(row0 + lane, (long long)g.m - 1);
-            const float* pb = g.sb + size_t(r.first) * per;
-            float (*sc)[32 + (ROWS ? kCols : 32)] = scales[w8];
-            auto copy_scales = [&](int b) {  // of the stretch's block b, if there is one
-                if (b < count) {
-                    copy4(&sc[b & 3][lane], pa + size_t(b) * g.m);
-                    if (ROWS) {
-#pragma unroll
-                        for (int i = 0; i < kCols; i += 32)
-                            copy4(&sc[b & 3][32 + i + lane], pb + size_t(b) * per + min(col + i + lane, per - 1));
-                    } else {
-                        copy4(&sc[b & 3][32 + lane], pb + size_t(b) * per + min(col / kBlock, per - 1));
-                    }
-                }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-            };
-            __syncwarp();  // every lane is done with the last tile's scales
-#pragma unroll
-            for (int i = 0; i < 3; ++i) copy_scales(i);
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
-            for (int b = 0; b < count; ++b) {
-                asm volatile("cp.async.wait_group 2;" ::: "memory");
-                __syncwarp();  // all lanes' copies; and every lane is done with block b - 1, whose place block b + 3 takes
-                const float f = ROWS ? sc[b & 3][lane] : sc[b & 3][lane] * sc[b & 3][32 + lane];
-                const uint64_t ff = pack2(f, f);
-                copy_scales(b + 3);
+            for (int b = r.first; b < r.last; ++b) {
                 // a wait that gave up ends the waiting, not the loop: what is added from then on is not stored
+                ok = ok && __all_sync(0xffffffffu, bar_wait(sc_full0 + slot * 8, sc_phase));
+                const float* sc = scales[slot];
+                const float* sb = sc + 128 + (ROWS ? half * kCols : half);
+                const float f = ROWS ? sc[wrow + lane] : sc[wrow + lane] * sb[0];
+                const uint64_t ff = pack2(f, f);
+                if (!ROWS) {
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(sc_empty0 + slot * 8);
+                }
                 ok = ok && __all_sync(0xffffffffu, bar_wait(full0 + h * 8, phase));
                 tc_after();
                 uint32_t v[2][16];
@@ -369,7 +382,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                     for (int j = 0; j < 16; j += 4) {
                         uint64_t p = pack2(v[c & 1][j], v[c & 1][j + 1]), q = pack2(v[c & 1][j + 2], v[c & 1][j + 3]);
                         if (ROWS) {
-                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(&sc[b & 3][32 + 16 * c + j]);
+                            const ulonglong2 s4 = *reinterpret_cast<const ulonglong2*>(sb + 16 * c + j);
                             p = mul2(p, s4.x);
                             q = mul2(q, s4.y);
                         }
@@ -377,6 +390,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                         acc[8 * c + j / 2 + 1] = fma2(q, ff, acc[8 * c + j / 2 + 1]);
                     }
                 }
+                if (ROWS) {
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(sc_empty0 + slot * 8);
+                }
+                if (++slot == kRing) slot = 0, sc_phase ^= 1;
                 if (++h == kAcc) h = 0, phase ^= 1;
             }
             if (!ok) break;
@@ -389,37 +407,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                     o[size_t(2 * j + 1) * 128] = x.y;
                 }
             } else if (col < g.n) {
-                constexpr int kOnce = 128 / sizeof(T);  // columns a pass
-                static_assert(kCols % (2 * kOnce) == 0 || kCols == kOnce, "passes take the two buffers in turn");
+                // Passes of 128 bytes a row, two to a fence (half of the way out's time was the fence).
+                constexpr int kOnce = 128 / sizeof(T), kPasses = kCols / kOnce, kTogether = kPasses < 2 ? kPasses : 2;
 #pragma unroll
-                for (int c = 0; c < kCols; c += kOnce) {
-                    uint4 w[8];
-                    uint32_t* ww = reinterpret_cast<uint32_t*>(w);
+                for (int c = 0; c < kPasses; c += kTogether) {
+                    // what was copied out of the buffers before has left them
+                    if (g.vec && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
 #pragma unroll
-                    for (int j = 0; j < kOnce; j += 2) {
-                        float2 x = unpack2(acc[(c + j) / 2]);
-                        if (g.relu) x = make_float2(relu(x.x), relu(x.y));
-                        if constexpr (sizeof(T) == 4) ww[j] = __float_as_uint(x.x), ww[j + 1] = __float_as_uint(x.y);
-                        else ww[j / 2] = pack_pair(x.x, x.y, T());
-                    }
-                    uint8_t* st = sm.stage[w8][passes++ & 1];
-                    if (g.vec) {
-                        // the copy before the last has left this buffer; the last may still run
-                        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        __syncwarp();
-                        stage_rows(st, w, lane);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (row0 < g.m && col + c < g.n) tma_store(&map_out, st, col + c, int(row0));
-                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");  // one a pass, for the wait above
+                    for (int q = 0; q < kTogether; ++q) {
+                        uint4 w[8];
+                        uint32_t* ww = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+                        for (int j = 0; j < kOnce; j += 2) {
+                            float2 x = unpack2(acc[((c + q) * kOnce + j) / 2]);
+                            if (g.relu) x = make_float2(relu(x.x), relu(x.y));
+                            if constexpr (sizeof(T) == 4) ww[j] = __float_as_uint(x.x), ww[j + 1] = __float_as_uint(x.y);
+                            else ww[j / 2] = pack_pair(x.x, x.y, T());
                         }
-                    } else {
-                        __syncwarp();
-                        stage_rows(st, w, lane);
-                        __syncwarp();
-                        copy_rows(st, static_cast<T*>(g.out) + row0 * g.os + col + c, g.os, g.m - row0, g.n - col - c, lane);
+                        stage_rows(sm.stage[w8][q], w, lane);
                     }
+                    if (g.vec) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int q = 0; q < kTogether; ++q) {
+                        const int x = col + (c + q) * kOnce;
+                        if (!g.vec)
+                            copy_rows(sm.stage[w8][q], static_cast<T*>(g.out) + row0 * g.os + x, g.os, g.m - row0, g.n - x, lane);
+                        else if (lane == 0 && row0 < g.m && x < g.n)
+                            tma_store(&map_out, sm.stage[w8][q], x, int(row0));
+                    }
+                    if (g.vec && lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
         }
@@ -540,7 +558,7 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
             }
             tc_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&acc_empty[h]);
+            if (lane == 0) bar_arrive(smem_u32(&acc_empty[h]));
         }
     }
     const int n = n0 + wrow;
