@@ -184,8 +184,8 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d:
 
 def _stream(stream):
     if stream is None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t, dtype=None, numel=None, name="tensor"):
@@ -331,7 +331,7 @@ def set_camera_struct(c: rs_camera, cam) -> rs_camera:
 
 
 def stream_handle(stream=None):
-    return _stream(stream)
+    return ctypes.c_void_p(_stream(stream))
 
 
 # ------------------------------------------------------------------ the five calls
@@ -702,7 +702,7 @@ def rs_l1_dssim_loss_grad(image: torch.Tensor, target: torch.Tensor, lam: float,
 RS_F32, RS_F16, RS_BF16 = 0, 1, 2
 RS_FP8_BLOCK, RS_NORM_MAX_COLS = 128, 16384
 _DTYPES = {torch.float32: RS_F32, torch.float16: RS_F16, torch.bfloat16: RS_BF16}
-_FP8 = (torch.float8_e4m3fn, torch.uint8)
+_FP8 = torch.float8_e4m3fn  # or the bytes as uint8
 
 
 def _dtype(t, name="tensor") -> int:
@@ -717,11 +717,12 @@ def _mat(t, name, dtype, shape):
     if t is None:
         return None, 0
     # the common case in one line: these checks are most of a small call's time
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and shape[0] > 1:
-        return t.data_ptr(), shape[1]
+    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        # a single row's stride is never followed: give one that the alignment rules allow
+        return t.data_ptr(), (shape[1] if shape[0] > 1 else (shape[1] + 15) // 16 * 16)
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype is not dtype and (dtype is not _FP8 or t.dtype not in _FP8):
+    if t.dtype is not dtype and not (dtype is _FP8 and t.dtype is torch.uint8):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, needs {tuple(shape)}")
@@ -729,7 +730,6 @@ def _mat(t, name, dtype, shape):
     rows, cols = shape
     if s1 != 1 and cols > 1:
         raise ValueError(f"{name} must be contiguous along its rows")
-    # a single row's stride is never followed: give one that the alignment rules allow
     return t.data_ptr(), (s0 if rows > 1 else (cols + 15) // 16 * 16)
 
 
@@ -757,10 +757,9 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
 
 
 def _scales(t, name, blocks: int, rows: int):
-    p = _vec(t, torch.float32, 0, name)
     if t is not None and t.shape != (blocks, rows):
         raise ValueError(f"{name} is {tuple(t.shape)}, needs {(blocks, rows)}")
-    return p
+    return _vec(t, torch.float32, 0, name)
 
 
 def _blocks(n: int) -> int:
