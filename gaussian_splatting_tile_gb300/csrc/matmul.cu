@@ -208,11 +208,14 @@ __device__ __forceinline__ void stage_rows(uint8_t* st, const uint4 (&w)[8], int
 #pragma unroll
     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = w[i];
 }
-// From there to rows of out that TMA cannot write (not on 16-byte boundaries), one value a lane.
+// From there to rows of out that TMA cannot write (not on 16-byte boundaries), one value a lane: two stores of 64 bytes a row
+// of 16-bit values.  (Words put together from neighbours, a store fewer, took 1.6 times as long.)
 template <typename T>
 __device__ __forceinline__ void copy_rows(const uint8_t* st, T* o, size_t os, long long rows, int cols, int lane) {
     constexpr int kPer = 16 / sizeof(T);
-    for (int r = 0; r < 32 && r < rows; ++r)
+    const int n = int(min(rows, 32LL));
+#pragma unroll 4
+    for (int r = 0; r < n; ++r)
 #pragma unroll
         for (int c = lane; c < 8 * kPer; c += 32)
             if (c < cols)

@@ -54,10 +54,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
         const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
-        load8<T, VEC>(x + c, left, v[i]);
+        load8<T, VEC>(x + c, left, v[i], c > 0);
         if (r) {
             float u[8];
-            load8<T, VEC>(r + c, left, u);
+            load8<T, VEC>(r + c, left, u, c > 0);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[i][j] += u[j];
         }
@@ -158,9 +158,9 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdA
 #pragma unroll
         for (int i = 0; i < RUNS; ++i) {
             const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
-            sv[i].template load<VEC>(s + c, left);
-            gv[i].template load<VEC>(dy + c, left);
-            if (ds) dv[i].template load<VEC>(ds + c, left);
+            sv[i].template load<VEC>(s + c, left, c > 0);
+            gv[i].template load<VEC>(dy + c, left, c > 0);
+            if (ds) dv[i].template load<VEC>(ds + c, left, c > 0);
         }
         float dot = 0.f;
 #pragma unroll

@@ -76,14 +76,14 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ?
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool in = r + i < a.rows;
-        v[i].template load<VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
+        v[i].template load<VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0, c > 0);
     }
     if constexpr (FORM == kRowsColsRelu) {
         Run8<T> u[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const bool in = r + i < a.rows;
-            u[i].template load<VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0);
+            u[i].template load<VEC>(static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0, c > 0);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i].mask(u[i]);

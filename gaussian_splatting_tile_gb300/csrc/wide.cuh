@@ -23,14 +23,15 @@ template <> __device__ __forceinline__ __half from_f<__half>(float x) { return _
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
 // Eight consecutive values as they are stored, of which the first `left` exist (the others read as zero).  VEC: the place
-// is aligned to 16 bytes, and a whole run is one or two 16-byte accesses.  16-bit types stay packed in four registers, where a maximum of
+// is aligned to 16 bytes, and a whole run is one or two 16-byte accesses; else a run of 16-bit values is read as aligned
+// words where its neighbours on both sides exist (`inner`).  16-bit types stay packed in four registers, where a maximum of
 // magnitudes is exact, and are widened where they are used.
 template <typename T>
 struct Run8 {
     float v[8];
     __device__ __forceinline__ float2 pair(int p) const { return make_float2(v[2 * p], v[2 * p + 1]); }
     template <bool VEC>
-    __device__ __forceinline__ void load(const T* p, int left) {
+    __device__ __forceinline__ void load(const T* p, int left, bool = false) {
         if (VEC && left >= 8) {
             const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
@@ -64,9 +65,16 @@ struct PackedRun8 {
         return make_float2(to_f(h.x), to_f(h.y));
     }
     template <bool VEC>
-    __device__ __forceinline__ void load(const T* p, int left) {
+    __device__ __forceinline__ void load(const T* p, int left, bool inner = false) {
         if (VEC && left >= 8) {
             w = *reinterpret_cast<const uint4*>(p);
+        } else if (inner && left > 8) {
+            // five aligned words hold the run; half a word too many where it starts on one
+            const uint32_t shift = reinterpret_cast<uintptr_t>(p) & 2 ? 16 : 0;
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+            const uint32_t a = q[0], b = q[1], c = q[2], d = q[3], e = shift ? q[4] : 0u;
+            w = make_uint4(__funnelshift_r(a, b, shift), __funnelshift_r(b, c, shift), __funnelshift_r(c, d, shift),
+                           __funnelshift_r(d, e, shift));
         } else {
             const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
             uint32_t h[8];
@@ -101,9 +109,9 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // The same as floats.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, int left, float (&v)[8], bool inner = false) {
     Run8<T> r;
-    r.template load<VEC>(p, left);
+    r.template load<VEC>(p, left, inner);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 w = r.pair(i);
@@ -132,6 +140,21 @@ __device__ __forceinline__ void store8(T* p, int left, const float (&v)[8]) {
                                                       pack_pair(v[4], v[5], T()), pack_pair(v[6], v[7], T()));
         }
         return;
+    }
+    if constexpr (!VEC && sizeof(T) == 2) {
+        if (left >= 8) {  // whole words, with one value before and one after them where the run does not start on one
+            uint32_t* q = reinterpret_cast<uint32_t*>((reinterpret_cast<uintptr_t>(p) + 3) & ~uintptr_t(3));
+            if (reinterpret_cast<uintptr_t>(p) & 2) {
+                p[0] = from_f<T>(v[0]);
+#pragma unroll
+                for (int i = 0; i < 3; ++i) q[i] = pack_pair(v[2 * i + 1], v[2 * i + 2], T());
+                p[7] = from_f<T>(v[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = pack_pair(v[2 * i], v[2 * i + 1], T());
+            }
+            return;
+        }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
