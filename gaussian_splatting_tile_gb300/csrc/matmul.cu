@@ -455,14 +455,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
 }
 
 // ---------------------------------------------------------------- few rows
-// With at most 128 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
+// With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
 // (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that every SM
 // reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its CTAs' sums
 // through distributed shared memory, rank by rank, each CTA finishing some of the columns.
 template <int NT>
 struct RowsSmem {
-    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = NT == 128 ? 2 : 128 / NT, kMaxStages = NT == 128 ? 6 : 8;
-    static constexpr int kTmem = kAcc * NT;  // columns
+    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = 128 / NT, kMaxStages = 8, kTmem = 128;
 };
 
 template <typename T, int NT, bool ROWS>
@@ -632,22 +631,33 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
 
 // ---------------------------------------------------------------- host side
 struct Plan {
-    int rows;      // 16, 32, 64 or 128: few rows, that many columns of products; 0: the tile kernel
+    int rows;      // 16, 32 or 64: few rows, that many columns of products; 0: the tile kernel
     int bn, splits, tiles_n, tiles;
     size_t workspace() const { return rows == 0 && splits > 1 ? size_t(splits) * tiles * 2 * bn * 128 * sizeof(float) : 0; }
 };
 
+// Which kernel and which tiles.
+//  - Up to 64 rows the rows kernel (64 x 4096 x 4096: 10.4 us; at 128 rows it took 33.8 us and the tiles 15.2).
+//  - 256 columns a tile move the fewest bytes and cost the fewest instructions a product, but with few tiles and little work
+//    for each pair of SMs, 128 columns spread it further: 2000 x 1000 x 2000 (32 wide tiles, 7 blocks a pair) 11.7 against 16.5 us,
+//    1000 x 1000 x 3000 14.7 against 17.7; with more of either the other way, 4000 x 1000 x 700 (64 tiles) 10.9 against 9.4,
+//    2000 x 700 x 10000 (25 blocks a pair) 41.2 against 33.3.  With one or two wide tiles the split sums count: 512 x 256 x 160000
+//    45 against 50.
+//  - Fewer tiles than pairs: the blocks are split among them, at least 8 to a stretch (4: 256 x 256 x 20000 23 against 13 us).
 Plan plan_matmul(int m, int n, int k) {
     Plan p{};
     const int blocks = ceil_div(k, kBlock);
-    if (m <= 128) {
-        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
+    if (m <= 64) {
+        p.rows = m <= 16 ? 16 : m <= 32 ? 32 : 64;
         p.bn = 128;
         p.tiles_n = p.tiles = ceil_div(n, 128);
+        // every SM reads, two CTAs on each at most, at least two blocks to a CTA
         for (p.splits = 1; p.splits < 8 && p.tiles * p.splits * 2 <= 2 * kSms && blocks >= p.splits * 4;) p.splits *= 2;
         return p;
     }
-    p.bn = n > 128 ? 256 : 128;
+    const long long wide = (long long)ceil_div(m, 256) * ceil_div(n, 256);
+    const bool narrow = wide < kPairs / 2 && (wide * blocks <= 10 * kPairs || wide <= 2);
+    p.bn = n <= 128 || narrow ? 128 : 256;
     p.tiles_n = ceil_div(n, p.bn);
     const long long tiles = (long long)ceil_div(m, 256) * p.tiles_n;
     p.tiles = int(std::min<long long>(tiles, 0x7fffffff));
@@ -775,7 +785,6 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
         const bool per_row = b_scale_rows == 1;
         if (p.rows == 16) return per_row ? launch_rows<T, 16, true>(ma, mb, g, s) : launch_rows<T, 16, false>(ma, mb, g, s);
         if (p.rows == 32) return per_row ? launch_rows<T, 32, true>(ma, mb, g, s) : launch_rows<T, 32, false>(ma, mb, g, s);
-        if (p.rows == 128) return per_row ? launch_rows<T, 128, true>(ma, mb, g, s) : launch_rows<T, 128, false>(ma, mb, g, s);
         if (p.rows == 64) return per_row ? launch_rows<T, 64, true>(ma, mb, g, s) : launch_rows<T, 64, false>(ma, mb, g, s);
         if (p.bn == 256)
             return b_scale_rows == 1 ? launch_tile<T, 256, true>(ma, mb, g, s) : launch_tile<T, 256, false>(ma, mb, g, s);
