@@ -153,8 +153,7 @@ __global__ void __launch_bounds__(256) k_grad_scale(const __grid_constant__ Clip
     if (T.norm && blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
     const float c = clip_factor(T.max_norm, norm);
     const uint32_t chunks = T.start[T.n];
-    for (uint32_t from = blockIdx.x; from < chunks; from += gridDim.x) {
-        const uint32_t k = chunks - 1 - from;  // the norm's pass ended there: L2 still has it
+    for (uint32_t k = blockIdx.x; k < chunks; k += gridDim.x) {
         const int i = tensor_of(T, k);
         const rs_grad_tensor& d = T.t[i];
         if (!d.d_out || (c == 1.f && d.d_out == d.d_grad)) continue;

@@ -613,9 +613,10 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
     const float* p = g.part + (size_t(half) * bn + c0 + cc) * 128 + row;
     const size_t step = size_t(g.tiles) * 2 * bn * 128;
     float v[4] = {};
-    for (int s = 0; s < g.splits; ++s, p += step)
+#pragma unroll 4
+    for (int s = 0; s < g.splits; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += p[j * 128];
+        for (int j = 0; j < 4; ++j) v[j] += p[s * step + j * 128];
 #pragma unroll
     for (int j = 0; j < 4; ++j) sm[cc + j][row] = g.relu ? relu(v[j]) : v[j];
     __syncthreads();

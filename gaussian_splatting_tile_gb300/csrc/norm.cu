@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
     const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
     float v = 0.f;
     if (c < cols)
+#pragma unroll 8
         for (int i = g; i < n; i += 32) v += part[size_t(i) * cols + c];
     sm[g][threadIdx.x & 31] = v;
     __syncthreads();

@@ -220,19 +220,19 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// The gradient norm from its partial sums of squares, the same bits in every block; all 256 threads call it.
+// The gradient norm from its partial sums of squares, the same bits in every block; all 256 threads call it.  In float32: the
+// sums are positive and the chains short, and in float64 this alone took 27 us of a step over 59 M parameters.
 __device__ __forceinline__ float norm_of_parts(const float* part, int parts) {
-    __shared__ double sm[8];
-    double v = 0.0;
-    for (int i = threadIdx.x; i < parts; i += 256) v += double(part[i]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __shared__ float sm[8];
+    float v = 0.f;
+    for (int i = threadIdx.x; i < parts; i += 256) v += part[i];
+    v = group_sum<32>(v);
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0;
+    v = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v += sm[i];
-    return sqrtf(float(v));
+    return sqrtf(v);
 }
 
 // min(1, max_norm / (norm + 1e-6)), a NaN norm's NaN kept.
