@@ -1,12 +1,21 @@
 // Matrix product of two 8-bit matrices with a scale for each block of 128 along the contracted axis.
 //
-//   out[i][j] = sum_b sa[b][i] sb[b][j] sum_{t in block b} a[i][t] b[j][t]
+// out[i][j] = sum_b sa[b][i] sb[b][j] sum_{t in block b} a[i][t] b[j][t]
 //
 // The inner sums are e4m3 products on the tensor cores (tcgen05.mma kind::f8f6f4, operands staged in shared memory by
-// TMA, accumulators in tensor memory).  The scales change from block to block, so a block's 128 products are summed by
-// themselves in tensor memory and then added, scaled, to a float32 total that stays in the registers of the threads
-// that read it back: thread = row, so a's scale is one number a thread, and with a scale per 128 rows of b one number a
-// warp -- one fused multiply-add per value and block.
+// TMA, accumulators in tensor memory).  The scales change from block to block, so a block's 128 products are summed
+// by themselves in tensor memory and then added, scaled, to a float32 total that stays in the registers of the
+// threads that read it back: thread = row, so a's scale is one number a thread, and with a scale per 128 rows of b
+// one number a warp -- one fused multiply-add per value and block.  (With a scale for every row of b a multiplication
+// more.)
+//
+// What bounds it: 128 products take 256 x 256 outputs of two SMs about 490 clocks on the tensor cores; adding them up
+// takes each of their schedulers 8192 multiply-adds, 390 clocks at the rate that two warps reach.  The two overlap,
+// but each accumulator's way round (products, word to the readers, reading, word back) is longer than both, and there
+// is room for two: that is what large products wait for.  Products with few blocks are bound by the results' way out.
+// Measured: 65536 x 2048 x 2048 float16 out 257 us (2.1 PFLOP/s; without any adding up the same loads and products
+// would take 148), 8192^3 2.4 PFLOP/s, 160,000 x 512 x 512 bf16 64 us (3.9 TB/s; 37 at the copy's rate), dW of it
+// (512 x 256 x 160,000, a scale a row) 45 us, 1 x 4096 x 4096 10 us, the call itself.
 #include <cuda.h>
 
 #include "wide.cuh"
@@ -41,9 +50,9 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// Arrival at a barrier of another CTA of the cluster (address from cluster_addr).  It says that tensor memory has been
-// read, nothing that this thread has stored: a release at the cluster's scope would wait for all of the thread's memory
-// operations each time (measured: half the product's speed).
+// Arrival at a barrier of another CTA of the cluster (address from cluster_addr).  It says that tensor memory has
+// been read, nothing that this thread has stored: a release at the cluster's scope would wait for all of the thread's
+// memory operations each time (measured: half the product's speed).
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -58,7 +67,8 @@ __device__ __forceinline__ void cluster_sync() {
 }
 __device__ __forceinline__ bool bar_test(uint32_t addr, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}\n"
                  : "=r"(ok) : "r"(addr), "r"(parity) : "memory");
     return ok != 0;
 }
@@ -67,7 +77,8 @@ __device__ __forceinline__ bool bar_wait(uint32_t addr, uint32_t parity) {
     for (uint32_t i = 0; i < kWaitPolls; ++i) {
         uint32_t ok;
         asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n selp.u32 %0, 1, 0, p;\n}\n"
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n"
+            " selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok) : "r"(addr), "r"(parity) : "memory");
         if (ok) return true;
     }
@@ -79,18 +90,20 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity) { return 
 
 // A tile's corner (x: element along the row, y: row); x is a multiple of 128 bytes.
 __device__ __forceinline__ void tma_load(const CUtensorMap* map, void* dst, uint64_t* bar, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
 }
 
 // The same by one CTA of a pair, into its own memory, counted at a barrier of either (address from cluster_addr).
 __device__ __forceinline__ void tma_load_pair(const CUtensorMap* map, void* dst, uint32_t bar, int x, int y) {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
                  ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
-// Matrix descriptor of a K-major operand in 128-byte swizzled rows (PTX ISA "Matrix Descriptors"): address >> 4, groups of
-// eight rows 1024 bytes apart (bits 32-45), 0b001 at bits 46-48, 128-byte swizzle = 2 at bits 61-63.
+// Matrix descriptor of a K-major operand in 128-byte swizzled rows (PTX ISA "Matrix Descriptors"): address >> 4,
+// groups of eight rows 1024 bytes apart (bits 32-45), 0b001 at bits 46-48, 128-byte swizzle = 2 at bits 61-63.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(64) << 32) | (uint64_t(1) << 46) |
            (uint64_t(2) << 61);
@@ -98,26 +111,32 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t saddr) {
 
 // Instruction descriptor of kind::f8f6f4 with e4m3 operands (type 0), both K-major, float32 sums.
 template <int M, int N>
-__host__ __device__ constexpr uint32_t tc_idesc() { return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24); }
+__host__ __device__ constexpr uint32_t tc_idesc() {
+    return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
 
 __device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
 }
-// The same of a pair of CTAs: operands at the same places of both, the sums' upper 128 rows in the second's tensor memory.
+// The same of a pair of CTAs: operands at the same places of both, the sums' upper 128 rows in the second's tensor
+// memory.
 __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
                  ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u) : "memory");
 }
 __device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {  // arrives at both CTAs' barriers
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                  ::"r"(smem_u32(bar)), "h"(uint16_t(3)) : "memory");
 }
-// True in one lane of a converged warp.  The loops that feed the tensor cores run in all lanes and let one act: what they
-// compute is then the same in every lane by construction, as those instructions' operands have to be.
+// True in one lane of a converged warp.  The loops that feed the tensor cores run in all lanes and let one act: what
+// they compute is then the same in every lane by construction, as those instructions' operands have to be.
 __device__ __forceinline__ bool elect_one() {
     uint32_t r;
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -128,9 +147,10 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 
 // 16 columns of this warp's 32 lanes; the registers are valid after tc_wait.
 __device__ __forceinline__ void tc_ld16(uint32_t addr, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                   "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32"
+                 " {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(addr) : "memory");
 }
 __device__ __forceinline__ void tc_wait(uint32_t (&r)[16]) {
@@ -171,11 +191,17 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 
 // ---------------------------------------------------------------- the tile kernel
-// A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA holds
-// 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is fetched and
-// stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warps 4 to 19 of both add
-// the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a half of the columns.  Tensor memory holds
-// kAcc accumulators of BN columns: the products of the next blocks run while a block is read.
+// A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA
+// holds 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is
+// fetched and stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warp 2 of each
+// fetches the scales, warps 4 to 11 of both add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a
+// half of the columns. Tensor memory holds kAcc accumulators of BN columns: the products of the next blocks run while
+// a block is read.
+//
+// What was tried and not kept: single CTAs with 128 x 256 tiles (8192^3 476 against 431 us); sixteen warps adding up
+// 64 columns each, which do not fit the registers without moves (527 us); accumulators of 128 columns, twice as many
+// (65536 x 2048 x 2048 263 against 257 us, 160,000 x 512 x 512 66 against 68); looking at the next barrier early;
+// scalar multiply-adds instead of pairs (8192^3 472 against 459 us).
 constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPairs = kSms / 2;
@@ -203,13 +229,14 @@ __device__ __forceinline__ float relu(float x) {
     return r;
 }
 // A warp's 32 rows x 128 bytes of results (thread = row, eight 16-byte words) in shared memory, the words of row r at
-// word ^ (r mod 8): the 128-byte swizzle of the tensor map that takes them out, and no two of eight neighbours share a bank.
+// word ^ (r mod 8): the 128-byte swizzle of the tensor map that takes them out, and no two of eight neighbours share
+// a bank.
 __device__ __forceinline__ void stage_rows(uint8_t* st, const uint4 (&w)[8], int lane) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(st + lane * 128 + ((i ^ (lane & 7)) << 4)) = w[i];
 }
-// From there to rows of out that TMA cannot write (not on 16-byte boundaries), one value a lane: two stores of 64 bytes a row
-// of 16-bit values.  (Words put together from neighbours, a store fewer, took 1.6 times as long.)
+// From there to rows of out that TMA cannot write (not on 16-byte boundaries), one value a lane: two stores of 64
+// bytes a row of 16-bit values.  (Words put together from neighbours, a store fewer, took 1.6 times as long.)
 template <typename T>
 __device__ __forceinline__ void copy_rows(const uint8_t* st, T* o, size_t os, long long rows, int cols, int lane) {
     constexpr int kPer = 16 / sizeof(T);
@@ -219,7 +246,8 @@ __device__ __forceinline__ void copy_rows(const uint8_t* st, T* o, size_t os, lo
 #pragma unroll
         for (int c = lane; c < 8 * kPer; c += 32)
             if (c < cols)
-                o[r * os + c] = *reinterpret_cast<const T*>(st + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(T));
+                o[r * os + c] =
+                    *reinterpret_cast<const T*>(st + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(T));
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
@@ -227,9 +255,9 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
 }
 
 template <typename T, int BN, bool ROWS>
-__global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_constant__ CUtensorMap map_a,
-                                                                 const __grid_constant__ CUtensorMap map_b,
-                                                                 const __grid_constant__ CUtensorMap map_out, MatmulArgs g) {
+__global__ void __launch_bounds__(kTileThreads, 1)
+    k_matmul_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_out, MatmulArgs g) {
     RS_PDL_ENTER();
     using Smem = TileSmem<BN>;
     constexpr int kStages = Smem::kStages, kAcc = Smem::kAcc, kCols = BN / (kSumWarps / 4);
@@ -249,8 +277,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(512)
-                     : "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_before();
@@ -282,7 +310,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                 }
             }
             // no copy and no arrival may outlast the CTA: a stage's products follow its copies
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) bar_wait(&empty[i % kStages], i / kStages & 1);
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                bar_wait(&empty[i % kStages], i / kStages & 1);
         } else if (warp == 1 && rank == 0) {
             const uint64_t da0 = tc_desc(smem_u32(sm.a[0])), db0 = tc_desc(smem_u32(sm.b[0]));
             uint32_t s = 0, phase = 0, h = 0, acc_phase = 1, it = 0;
@@ -310,8 +339,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
             }
             if (!ok && it > 0) bar_wait(&acc_full[(it - 1) % kAcc], (it - 1) / kAcc & 1);  // products in flight
         } else if (warp == 2) {
-            // The scales, up to kRing blocks ahead of their use and on into the next tiles: a load takes longer than a block.
-            // Rows and columns outside the matrices take the last one's: what comes of them is not stored.
+            // The scales, up to kRing blocks ahead of their use and on into the next tiles: a load takes longer than
+            // a block. Rows and columns outside the matrices take the last one's: what comes of them is not stored.
             const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;  // b's scales a block
             uint32_t slot = 0, phase = 1;
             bool ok = true;
@@ -332,7 +361,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                     } else if (lane < 2) {
                         copy4(to + 128 + lane, pb + min((x + lane * kCols) / kBlock, per - 1));
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[slot])) : "memory");
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[slot]))
+                                 : "memory");
                     if (++slot == kRing) slot = 0, phase ^= 1;
                 }
             }
@@ -425,8 +455,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                         for (int j = 0; j < kOnce; j += 2) {
                             float2 x = unpack2(acc[((c + q) * kOnce + j) / 2]);
                             if (g.relu) x = make_float2(relu(x.x), relu(x.y));
-                            if constexpr (sizeof(T) == 4) ww[j] = __float_as_uint(x.x), ww[j + 1] = __float_as_uint(x.y);
-                            else ww[j / 2] = pack_pair(x.x, x.y, T());
+                            if constexpr (sizeof(T) == 4) {
+                                ww[j] = __float_as_uint(x.x);
+                                ww[j + 1] = __float_as_uint(x.y);
+                            } else {
+                                ww[j / 2] = pack_pair(x.x, x.y, T());
+                            }
                         }
                         stage_rows(sm.stage[w8][q], w, lane);
                     }
@@ -436,7 +470,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
                     for (int q = 0; q < kTogether; ++q) {
                         const int x = col + (c + q) * kOnce;
                         if (!g.vec)
-                            copy_rows(sm.stage[w8][q], static_cast<T*>(g.out) + row0 * g.os + x, g.os, g.m - row0, g.n - x, lane);
+                            copy_rows(sm.stage[w8][q], static_cast<T*>(g.out) + row0 * g.os + x, g.os, g.m - row0,
+                                      g.n - x, lane);
                         else if (lane == 0 && row0 < g.m && x < g.n)
                             tma_store(&map_out, sm.stage[w8][q], x, int(row0));
                     }
@@ -451,22 +486,26 @@ __global__ void __launch_bounds__(kTileThreads, 1) k_matmul_tile(const __grid_co
     __syncthreads();
     cluster_sync();  // neither CTA's memory goes while the other's products or arrivals use it
     tc_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
 // ---------------------------------------------------------------- few rows
-// With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are rows of b
-// (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that every SM
-// reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its CTAs' sums
-// through distributed shared memory, rank by rank, each CTA finishing some of the columns.
+// With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are
+// rows of b (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that
+// every SM reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its
+// CTAs' sums through distributed shared memory, rank by rank, each CTA finishing some of the columns.
+constexpr int kRowsTmem = 128;  // columns of tensor memory
+
 template <int NT>
 struct RowsSmem {
-    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = 128 / NT, kMaxStages = 8, kTmem = 128;
+    static constexpr int kStage = 128 * 128 + NT * 128, kAcc = kRowsTmem / NT, kMaxStages = 8;
 };
 
 template <typename T, int NT, bool ROWS>
-__global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUtensorMap map_a,
-                                                     const __grid_constant__ CUtensorMap map_b, MatmulArgs g, int stages) {
+__global__ void __launch_bounds__(192)
+    k_matmul_rows(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, MatmulArgs g,
+                  int stages) {
     RS_PDL_ENTER();
     constexpr int kStage = RowsSmem<NT>::kStage, kAcc = RowsSmem<NT>::kAcc, kMax = RowsSmem<NT>::kMaxStages;
     extern __shared__ uint8_t raw[];
@@ -482,8 +521,8 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(RowsSmem<NT>::kTmem)
-                     : "memory");
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(kRowsTmem) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     tc_before();
@@ -516,7 +555,8 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
                 const int s = it % stages, h = it % kAcc;
                 if (!(ok = bar_wait(&full[s], it / stages & 1) && bar_wait(&acc_empty[h], (it / kAcc & 1) ^ 1))) break;
                 tc_after();
-                const uint64_t da = tc_desc(smem_u32(ops + s * kStage)), db = tc_desc(smem_u32(ops + s * kStage + 128 * 128));
+                const uint32_t at = smem_u32(ops + s * kStage);
+                const uint64_t da = tc_desc(at), db = tc_desc(at + 128 * 128);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) tc_mma(tmem + h * NT, da + 2 * t, db + 2 * t, tc_idesc<128, NT>(), t > 0);
                 tc_commit(&empty[s]);
@@ -556,7 +596,8 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
                 tc_ld16(lanes + h * NT + 16 * c, v);
                 tc_wait(v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) acc[16 * c + j] = fmaf(__uint_as_float(v[j]) * sa[16 * c + j], f, acc[16 * c + j]);
+                for (int j = 0; j < 16; ++j)
+                    acc[16 * c + j] = fmaf(__uint_as_float(v[j]) * sa[16 * c + j], f, acc[16 * c + j]);
             }
             tc_before();
             __syncwarp();
@@ -588,7 +629,8 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
                 float v = 0.f;
                 for (int s = 0; s < g.splits; ++s) {
                     float x;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr(red + j * 128 + wrow, s)) : "memory");
+                    const uint32_t there = cluster_addr(red + j * 128 + wrow, s);
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
                     v += x;
                 }
                 store(j, v);
@@ -599,11 +641,12 @@ __global__ void __launch_bounds__(192) k_matmul_rows(const __grid_constant__ CUt
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(RowsSmem<NT>::kTmem) : "memory");
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kRowsTmem) : "memory");
 }
 
-// out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row reads
-// 128 consecutive floats a warp group, and the values leave through shared memory along out's rows.
+// out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row
+// reads 128 consecutive floats a warp group, and the values leave through shared memory along out's rows.
 template <typename T>
 __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
     RS_PDL_ENTER();
@@ -634,17 +677,20 @@ __global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
 struct Plan {
     int rows;      // 16, 32 or 64: few rows, that many columns of products; 0: the tile kernel
     int bn, splits, tiles_n, tiles;
-    size_t workspace() const { return rows == 0 && splits > 1 ? size_t(splits) * tiles * 2 * bn * 128 * sizeof(float) : 0; }
+    size_t workspace() const {
+        return rows == 0 && splits > 1 ? size_t(splits) * tiles * 2 * bn * 128 * sizeof(float) : 0;
+    }
 };
 
 // Which kernel and which tiles.
 //  - Up to 64 rows the rows kernel (64 x 4096 x 4096: 10.4 us; at 128 rows it took 33.8 us and the tiles 15.2).
-//  - 256 columns a tile move the fewest bytes and cost the fewest instructions a product, but with few tiles and little work
-//    for each pair of SMs, 128 columns spread it further: 2000 x 1000 x 2000 (32 wide tiles, 7 blocks a pair) 11.7 against 16.5 us,
-//    1000 x 1000 x 3000 14.7 against 17.7; with more of either the other way, 4000 x 1000 x 700 (64 tiles) 10.9 against 9.4,
-//    2000 x 700 x 10000 (25 blocks a pair) 41.2 against 33.3.  With one or two wide tiles the split sums count: 512 x 256 x 160000
-//    45 against 50.
-//  - Fewer tiles than pairs: the blocks are split among them, at least 8 to a stretch (4: 256 x 256 x 20000 23 against 13 us).
+//  - 256 columns a tile move the fewest bytes and cost the fewest instructions a product, but with few tiles and
+//    little work for each pair of SMs, 128 columns spread it further: 2000 x 1000 x 2000 (32 wide tiles, 7 blocks a
+//    pair) 11.7 against 16.5 us, 1000 x 1000 x 3000 14.7 against 17.7; with more of either the other way, 4000 x 1000
+//    x 700 (64 tiles) 10.9 against 9.4, 2000 x 700 x 10000 (25 blocks a pair) 41.2 against 33.3.  With one or two
+//    wide tiles the split sums count: 512 x 256 x 160000 45 against 50.
+//  - Fewer tiles than pairs: the blocks are split among them, at least 8 to a stretch (4: 256 x 256 x 20000 23
+//    against 13 us).
 Plan plan_matmul(int m, int n, int k) {
     Plan p{};
     const int blocks = ceil_div(k, kBlock);
@@ -671,17 +717,18 @@ EncodeTiled encode_tiled() {
     static const EncodeTiled f = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
+        const char* name = "cuTensorMapEncodeTiled";
+        const cudaError_t e = cudaGetDriverEntryPointByVersion(name, &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess) p = nullptr;
         return reinterpret_cast<EncodeTiled>(p);
     }();
     return f;
 }
 
-// A [rows][cols] matrix, moved in boxes of 128 bytes of a row and `box` rows; what lies outside reads as zero and is not
-// written.
-bool encode(CUtensorMap* map, CUtensorMapDataType type, size_t size, const void* p, size_t stride, int rows, int cols, int box) {
+// A [rows][cols] matrix, moved in boxes of 128 bytes of a row and `box` rows; what lies outside reads as zero and is
+// not written.
+bool encode(CUtensorMap* map, CUtensorMapDataType type, size_t size, const void* p, size_t stride, int rows, int cols,
+            int box) {
     const EncodeTiled f = encode_tiled();
     if (!f) return false;
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)}, strides[1] = {cuuint64_t(stride * size)};
@@ -693,8 +740,8 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, size_t size, const void*
 
 // With programmatic stream serialization, in clusters of `cluster` CTAs.
 template <typename... Params, typename... Args>
-cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned grid, unsigned block, int smem, cudaStream_t s,
-                            Args&&... args) {
+cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned grid, unsigned block, int smem,
+                            cudaStream_t s, Args&&... args) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -716,7 +763,8 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned gri
 template <typename T, int BN, bool ROWS>
 cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
     CUtensorMap out{};
-    constexpr CUtensorMapDataType type = sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    constexpr CUtensorMapDataType type =
+        sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     if (g.vec && g.splits == 1 && !encode(&out, type, sizeof(T), g.out, g.os, g.m, g.n, 32)) return cudaErrorUnknown;
     constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
     // the kernel's register split counts on what it is launched with
@@ -725,7 +773,8 @@ cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Matmul
         return cudaFuncGetAttributes(&f, k_matmul_tile<T, BN, ROWS>) == cudaSuccess && f.numRegs >= kRegsLaunch;
     }();
     if (!enough) return cudaErrorInvalidConfiguration;
-    return launch_clusters(k_matmul_tile<T, BN, ROWS>, 2, 2u * std::min(kPairs, g.tiles * g.splits), kTileThreads, smem, s, a, b, out, g);
+    const unsigned grid = 2u * std::min(kPairs, g.tiles * g.splits);
+    return launch_clusters(k_matmul_tile<T, BN, ROWS>, 2, grid, kTileThreads, smem, s, a, b, out, g);
 }
 
 template <typename T, int NT, bool ROWS>
@@ -733,7 +782,8 @@ cudaError_t launch_rows(const CUtensorMap& a, const CUtensorMap& b, const Matmul
     using Smem = RowsSmem<NT>;
     const int per = ceil_div(ceil_div(g.k, kBlock), g.splits), stages = std::min(per, Smem::kMaxStages);
     const int smem = std::max(stages * Smem::kStage, NT * 128 * 4) + 1024;
-    return launch_clusters(k_matmul_rows<T, NT, ROWS>, g.splits, unsigned(g.tiles) * g.splits, 192, smem, s, a, b, g, stages);
+    const unsigned grid = unsigned(g.tiles) * g.splits;
+    return launch_clusters(k_matmul_rows<T, NT, ROWS>, g.splits, grid, 192, smem, s, a, b, g, stages);
 }
 
 }  // namespace
@@ -778,18 +828,22 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     if (workspace_bytes < need) return RS_ERR_WORKSPACE;
     CUtensorMap ma, mb;
     constexpr CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    if (!encode(&ma, bytes, 1, d_a, a_stride, m, k, p.rows ? p.rows : 128) || !encode(&mb, bytes, 1, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2)) return RS_ERR_CUDA;
-    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40),
+    if (!encode(&ma, bytes, 1, d_a, a_stride, m, k, p.rows ? p.rows : 128) ||
+        !encode(&mb, bytes, 1, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2))
+        return RS_ERR_CUDA;
+    const bool vec = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40);
+    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, vec,
                  p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
         const bool per_row = b_scale_rows == 1;
-        if (p.rows == 16) return per_row ? launch_rows<T, 16, true>(ma, mb, g, s) : launch_rows<T, 16, false>(ma, mb, g, s);
-        if (p.rows == 32) return per_row ? launch_rows<T, 32, true>(ma, mb, g, s) : launch_rows<T, 32, false>(ma, mb, g, s);
-        if (p.rows == 64) return per_row ? launch_rows<T, 64, true>(ma, mb, g, s) : launch_rows<T, 64, false>(ma, mb, g, s);
+        const auto launch = [&](auto rows, auto blocks) { return per_row ? rows(ma, mb, g, s) : blocks(ma, mb, g, s); };
+        if (p.rows == 16) return launch(launch_rows<T, 16, true>, launch_rows<T, 16, false>);
+        if (p.rows == 32) return launch(launch_rows<T, 32, true>, launch_rows<T, 32, false>);
+        if (p.rows == 64) return launch(launch_rows<T, 64, true>, launch_rows<T, 64, false>);
         if (p.bn == 256)
-            return b_scale_rows == 1 ? launch_tile<T, 256, true>(ma, mb, g, s) : launch_tile<T, 256, false>(ma, mb, g, s);
-        return b_scale_rows == 1 ? launch_tile<T, 128, true>(ma, mb, g, s) : launch_tile<T, 128, false>(ma, mb, g, s);
+            return launch(launch_tile<T, 256, true>, launch_tile<T, 256, false>);
+        return launch(launch_tile<T, 128, true>, launch_tile<T, 128, false>);
     });
     if (e == cudaSuccess && need > 0)
         e = with_dtype(out_dtype, [&](auto v) {

@@ -44,10 +44,10 @@ __device__ __forceinline__ float adam_one(const AdamTable& T, int act, float lr,
     return act == RS_ACT_EXP ? expf(p) : act == RS_ACT_SIGMOID ? 1.0f / (1.0f + expf(-p)) : p;
 }
 
-// CLIP: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by itself
-// (a few KB in L2; a launch fewer than a kernel between); a norm that is not finite leaves everything as it is.  Six blocks
-// an SM as without it: 1M Gaussians 306 us with the norm's 52, 312 us with five blocks; going backwards, where L2 might
-// still hold the norm's last reads, gave nothing (308).
+// CLIP: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by
+// itself (a few KB in L2; a launch fewer than a kernel between); a norm that is not finite leaves everything as it
+// is.  Six blocks an SM as without it: 1M Gaussians 306 us with the norm's 52, 312 us with five blocks; going
+// backwards, where L2 might still hold the norm's last reads, gave nothing (308).
 template <bool CLIP>
 __global__ void __launch_bounds__(256, CLIP ? 6 : 1) k_adam(const __grid_constant__ AdamTable T) {
     RS_PDL_ENTER();

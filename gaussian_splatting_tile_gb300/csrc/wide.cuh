@@ -22,10 +22,10 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
-// Eight consecutive values as they are stored, of which the first `left` exist (the others read as zero).  VEC: the place
-// is aligned to 16 bytes, and a whole run is one or two 16-byte accesses; else a run of 16-bit values is read as aligned
-// words where its neighbours on both sides exist (`inner`).  16-bit types stay packed in four registers, where a maximum of
-// magnitudes is exact, and are widened where they are used.
+// Eight consecutive values as they are stored, of which the first `left` exist (the others read as zero).  VEC: the
+// place is aligned to 16 bytes, and a whole run is one or two 16-byte accesses; else a run of 16-bit values is read
+// as aligned words where its neighbours on both sides exist (`inner`).  16-bit types stay packed in four registers,
+// where a maximum of magnitudes is exact, and are widened where they are used.
 template <typename T>
 struct Run8 {
     float v[8];
@@ -180,7 +180,8 @@ __device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const float (&
 template <typename T>
 __device__ __forceinline__ void store8_e4m3(uint8_t* p, int left, const Run8<T>& v, float inv) {
     const float2 a = v.pair(0), b = v.pair(1), c = v.pair(2), d = v.pair(3);
-    store8_bytes(p, left, e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv), e4m3x4(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
+    store8_bytes(p, left, e4m3x4(a.x * inv, a.y * inv, b.x * inv, b.y * inv),
+                 e4m3x4(c.x * inv, c.y * inv, d.x * inv, d.y * inv));
 }
 
 // A block's scale and the factor its values are multiplied by, from its largest magnitude.  Both are correctly rounded
@@ -220,8 +221,9 @@ __device__ __forceinline__ float group_sum(float x) {
     return x;
 }
 
-// The gradient norm from its partial sums of squares, the same bits in every block; all 256 threads call it.  In float32: the
-// sums are positive and the chains short, and in float64 this alone took 27 us of a step over 59 M parameters.
+// The gradient norm from its partial sums of squares, the same bits in every block; all 256 threads call it.  In
+// float32: the sums are positive and the chains short, and in float64 this alone took 27 us of a step over 59 M
+// parameters.
 __device__ __forceinline__ float norm_of_parts(const float* part, int parts) {
     __shared__ float sm[8];
     float v = 0.f;

@@ -442,20 +442,21 @@ int rs_densify_apply(int32_t n, const void* d_workspace, size_t workspace_bytes,
  * Wide appearance networks: the root-mean-square norm, 8-bit matrix product and gradient clipping
  * that a network wider than rs_mlp is made of and trained with.  The pages have no counterpart.
  *
- * These calls work on row-major matrices (one row per Gaussian, or per weight row): element
- * (r, c) sits at base[r * stride + c], with stride >= the columns, in elements.  An element type
- * is one of RS_F32, RS_F16, RS_BF16; sums, statistics and norms are float32 whatever the type.
+ * These calls work on row-major matrices (one row per Gaussian, or per weight row): element (r,
+ * c) sits at base[r * stride + c], with stride >= the columns, in elements.  An element type is
+ * one of RS_F32, RS_F16, RS_BF16; sums, statistics and norms are float32 whatever the type.
  *
  * 8-bit matrices hold e4m3 values (OCP 8-bit floating point: 4 exponent bits, 3 mantissa bits,
- * largest 448, one NaN and no infinity) with one float32 scale for each block of RS_FP8_BLOCK = 128
- * consecutive elements of a row; the value is q * scale.  With A = max(largest magnitude of the block, 2^-100):
- * scale = A / 448 and q = e4m3(y * (448 / A)), both quotients and the product rounded to float32, the conversion to the
- * nearest value with ties to even.  A block that holds an infinity or a NaN reads back as NaN
- * wherever its value was not finite (with an infinity in it, everywhere).  Rows of 8-bit matrices
- * start on 16-byte boundaries (base and stride multiples of 16 bytes); the bytes past a row's last
- * column are neither read nor written.  Scales are planar like the library's other per-row
- * values: [ceil(columns / 128)][rows], row stride `rows`.  Weights may instead have one scale for each
- * 128 x 128 block: [ceil(columns / 128)][ceil(rows / 128)]. */
+ * largest 448, one NaN and no infinity) with one float32 scale for each block of RS_FP8_BLOCK =
+ * 128 consecutive elements of a row; the value is q * scale.  With A = max(largest magnitude of
+ * the block, 2^-100): scale = A / 448 and q = e4m3(y * (448 / A)), both quotients and the product
+ * rounded to float32, the conversion to the nearest value with ties to even.  A block that holds
+ * an infinity or a NaN reads back as NaN wherever its value was not finite (with an infinity in
+ * it, everywhere).  Rows of 8-bit matrices start on 16-byte boundaries (base and stride multiples
+ * of 16 bytes); the bytes past a row's last column are neither read nor written.  Scales are
+ * planar like the library's other per-row values: [ceil(columns / 128)][rows], row stride `rows`.
+ * Weights may instead have one scale for each 128 x 128 block: [ceil(columns / 128)][ceil(rows /
+ * 128)]. */
 #define RS_F32 0
 #define RS_F16 1
 #define RS_BF16 2
@@ -466,23 +467,26 @@ int rs_densify_apply(int32_t n, const void* d_workspace, size_t workspace_bytes,
  *   s = x + residual (residual may be NULL: s = x), rstd = 1 / sqrt(mean(s^2) + eps),
  *   y = s rstd weight, and q, scales = the 8-bit form of y.
  * d_sum (may be NULL) receives s and d_y (may be NULL) y, both in the input's type; d_rstd [rows]
- * (may be NULL) what rs_rms_norm_bwd needs.  d_q and d_scales may both be NULL when d_y is given.  d_sum may be d_x
- * or d_residual (same stride): the addition in place.  The other outputs must not overlap inputs.
- * weight [cols] is float32.  1 <= cols <= RS_NORM_MAX_COLS; rows = 0 is valid.  eps >= 0.  With
- * eps = 0 a row of zeros gives NaN.  Errors: RS_ERR_INVALID_ARG, RS_ERR_CUDA. */
+ * (may be NULL) what rs_rms_norm_bwd needs.  d_q and d_scales may both be NULL when d_y is given.
+ * d_sum may be d_x or d_residual (same stride): the addition in place.  The other outputs must
+ * not overlap inputs. weight [cols] is float32.  1 <= cols <= RS_NORM_MAX_COLS; rows = 0 is
+ * valid.  eps >= 0.  With eps = 0 a row of zeros gives NaN.  Errors: RS_ERR_INVALID_ARG,
+ * RS_ERR_CUDA. */
 int rs_rms_norm_fwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
                     const void* d_residual, size_t residual_stride, const float* d_weight, float eps,
                     void* d_sum, size_t sum_stride, void* d_y, size_t y_stride, uint8_t* d_q,
                     size_t q_stride, float* d_scales, float* d_rstd, void* stream);
 
-/* Backward of rs_rms_norm_fwd, the rounding to 8 bits taken as the identity.  With xh = s rstd and t = dL_dy weight:
+/* Backward of rs_rms_norm_fwd, the rounding to 8 bits taken as the identity.  With xh = s rstd
+ * and t = dL_dy weight:
  *   dL_dx = rstd (t - xh mean(t xh)) + dL_dsum,   dL_dweight = sum over rows of dL_dy xh.
- * d_s is the forward's input sum (d_sum, or d_x without a residual), d_rstd its statistic.  d_dL_dsum
- * (may be NULL) is the gradient that reaches the sum by its other uses.  dL_dx is the gradient of x and of the
- * residual alike; it may be d_dL_dy or d_dL_dsum (same stride).  All matrices have one type.  d_dL_dweight [cols]
- * float32 (may be NULL), summed in a fixed order.  Both outputs are overwritten; with rows = 0 dL_dweight is zero.
- * d_workspace: rs_rms_norm_bwd_workspace_size bytes (0 for invalid sizes), 16-byte aligned, contents undefined on entry and
- * exit.  Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
+ * d_s is the forward's input sum (d_sum, or d_x without a residual), d_rstd its statistic.
+ * d_dL_dsum (may be NULL) is the gradient that reaches the sum by its other uses.  dL_dx is the
+ * gradient of x and of the residual alike; it may be d_dL_dy or d_dL_dsum (same stride).  All
+ * matrices have one type.  d_dL_dweight [cols] float32 (may be NULL), summed in a fixed order.
+ * Both outputs are overwritten; with rows = 0 dL_dweight is zero. d_workspace:
+ * rs_rms_norm_bwd_workspace_size bytes (0 for invalid sizes), 16-byte aligned, contents undefined
+ * on entry and exit.  Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
 size_t rs_rms_norm_bwd_workspace_size(int32_t rows, int32_t cols);
 int rs_rms_norm_bwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_s, size_t s_stride,
                     const float* d_weight, const float* d_rstd, const void* d_dL_dy, size_t dy_stride,
@@ -492,12 +496,11 @@ int rs_rms_norm_bwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_s, 
 /* 8-bit forms of a matrix x [rows][cols], either or both in one pass over it:
  *   d_q [rows][cols] with d_scales [ceil(cols / 128)][rows] (blocks along a row), and
  *   d_qt [cols][rows], the transpose, with d_scales_t [ceil(rows / 128)][cols] (blocks of 128 rows).
- * A pair may be NULL; not both.  d_relu (may be NULL): a matrix of x's type and shape; x counts as
- * zero where it is <= 0 (the backward of a relu, given its output).
- * rs_quantize_fp8_blocks gives one scale to each 128 x 128 block (weights): d_scales
- * [ceil(cols / 128)][ceil(rows / 128)]; d_qt holds the same values transposed, its
- * d_scales_t [ceil(rows / 128)][ceil(cols / 128)] the same scales.
- * rows or cols = 0 is valid.  Errors: RS_ERR_INVALID_ARG, RS_ERR_CUDA. */
+ * A pair may be NULL; not both.  d_relu (may be NULL): a matrix of x's type and shape; x counts
+ * as zero where it is <= 0 (the backward of a relu, given its output). rs_quantize_fp8_blocks
+ * gives one scale to each 128 x 128 block (weights): d_scales [ceil(cols / 128)][ceil(rows /
+ * 128)]; d_qt holds the same values transposed, its d_scales_t [ceil(rows / 128)][ceil(cols /
+ * 128)] the same scales. rows or cols = 0 is valid.  Errors: RS_ERR_INVALID_ARG, RS_ERR_CUDA. */
 int rs_quantize_fp8(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
                     const void* d_relu, size_t relu_stride, uint8_t* d_q, size_t q_stride,
                     float* d_scales, uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream);
@@ -508,14 +511,15 @@ int rs_quantize_fp8_blocks(int32_t rows, int32_t cols, int32_t dtype, const void
 /* Matrix product of two 8-bit matrices, both with the contracted axis along their rows:
  *   out[i][j] = sum over blocks b of a_scales[b][i] b_scales[b][j] sum over t in block b of a[i][t] b[j][t]
  * a [m][k], b [n][k] (a linear layer's weights as they are stored), out [m][n] of out_dtype.
- * b_scale_rows: 1 when d_b_scales is [ceil(k / 128)][n] (a scale per row of b, as a's), 128 when it is
- * [ceil(k / 128)][ceil(n / 128)] (a scale per 128 rows).  relu != 0: negative results become zero (NaN stays).
- * The sums are float32, in an order that the sizes alone fix.  A layer's backward is the same product: dL_dx = dY W with the
- * transposed weights of rs_quantize_fp8_blocks, dW = dY^T X with the transposed forms of rs_quantize_fp8.
- * m, n, k >= 0; k = 0 gives zeros.  d_workspace: rs_matmul_fp8_workspace_size bytes (0: none
- * needed, may be NULL), 16-byte aligned, contents undefined on entry and exit.  The kernels' waits are bounded; one that gives up leaves its part
- * of the output unwritten and raises the flag rs_device_error reports.
- * Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
+ * b_scale_rows: 1 when d_b_scales is [ceil(k / 128)][n] (a scale per row of b, as a's), 128 when
+ * it is [ceil(k / 128)][ceil(n / 128)] (a scale per 128 rows).  relu != 0: negative results
+ * become zero (NaN stays). The sums are float32, in an order that the sizes alone fix.  A layer's
+ * backward is the same product: dL_dx = dY W with the transposed weights of
+ * rs_quantize_fp8_blocks, dW = dY^T X with the transposed forms of rs_quantize_fp8. m, n, k >= 0;
+ * k = 0 gives zeros.  d_workspace: rs_matmul_fp8_workspace_size bytes (0: none needed, may be
+ * NULL), 16-byte aligned, contents undefined on entry and exit.  The kernels' waits are bounded;
+ * one that gives up leaves its part of the output unwritten and raises the flag rs_device_error
+ * reports. Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
 size_t rs_matmul_fp8_workspace_size(int32_t m, int32_t n, int32_t k);
 int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride,
                   const float* d_a_scales, const uint8_t* d_b, size_t b_stride, const float* d_b_scales,
@@ -523,9 +527,9 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
                   void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* One gradient tensor: `count` contiguous values of `dtype`.  d_out (may be NULL; may be d_grad)
- * receives the clipped values, in the same type.  With an activation (RS_ACT_*), d_param holds the stored
- * float32 parameters and the gradient counts in the norm as dL/dparam = d_grad * act'(param), as the
- * Adam step applies it. */
+ * receives the clipped values, in the same type.  With an activation (RS_ACT_*), d_param holds
+ * the stored float32 parameters and the gradient counts in the norm as dL/dparam = d_grad *
+ * act'(param), as the Adam step applies it. */
 typedef struct rs_grad_tensor {
     const void* d_grad;
     void* d_out;
@@ -535,13 +539,14 @@ typedef struct rs_grad_tensor {
     int32_t activation;    /* RS_ACT_* */
 } rs_grad_tensor;
 
-/* Global gradient norm: *d_norm (one device float) = sqrt(sum over all tensors and values of g^2), in
- * float32, summed in an order that the sizes alone fix.  (Squares above float32's range give an infinite norm.)
- * rs_grad_clip also writes every tensor's d_out = g * c with c = min(1, max_norm / (norm + 1e-6)); a NaN norm
- * makes c NaN.  max_norm > 0 (infinity: norm only).  `tensors` is a host array that may be reused on return;
- * tensors must not overlap.  n_tensors >= 0 (the norm of none is 0).  d_workspace:
- * rs_grad_norm_workspace_size(n_tensors) bytes, 16-byte aligned, contents undefined on entry and exit.
- * Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
+/* Global gradient norm: *d_norm (one device float) = sqrt(sum over all tensors and values of
+ * g^2), in float32, summed in an order that the sizes alone fix.  (Squares above float32's range
+ * give an infinite norm.) rs_grad_clip also writes every tensor's d_out = g * c with c = min(1,
+ * max_norm / (norm + 1e-6)); a NaN norm makes c NaN.  max_norm > 0 (infinity: norm only).
+ * `tensors` is a host array that may be reused on return; tensors must not overlap.  n_tensors >=
+ * 0 (the norm of none is 0).  d_workspace: rs_grad_norm_workspace_size(n_tensors) bytes, 16-byte
+ * aligned, contents undefined on entry and exit. Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE,
+ * RS_ERR_CUDA. */
 size_t rs_grad_norm_workspace_size(int32_t n_tensors);
 int rs_grad_norm(const rs_grad_tensor* tensors, int32_t n_tensors, float* d_norm, void* d_workspace,
                  size_t workspace_bytes, void* stream);
@@ -549,10 +554,11 @@ int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_nor
                  void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* rs_adam_step on clipped gradients: *d_norm = the global norm of the segments' dL/dparam (their
- * activations' derivatives applied), and the step of rs_adam_step with every d_grad multiplied by c as in
- * rs_grad_clip (d_grad itself is not changed).  A norm that is not finite skips the step: parameters,
- * moments and activated values stay as they are, and *d_norm tells.  Nothing waits on the host.
- * d_workspace: rs_grad_norm_workspace_size(n_segs) bytes.  Errors: as rs_adam_step, RS_ERR_WORKSPACE. */
+ * activations' derivatives applied), and the step of rs_adam_step with every d_grad multiplied by
+ * c as in rs_grad_clip (d_grad itself is not changed).  A norm that is not finite skips the step:
+ * parameters, moments and activated values stay as they are, and *d_norm tells.  Nothing waits on
+ * the host. d_workspace: rs_grad_norm_workspace_size(n_segs) bytes.  Errors: as rs_adam_step,
+ * RS_ERR_WORKSPACE. */
 int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2,
                          double eps, int32_t step, float max_norm, float* d_norm, void* d_workspace,
                          size_t workspace_bytes, void* stream);
