@@ -139,10 +139,9 @@ struct NormBwdArgs {
 };
 
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its share of
-// dL/dweight stays in registers and leaves once per block, to be added up in a fixed order.  As many blocks as an SM
-// holds at once keep the memory busy: one run a thread (56 registers and less) with eight blocks of 128 threads;
-// asking for the next row's values ahead took registers, and blocks, and was slower (160,000 x 512 bf16 128 against
-// 121 us), as were four runs a thread (100,000 x 1000 bf16: 541 against 182 us).
+// dL/dweight stays in registers and leaves once per block, to be added up in a fixed order.  What keeps the memory busy
+// is the number of rows in flight on an SM; asking for the next row's values ahead took registers, and blocks, and was
+// slower (160,000 x 512 bf16 128 against 121 us), as were four runs a thread (100,000 x 1000 bf16 541 us).
 template <typename T, bool VEC, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdArgs a) {
     RS_PDL_ENTER();
@@ -246,14 +245,16 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = v;
 }
 
-// Threads a row and blocks an SM for a width.  One run a thread as far as that goes: its registers (the share of
-// dL/dweight among them) then leave room for many rows in flight.
+// Threads a row and blocks an SM for a width: as many blocks as fit at once, with the rows in flight that their registers
+// leave room for (a thread's share of dL/dweight among them).  One run a thread up to 512 columns and from 1025 to 2048
+// (60,000 x 2048 bf16 194 us, with two 204), two otherwise (100,000 x 1000 bf16 156 us, with one 184; 30,000 x 4096 206
+// against 236).
 int bwd_threads(int cols) {
     const int runs = ceil_div(cols, 8);
-    return runs <= 16 ? 16 : runs <= 32 ? 32 : runs <= 64 ? 64 : runs <= 128 ? 128 : runs <= 256 ? 256 : 512;
+    return runs <= 16 ? 16 : runs <= 32 ? 32 : runs <= 128 ? 64 : runs <= 512 ? 256 : 512;
 }
 int bwd_blocks(int rows, int cols) {
-    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1, per = t <= 128 ? 8 : t == 256 ? 4 : 2;
+    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1, per = cols <= 512 ? 8 : t == 64 ? 5 : cols <= 2048 ? 4 : t == 256 ? 2 : 1;
     return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * per));
 }
 
@@ -267,11 +268,9 @@ cudaError_t bwd_width(const NormBwdArgs& a, cudaStream_t s) {
     switch (bwd_threads(a.cols)) {
         case 16: return bwd<T, VEC, 16, 1>(a, s);
         case 32: return bwd<T, VEC, 32, 1>(a, s);
-        case 64: return bwd<T, VEC, 64, 1>(a, s);
-        case 128: return bwd<T, VEC, 128, 1>(a, s);
-        case 256: return bwd<T, VEC, 256, 1>(a, s);
+        case 64: return a.cols <= 512 ? bwd<T, VEC, 64, 1>(a, s) : bwd<T, VEC, 64, 2>(a, s);
+        case 256: return a.cols <= 2048 ? bwd<T, VEC, 256, 1>(a, s) : bwd<T, VEC, 256, 2>(a, s);
     }
-    if (a.cols <= 4096) return bwd<T, VEC, 512, 1>(a, s);
     return a.cols <= 8192 ? bwd<T, VEC, 512, 2>(a, s) : bwd<T, VEC, 512, 4>(a, s);
 }
 
