@@ -7,7 +7,7 @@
 // shuffles.  The norm is taken of the sum before its rounding to 16 bits.
 //
 // Measured (GB300, inputs beyond L2): 250,000 x 512 bf16 with the residual 152 us (5.9 TB/s of the copy's 6.7),
-// float32 6.9 TB/s; 160,000 x 1000 bf16 5.0 TB/s.  Rows that do not start on 16-byte boundaries go by words: 100,000
+// float32 6.9 TB/s; 160,000 x 1000 bf16 5.4 TB/s.  Rows that do not start on 16-byte boundaries go by words: 100,000
 // x 777 bf16 2.6 TB/s.  One row of 4096 costs the call (9 us).
 //
 // Backward, per row: xh = s rstd, t = dy w, dx = rstd (t - xh mean(t xh)) + ds; dw = sum over rows of dy xh.  Bound
@@ -112,13 +112,16 @@ cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
     return pdl_launch(k_rms_norm_fwd<T, VEC, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
 }
 
+// Threads a row and runs a thread, measured with the residual in bf16: 250,000 x 512 on a warp 158 us, on two with
+// one run each the same (without a residual 105 against 132), on half a warp 203; 160,000 x 1000 on four warps 208,
+// on two 224, on one 267; 30,000 x 4096 on eight 171, on sixteen 179, on four 195.
 template <typename T, bool VEC>
 cudaError_t fwd_width(const NormArgs& a, cudaStream_t s) {
     const int runs = ceil_div(a.cols, 8);
     if (runs <= 16) return fwd<T, VEC, 16, 1>(a, s);
     if (runs <= 32) return fwd<T, VEC, 32, 1>(a, s);
     if (runs <= 64) return fwd<T, VEC, 32, 2>(a, s);
-    if (runs <= 128) return fwd<T, VEC, 64, 2>(a, s);
+    if (runs <= 128) return fwd<T, VEC, 128, 1>(a, s);
     if (runs <= 256) return fwd<T, VEC, 128, 2>(a, s);
     if (runs <= 512) return fwd<T, VEC, 256, 2>(a, s);
     if (runs <= 1024) return fwd<T, VEC, 512, 2>(a, s);
@@ -139,9 +142,9 @@ struct NormBwdArgs {
 };
 
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its share of
-// dL/dweight stays in registers and leaves once per block, to be added up in a fixed order.  What keeps the memory busy
-// is the number of rows in flight on an SM; asking for the next row's values ahead took registers, and blocks, and was
-// slower (160,000 x 512 bf16 128 against 121 us), as were four runs a thread (100,000 x 1000 bf16 541 us).
+// dL/dweight stays in registers and leaves once per block, to be added up in a fixed order.  What keeps the memory
+// busy is the number of rows in flight on an SM; asking for the next row's values ahead took registers, and blocks,
+// and was slower (160,000 x 512 bf16 128 against 121 us), as were four runs a thread (100,000 x 1000 bf16 541 us).
 template <typename T, bool VEC, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_bwd(NormBwdArgs a) {
     RS_PDL_ENTER();
@@ -245,10 +248,10 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = v;
 }
 
-// Threads a row and blocks an SM for a width: as many blocks as fit at once, with the rows in flight that their registers
-// leave room for (a thread's share of dL/dweight among them).  One run a thread up to 512 columns and from 1025 to 2048
-// (60,000 x 2048 bf16 194 us, with two 204), two otherwise (100,000 x 1000 bf16 156 us, with one 184; 30,000 x 4096 206
-// against 236).
+// Threads a row and blocks an SM for a width: as many blocks as fit at once, with the rows in flight that their
+// registers leave room for (a thread's share of dL/dweight among them).  One run a thread up to 512 columns and from
+// 1025 to 2048 (60,000 x 2048 bf16 194 us, with two 204), two otherwise (100,000 x 1000 bf16 156 us, with one 184;
+// 30,000 x 4096 206 against 236).
 int bwd_threads(int cols) {
     const int runs = ceil_div(cols, 8);
     return runs <= 16 ? 16 : runs <= 32 ? 32 : runs <= 128 ? 64 : runs <= 512 ? 256 : 512;

@@ -580,18 +580,12 @@ class AdamGroup:
 def _adam_segments(groups):
     if len(groups) > RS_ADAM_MAX_SEGMENTS:
         raise ValueError(f"at most {RS_ADAM_MAX_SEGMENTS} groups per call")
-    arr = (rs_adam_segment * max(1, len(groups)))()
-    for i, gr in enumerate(groups):
-        k = int(gr.param.numel())
-        arr[i].d_param = _ptr(gr.param, torch.float32, k, "param")
-        arr[i].d_grad = _ptr(gr.grad, torch.float32, k, "grad")
-        arr[i].d_m = _ptr(gr.m, torch.float32, k, "m")
-        arr[i].d_v = _ptr(gr.v, torch.float32, k, "v")
-        arr[i].d_activated = _ptr(gr.activated, torch.float32, k, "activated")
-        arr[i].count = k
-        arr[i].lr = float(gr.lr)
-        arr[i].activation = int(gr.activation)
-    return arr
+    f32, segs = torch.float32, []
+    for gr in groups:
+        k = gr.param.numel()
+        segs.append((_vec(gr.param, f32, k, "param"), _vec(gr.grad, f32, k, "grad"), _vec(gr.m, f32, k, "m"),
+                     _vec(gr.v, f32, k, "v"), _vec(gr.activated, f32, k, "activated"), k, float(gr.lr), int(gr.activation)))
+    return (rs_adam_segment * max(1, len(segs)))(*segs)
 
 
 def rs_adam_step(groups, step: int, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-15,
