@@ -265,15 +265,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
     __shared__ uint32_t tmem_slot;
-    // The scales of kRing blocks: a's of the CTA's rows, then b's of the tile's columns (ROWS) or of its halves.
-    constexpr int kRing = 8, kScales = 128 + (ROWS ? BN : 4);
+    // The scales of kRing blocks: a's of the CTA's rows, then b's of the tile's columns (ROWS) or of its halves.  Four blocks
+    // share a barrier, so that the readers ask and answer once in four.
+    constexpr int kRing = 16, kGroups = kRing / 4, kScales = 128 + (ROWS ? BN : 4);
     __shared__ __align__(16) float scales[kRing][kScales];
-    __shared__ uint64_t sc_full[kRing], sc_empty[kRing];
+    __shared__ uint64_t sc_full[kGroups], sc_empty[kGroups];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
         for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 2 * kSumWarps);
-        for (int i = 0; i < kRing; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps);
+        for (int i = 0; i < kGroups; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -342,8 +343,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // The scales, up to kRing blocks ahead of their use and on into the next tiles: a load takes longer than
             // a block. Rows and columns outside the matrices take the last one's: what comes of them is not stored.
             const int per = ROWS ? g.n : (g.n + kBlock - 1) / kBlock;  // b's scales a block
-            uint32_t slot = 0, phase = 1;
+            uint32_t count = 0;  // of blocks
             bool ok = true;
+            const auto done = [&] {  // with the copies of a group, when they are
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[(count >> 2) % kGroups]))
+                             : "memory");
+            };
             for (int u = pair; u < units && ok; u += pairs) {
                 const int tile = u % g.tiles, x = tile % g.tiles_n * BN;
                 const long long y = (long long)(tile / g.tiles_n * 2 + rank) * 128 + lane;
@@ -351,8 +356,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const float* pa = g.sa + size_t(r.first) * g.m;
                 const float* pb = g.sb + size_t(r.first) * per;
                 for (int b = r.first; b < r.last; ++b, pa += g.m, pb += per) {
-                    if (!(ok = __all_sync(0xffffffffu, bar_wait(&sc_empty[slot], phase)))) break;
-                    float* to = scales[slot];
+                    if (count % 4 == 0) {
+                        const uint32_t parity = (count / kRing & 1) ^ 1;
+                        ok = __all_sync(0xffffffffu, bar_wait(&sc_empty[(count >> 2) % kGroups], parity));
+                        if (!ok) break;
+                    }
+                    float* to = scales[count % kRing];
 #pragma unroll
                     for (int i = 0; i < 128; i += 32) copy4(to + i + lane, pa + min(y + i, (long long)g.m - 1));
                     if (ROWS) {
@@ -361,11 +370,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     } else if (lane < 2) {
                         copy4(to + 128 + lane, pb + min((x + lane * kCols) / kBlock, per - 1));
                     }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[slot]))
-                                 : "memory");
-                    if (++slot == kRing) slot = 0, phase ^= 1;
+                    if (count % 4 == 3) done();
+                    ++count;
                 }
             }
+            if (count % 4 != 0) done();
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t full0 = smem_u32(acc_full), empty0 = cluster_addr(acc_empty, 0);
         const uint32_t sc_full0 = smem_u32(sc_full), sc_empty0 = smem_u32(sc_empty);
         uint32_t h = 0, phase = 0;         // the accumulator to read next
-        uint32_t slot = 0, sc_phase = 0;   // and the scales
+        uint32_t count = 0;                // of blocks
         bool ok = true;
         for (int u = pair; u < units; u += pairs) {
             const int tile = u % g.tiles;
@@ -388,14 +397,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
             for (int b = r.first; b < r.last; ++b) {
                 // a wait that gave up ends the waiting, not the loop: what is added from then on is not stored
-                ok = ok && __all_sync(0xffffffffu, bar_wait(sc_full0 + slot * 8, sc_phase));
-                const float* sc = scales[slot];
+                const uint32_t group = (count >> 2) % kGroups;
+                if (count % 4 == 0)
+                    ok = ok && __all_sync(0xffffffffu, bar_wait(sc_full0 + group * 8, count / kRing & 1));
+                const float* sc = scales[count % kRing];
                 const float* sb = sc + 128 + (ROWS ? half * kCols : half);
                 const float f = ROWS ? sc[wrow + lane] : sc[wrow + lane] * sb[0];
                 const uint64_t ff = pack2(f, f);
-                if (!ROWS) {
+                if (!ROWS && count % 4 == 3) {
                     __syncwarp();
-                    if (lane == 0) bar_arrive(sc_empty0 + slot * 8);
+                    if (lane == 0) bar_arrive(sc_empty0 + group * 8);
                 }
                 ok = ok && __all_sync(0xffffffffu, bar_wait(full0 + h * 8, phase));
                 tc_after();
@@ -423,11 +434,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         acc[8 * c + j / 2 + 1] = fma2(q, ff, acc[8 * c + j / 2 + 1]);
                     }
                 }
-                if (ROWS) {
+                if (ROWS && count % 4 == 3) {
                     __syncwarp();
-                    if (lane == 0) bar_arrive(sc_empty0 + slot * 8);
+                    if (lane == 0) bar_arrive(sc_empty0 + group * 8);
                 }
-                if (++slot == kRing) slot = 0, sc_phase ^= 1;
+                ++count;
                 if (++h == kAcc) h = 0, phase ^= 1;
             }
             if (!ok) break;
@@ -812,6 +823,8 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     using namespace rs;
     if (m < 0 || n < 0 || k < 0 || !dtype_ok(out_dtype) || (b_scale_rows != 1 && b_scale_rows != kBlock))
         return RS_ERR_INVALID_ARG;
+    constexpr int32_t kMost = 0x7ffffc00;  // the last tile's rows still are numbers of 32 bits
+    if (m > kMost || n > kMost || k > kMost) return RS_ERR_INVALID_ARG;
     if (m == 0 || n == 0) return RS_OK;
     const size_t z = dtype_size(out_dtype);
     if (!ptr_ok(d_out, z) || out_stride < size_t(n)) return RS_ERR_INVALID_ARG;
