@@ -12,10 +12,11 @@
 // What bounds it: 128 products take 256 x 256 outputs of two SMs about 490 clocks on the tensor cores; adding them up
 // takes each of their schedulers 8192 multiply-adds, 390 clocks at the rate that two warps reach.  The two overlap,
 // but each accumulator's way round (products, word to the readers, reading, word back) is longer than both, and there
-// is room for two: that is what large products wait for.  Products with few blocks are bound by the results' way out.
-// Measured: 65536 x 2048 x 2048 float16 out 257 us (2.1 PFLOP/s; without any adding up the same loads and products
-// would take 148), 8192^3 2.4 PFLOP/s, 160,000 x 512 x 512 bf16 64 us (3.9 TB/s; 37 at the copy's rate), dW of it
-// (512 x 256 x 160,000, a scale a row) 45 us, 1 x 4096 x 4096 10 us, the call itself.
+// is room for two: that, and every instruction between the readers' loads, is what large products wait for.  Products
+// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 236 us alone, 249 back to back (2.2 PFLOP/s;
+// without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 64
+// us (3.9 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us, 1 x 4096 x 4096 9
+// us, the call itself.
 #include <cuda.h>
 
 #include "wide.cuh"
@@ -198,10 +199,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // half of the columns. Tensor memory holds kAcc accumulators of BN columns: the products of the next blocks run while
 // a block is read.
 //
-// What was tried and not kept: single CTAs with 128 x 256 tiles (8192^3 476 against 431 us); sixteen warps adding up
-// 64 columns each, which do not fit the registers without moves (527 us); accumulators of 128 columns, twice as many
-// (65536 x 2048 x 2048 263 against 257 us, 160,000 x 512 x 512 66 against 68); looking at the next barrier early;
-// scalar multiply-adds instead of pairs (8192^3 472 against 459 us).
+// What was tried and not kept (8192^3, each against the kernel of the time): single CTAs with 128 x 256 tiles, 476
+// against 431 us; sixteen warps adding up 64 columns each, which do not fit the registers without moves, 527 against
+// 420; accumulators of 128 columns, twice as many, 494 against 463 (160,000 x 512 x 512: 66 against 68); scalar
+// multiply-adds instead of pairs, 472 against 459; the scales fetched by the readers themselves, a little better here
+// (431) and worse where tiles are short (160,000 x 512 x 512: 76); asking for the next accumulator early, nothing.
 constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;
 constexpr int kPairs = kSms / 2;
@@ -265,8 +267,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     Smem& sm = *reinterpret_cast<Smem*>(raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u));
     __shared__ uint64_t full[kStages], empty[kStages], acc_full[kAcc], acc_empty[kAcc];
     __shared__ uint32_t tmem_slot;
-    // The scales of kRing blocks: a's of the CTA's rows, then b's of the tile's columns (ROWS) or of its halves.  Four blocks
-    // share a barrier, so that the readers ask and answer once in four.
+    // The scales of kRing blocks: a's of the CTA's rows, then b's of the tile's columns (ROWS) or of its halves.
+    // Four blocks share a barrier, so that the readers ask and answer once in four.
     constexpr int kRing = 16, kGroups = kRing / 4, kScales = 128 + (ROWS ? BN : 4);
     __shared__ __align__(16) float scales[kRing][kScales];
     __shared__ uint64_t sc_full[kGroups], sc_empty[kGroups];
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint32_t count = 0;  // of blocks
             bool ok = true;
             const auto done = [&] {  // with the copies of a group, when they are
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&sc_full[(count >> 2) % kGroups]))
-                             : "memory");
+                const uint32_t bar = smem_u32(&sc_full[(count >> 2) % kGroups]);
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
             };
             for (int u = pair; u < units && ok; u += pairs) {
                 const int tile = u % g.tiles, x = tile % g.tiles_n * BN;
@@ -396,10 +398,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
             for (int b = r.first; b < r.last; ++b) {
-                // a wait that gave up ends the waiting, not the loop: what is added from then on is not stored
                 const uint32_t group = (count >> 2) % kGroups;
+                // a wait that gave up ends the waiting, not the loop: what is added from then on is not stored
                 if (count % 4 == 0)
-                    ok = ok && __all_sync(0xffffffffu, bar_wait(sc_full0 + group * 8, count / kRing & 1));
+                    ok = ok && bar_wait(sc_full0 + group * 8, count / kRing & 1);
                 const float* sc = scales[count % kRing];
                 const float* sb = sc + 128 + (ROWS ? half * kCols : half);
                 const float f = ROWS ? sc[wrow + lane] : sc[wrow + lane] * sb[0];
@@ -408,7 +410,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     __syncwarp();
                     if (lane == 0) bar_arrive(sc_empty0 + group * 8);
                 }
-                ok = ok && __all_sync(0xffffffffu, bar_wait(full0 + h * 8, phase));
+                ok = ok && bar_wait(full0 + h * 8, phase);
+                __syncwarp();
                 tc_after();
                 uint32_t v[2][16];
                 tc_ld16(lanes + h * BN, v[0]);
@@ -441,6 +444,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 ++count;
                 if (++h == kAcc) h = 0, phase ^= 1;
             }
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             if (g.splits > 1) {
                 float* o = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + wrow + lane;
