@@ -6,9 +6,9 @@
 // of a 16-bit type), and a block of 128 columns is the run of 16 neighbouring threads, whose maximum takes four
 // shuffles.  The norm is taken of the sum before its rounding to 16 bits.
 //
-// Measured (GB300, inputs beyond L2): 250,000 x 512 bf16 with the residual 152 us (5.9 TB/s of the copy's 6.7),
-// float32 6.9 TB/s; 160,000 x 1000 bf16 5.4 TB/s.  Rows that do not start on 16-byte boundaries go by words: 100,000
-// x 777 bf16 2.6 TB/s.  One row of 4096 costs the call (9 us).
+// Measured (GB300, inputs beyond L2): 250,000 x 512 bf16 with the residual 128 us (7.0 TB/s; the copy 6.7), float32
+// 6.9 TB/s; 160,000 x 1000 bf16, whose rows end inside a thread's runs, 5.4 TB/s. Rows that do not start on 16-byte
+// boundaries go by words: 100,000 x 777 bf16 2.6 TB/s.  One row of 4096 costs the call (9 us).
 //
 // Backward, per row: xh = s rstd, t = dy w, dx = rstd (t - xh mean(t xh)) + ds; dw = sum over rows of dy xh.  Bound
 // by memory too: three matrices in, one out.  160,000 x 256 float32 103 us (6.3 TB/s), 160,000 x 512 bf16 5.4 TB/s.
@@ -47,9 +47,14 @@ __device__ __forceinline__ float row_sum(float v, float* smem) {
     return v;
 }
 
-template <typename T, bool VEC, int TPR, int RUNS>
+// How a row is moved: value by value or word by word, in 16-byte accesses with a ragged end, or all of it in such
+// accesses (the width is 8 TPR RUNS).
+enum Move { kAny, kVec, kFull };
+
+template <typename T, Move MOVE, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs a) {
     RS_PDL_ENTER();
+    constexpr bool VEC = MOVE != kAny;
     constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
     __shared__ float smem[32];
     const int t = threadIdx.x % TPR;
@@ -61,7 +66,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
-        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        const int c = (i * TPR + t) * 8, left = MOVE == kFull ? 8 : in ? a.cols - c : 0;
         load8<T, VEC>(x + c, left, v[i], c > 0);
         if (r) {
             float u[8];
@@ -77,17 +82,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
     if (a.sum && in) {
         T* s = static_cast<T*>(a.sum) + row * a.sums;
 #pragma unroll
-        for (int i = 0; i < RUNS; ++i) store8<T, VEC>(s + (i * TPR + t) * 8, a.cols - (i * TPR + t) * 8, v[i]);
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = (i * TPR + t) * 8;
+            store8<T, VEC>(s + c, MOVE == kFull ? 8 : a.cols - c, v[i]);
+        }
     }
     float top[RUNS];
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
-        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        const int c = (i * TPR + t) * 8, left = MOVE == kFull ? 8 : in ? a.cols - c : 0;
         float w[8];
         load8<float, VEC>(a.w + c, left, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] * rstd * w[j];
-        if (a.y && left > 0) store8<T, VEC>(static_cast<T*>(a.y) + row * a.ys + c, left, v[i]);
+        if (a.y && in && left > 0) store8<T, VEC>(static_cast<T*>(a.y) + row * a.ys + c, left, v[i]);
         top[i] = group_max<16>(max_abs8(v[i], 0.f));
     }
     if (!a.q) return;
@@ -99,33 +107,58 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
     block_scale(mine, scale, inv);
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
-        const int c = (i * TPR + t) * 8, left = in ? a.cols - c : 0;
+        const int c = (i * TPR + t) * 8, left = MOVE == kFull ? 8 : a.cols - c;
         const float k = __shfl_sync(0xffffffffu, inv, i, 16);
-        if (of == i && c - of * 8 < a.cols && in) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
-        if (left > 0) store8_e4m3(a.q + row * a.qs + c, left, v[i], k);
+        if (of == i && in && (MOVE == kFull || c - of * 8 < a.cols)) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
+        if (in && left > 0) store8_e4m3(a.q + row * a.qs + c, left, v[i], k);
     }
 }
 
-template <typename T, bool VEC, int TPR, int RUNS>
+template <typename T, Move MOVE, int TPR, int RUNS>
 cudaError_t fwd(const NormArgs& a, cudaStream_t s) {
     constexpr int kRows = TPR < 128 ? 128 / TPR : 1;
-    return pdl_launch(k_rms_norm_fwd<T, VEC, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
+    return pdl_launch(k_rms_norm_fwd<T, MOVE, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
 }
 
-// Threads a row and runs a thread, measured with the residual in bf16: 250,000 x 512 on a warp 158 us, on two with
-// one run each the same (without a residual 105 against 132), on half a warp 203; 160,000 x 1000 on four warps 208,
-// on two 224, on one 267; 30,000 x 4096 on eight 171, on sixteen 179, on four 195.
-template <typename T, bool VEC>
+// Widths that two or three runs for each of 16, 32, ... 512 threads fit exactly (and 128): no run asks whether it
+// exists, which is a third of the instructions (bf16 with the residual: 250,000 x 512 136 us, 158 with the questions;
+// 160,000 x 768 132 against 189, x 1024 171 against 197).
+template <typename T, int TPR>
+cudaError_t fwd_two_three(const NormArgs& a, cudaStream_t s) {
+    return a.cols == TPR * 16 ? fwd<T, kFull, TPR, 2>(a, s) : fwd<T, kFull, TPR, 3>(a, s);
+}
+
+template <typename T>
+cudaError_t fwd_exact(const NormArgs& a, cudaStream_t s, bool& taken) {
+    const int runs = a.cols / 8, each = runs % 3 == 0 ? 3 : 2, threads = runs / each;
+    taken = a.cols % 8 == 0 && threads * each == runs;
+    if (taken) switch (threads) {
+        case 16: return fwd_two_three<T, 16>(a, s);
+        case 32: return fwd_two_three<T, 32>(a, s);
+        case 64: return fwd_two_three<T, 64>(a, s);
+        case 128: return fwd_two_three<T, 128>(a, s);
+        case 256: return fwd_two_three<T, 256>(a, s);
+        case 512: return fwd_two_three<T, 512>(a, s);
+        case 8: if (each == 2) return fwd<T, kFull, 16, 1>(a, s);
+    }
+    taken = false;
+    return cudaSuccess;
+}
+
+// Other widths: threads a row and runs a thread, measured with the residual in bf16: 250,000 x 512 on a warp 158 us,
+// on two with one run each the same (without a residual 105 against 132), on half a warp 203; 160,000 x 1000 on four
+// warps 208, on two 224, on one 267; 30,000 x 4096 on eight 171, on sixteen 179, on four 195.
+template <typename T, Move MOVE>
 cudaError_t fwd_width(const NormArgs& a, cudaStream_t s) {
     const int runs = ceil_div(a.cols, 8);
-    if (runs <= 16) return fwd<T, VEC, 16, 1>(a, s);
-    if (runs <= 32) return fwd<T, VEC, 32, 1>(a, s);
-    if (runs <= 64) return fwd<T, VEC, 32, 2>(a, s);
-    if (runs <= 128) return fwd<T, VEC, 128, 1>(a, s);
-    if (runs <= 256) return fwd<T, VEC, 128, 2>(a, s);
-    if (runs <= 512) return fwd<T, VEC, 256, 2>(a, s);
-    if (runs <= 1024) return fwd<T, VEC, 512, 2>(a, s);
-    return fwd<T, VEC, 512, 4>(a, s);
+    if (runs <= 16) return fwd<T, MOVE, 16, 1>(a, s);
+    if (runs <= 32) return fwd<T, MOVE, 32, 1>(a, s);
+    if (runs <= 64) return fwd<T, MOVE, 32, 2>(a, s);
+    if (runs <= 128) return fwd<T, MOVE, 128, 1>(a, s);
+    if (runs <= 256) return fwd<T, MOVE, 128, 2>(a, s);
+    if (runs <= 512) return fwd<T, MOVE, 256, 2>(a, s);
+    if (runs <= 1024) return fwd<T, MOVE, 512, 2>(a, s);
+    return fwd<T, MOVE, 512, 4>(a, s);
 }
 
 // ---------------------------------------------------------------- backward
@@ -312,7 +345,9 @@ int rs_rms_norm_fwd(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
-        return vec ? fwd_width<T, true>(a, s) : fwd_width<T, false>(a, s);
+        bool taken = false;
+        const cudaError_t e = vec ? fwd_exact<T>(a, s, taken) : cudaSuccess;
+        return taken ? e : vec ? fwd_width<T, kVec>(a, s) : fwd_width<T, kAny>(a, s);
     });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }

@@ -66,7 +66,8 @@ __device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<
 // 16-bit values leave registers for three blocks an SM; with a mask beside x two, so that both tiles are in flight at
 // once.
 enum Form { kRowsCols, kRowsColsRelu, kBlocks };
-template <typename T, bool VEC, Form FORM>
+// FULL: 16-byte rows, and no tile ends inside its columns.
+template <typename T, bool VEC, bool FULL, Form FORM>
 __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ? 2 : 3) k_quantize(QuantArgs a) {
     constexpr bool BLOCKS = FORM == kBlocks;
     RS_PDL_ENTER();
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ?
     const int ct = blockIdx.x % a.ctiles, rt = blockIdx.x / a.ctiles;  // neighbours share the rows
     const int c0 = ct * kBlock, c = c0 + tx * 8;
     const long long r0 = (long long)rt * kBlock, r = r0 + ty * 8;
-    const int left = a.cols - c;
+    const int left = FULL ? 8 : a.cols - c;
     Run8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -186,11 +187,17 @@ int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s) {
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         const unsigned g = unsigned(a.ctiles) * a.rtiles;
-        const auto launch = [&](auto kernel) { return pdl_launch(kernel, g, 256, 0, s, a); };
-        if (blocks) return vec ? launch(k_quantize<T, true, kBlocks>) : launch(k_quantize<T, false, kBlocks>);
+        const auto launch = [&](auto any, auto ragged, auto full) {
+            return pdl_launch(!vec ? any : a.cols % kBlock ? ragged : full, g, 256, 0, s, a);
+        };
+        if (blocks)
+            return launch(k_quantize<T, false, false, kBlocks>, k_quantize<T, true, false, kBlocks>,
+                          k_quantize<T, true, true, kBlocks>);
         if (a.relu)
-            return vec ? launch(k_quantize<T, true, kRowsColsRelu>) : launch(k_quantize<T, false, kRowsColsRelu>);
-        return vec ? launch(k_quantize<T, true, kRowsCols>) : launch(k_quantize<T, false, kRowsCols>);
+            return launch(k_quantize<T, false, false, kRowsColsRelu>, k_quantize<T, true, false, kRowsColsRelu>,
+                          k_quantize<T, true, true, kRowsColsRelu>);
+        return launch(k_quantize<T, false, false, kRowsCols>, k_quantize<T, true, false, kRowsCols>,
+                      k_quantize<T, true, true, kRowsCols>);
     });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
