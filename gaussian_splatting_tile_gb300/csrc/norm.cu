@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_rms_norm_fwd(NormArgs
     for (int i = 0; i < RUNS; ++i) {
         const int c = (i * TPR + t) * 8, left = MOVE == kFull ? 8 : a.cols - c;
         const float k = __shfl_sync(0xffffffffu, inv, i, 16);
-        if (of == i && in && (MOVE == kFull || c - of * 8 < a.cols)) a.scales[size_t(c / kBlock) * a.rows + row] = scale;
+        if (of == i && in && (MOVE == kFull || c - of * 8 < a.cols))
+            a.scales[size_t(c / kBlock) * a.rows + row] = scale;
         if (in && left > 0) store8_e4m3(a.q + row * a.qs + c, left, v[i], k);
     }
 }
@@ -290,7 +291,8 @@ int bwd_threads(int cols) {
     return runs <= 16 ? 16 : runs <= 32 ? 32 : runs <= 128 ? 64 : runs <= 512 ? 256 : 512;
 }
 int bwd_blocks(int rows, int cols) {
-    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1, per = cols <= 512 ? 8 : t == 64 ? 5 : cols <= 2048 ? 4 : t == 256 ? 2 : 1;
+    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1;
+    const int per = cols <= 512 ? 8 : t == 64 ? 5 : cols <= 2048 ? 4 : t == 256 ? 2 : 1;
     return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * per));
 }
 

@@ -89,6 +89,15 @@ def test_norm_forward(dt, rows, cols, residual):
     check_norm(x, 1 + 0.3 * rand(g, cols), res, dt)
 
 
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [16, 192, 384, 640, 768, 1024, 1536, 12288])
+def test_norm_forward_of_widths_that_threads_fit_exactly_or_nearly(dt, cols):
+    g = gen(cols)
+    for rows in (1, 5, 67):
+        x, res = (3 * rand(g, rows, cols)).to(DT[dt]), rand(g, rows, cols).to(DT[dt])
+        check_norm(x, 1 + 0.3 * rand(g, cols), res, dt)
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_norm_strides_offsets_and_in_place(dt):
     g = gen(5)
