@@ -13,10 +13,10 @@
 // takes each of their schedulers 8192 multiply-adds, 390 clocks at the rate that two warps reach.  The two overlap,
 // but each accumulator's way round (products, word to the readers, reading, word back) is longer than both, and there
 // is room for two: that, and every instruction between the readers' loads, is what large products wait for.  Products
-// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 236 us alone, 249 back to back (2.2 PFLOP/s;
-// without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 64
-// us (3.9 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us, 1 x 4096 x 4096 9
-// us, the call itself.
+// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 243 us (2.3 PFLOP/s;
+// without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 57
+// us (4.3 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 50 us from a cold cache, 1
+// x 4096 x 4096 9 us, the call itself.
 #include <cuda.h>
 
 #include "wide.cuh"
@@ -34,6 +34,7 @@ struct MatmulArgs {
     void* out; size_t os;
     int vec;                    // rows of out take 16-byte stores
     int splits, tiles_n, tiles;
+    int each, extra;            // blocks a stretch; the first `extra` stretches have one more
     float* part;                // splits > 1: [split][tile][column][128 rows]
 };
 
@@ -219,9 +220,18 @@ struct TileSmem {
     uint8_t stage[kSumWarps][2][32 * 128];  // a warp's way out: twice 32 rows of 128 bytes
 };
 
+// The blocks of a stretch.  Between tiles every warp asks for them, so no division of 64 bits stands here, and unsplit
+// products divide once for a tile: 160,000 x 512 x 512 bfloat16 out 66 -> 60 to 62 us, float32 out 91 -> 85.
 struct Range { int first, last; };
-__device__ __forceinline__ Range split_blocks(int blocks, int splits, int s) {
-    return {int((long long)blocks * s / splits), int((long long)blocks * (s + 1) / splits)};
+__device__ __forceinline__ Range blocks_of(const MatmulArgs& g, int s) {
+    const int first = s * g.each + min(s, g.extra);
+    return {first, first + g.each + (s < g.extra ? 1 : 0)};
+}
+// Unit u is tile u mod tiles of stretch u / tiles.
+struct Unit { int tile; Range r; };
+__device__ __forceinline__ Unit unit_of(const MatmulArgs& g, int u) {
+    const int s = g.splits > 1 ? u / g.tiles : 0;
+    return {u - s * g.tiles, blocks_of(g, s)};
 }
 
 // max(x, 0), a NaN kept.
@@ -289,7 +299,6 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     cluster_sync();  // the other CTA's barriers are set up before anything arrives there
     tc_after();
     const uint32_t tmem = tmem_slot;
-    const int blocks = (g.k + kBlock - 1) / kBlock;
     const int units = g.tiles * g.splits, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
@@ -298,9 +307,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint32_t s = 0, phase = 1, it = 0;
             bool ok = true;
             for (int u = pair; u < units && ok; u += pairs) {
-                const int tile = u % g.tiles, y = (tile / g.tiles_n * 2 + rank) * 128,
-                          x = tile % g.tiles_n * BN + rank * (BN / 2);
-                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                const auto [tile, r] = unit_of(g, u);
+                const int ty = tile / g.tiles_n, y = (ty * 2 + rank) * 128,
+                          x = (tile - ty * g.tiles_n) * BN + rank * (BN / 2);
                 for (int b = r.first; b < r.last; ++b, ++it) {
                     if (!(ok = __all_sync(0xffffffffu, bar_wait(&empty[s], phase)))) break;
                     if (elect_one()) {
@@ -320,7 +329,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint32_t s = 0, phase = 0, h = 0, acc_phase = 1, it = 0;
             bool ok = true, ready = false;
             for (int u = pair; u < units && ok; u += pairs) {
-                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                const Range r = unit_of(g, u).r;
                 for (int b = r.first; b < r.last; ++b, ++it) {
                     ok = (ready || bar_wait(&full[s], phase)) && bar_wait(&acc_empty[h], acc_phase);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
@@ -352,9 +361,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
             };
             for (int u = pair; u < units && ok; u += pairs) {
-                const int tile = u % g.tiles, x = tile % g.tiles_n * BN;
-                const long long y = (long long)(tile / g.tiles_n * 2 + rank) * 128 + lane;
-                const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+                const auto [tile, r] = unit_of(g, u);
+                const int ty = tile / g.tiles_n, x = (tile - ty * g.tiles_n) * BN;
+                const long long y = (long long)(ty * 2 + rank) * 128 + lane;
                 const float* pa = g.sa + size_t(r.first) * g.m;
                 const float* pb = g.sb + size_t(r.first) * per;
                 for (int b = r.first; b < r.last; ++b, pa += g.m, pb += per) {
@@ -390,10 +399,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         uint32_t count = 0;                // of blocks
         bool ok = true;
         for (int u = pair; u < units; u += pairs) {
-            const int tile = u % g.tiles;
-            const long long row0 = (long long)(tile / g.tiles_n * 2 + rank) * 128 + wrow;
-            const int col = tile % g.tiles_n * BN + half * kCols;
-            const Range r = split_blocks(blocks, g.splits, u / g.tiles);
+            const auto [tile, r] = unit_of(g, u);
+            const int ty = tile / g.tiles_n;
+            const long long row0 = (long long)(ty * 2 + rank) * 128 + wrow;
+            const int col = (tile - ty * g.tiles_n) * BN + half * kCols;
             uint64_t acc[kCols / 2];
 #pragma unroll
             for (int j = 0; j < kCols / 2; ++j) acc[j] = 0;
@@ -544,7 +553,7 @@ __global__ void __launch_bounds__(192)
     __syncthreads();
     tc_after();
     const uint32_t tmem = tmem_slot;
-    const Range r = split_blocks((g.k + kBlock - 1) / kBlock, g.splits, rank);
+    const Range r = blocks_of(g, rank);
     const int count = r.last - r.first;
     const int wrow = (warp & 3) * 32 + lane;
     float acc[NT];
@@ -848,9 +857,10 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     if (!encode(&ma, bytes, 1, d_a, a_stride, m, k, p.rows ? p.rows : 128) ||
         !encode(&mb, bytes, 1, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2))
         return RS_ERR_CUDA;
+    const int blocks = ceil_div(k, kBlock);
     const bool vec = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40);
     MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, vec,
-                 p.splits, p.tiles_n, p.tiles, static_cast<float*>(d_workspace)};
+                 p.splits, p.tiles_n, p.tiles, blocks / p.splits, blocks % p.splits, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
         const bool per_row = b_scale_rows == 1;
