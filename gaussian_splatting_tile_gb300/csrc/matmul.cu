@@ -13,9 +13,9 @@
 // takes each of their schedulers 8192 multiply-adds, 390 clocks at the rate that two warps reach.  The two overlap,
 // but each accumulator's way round (products, word to the readers, reading, word back) is longer than both, and there
 // is room for two: that, and every instruction between the readers' loads, is what large products wait for.  Products
-// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 243 us (2.3 PFLOP/s;
+// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 245 us (2.2 PFLOP/s;
 // without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 57
-// us (4.3 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 50 us from a cold cache, 1
+// us (4.3 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us from a cold cache, 1
 // x 4096 x 4096 9 us, the call itself.
 #include <cuda.h>
 
@@ -669,31 +669,46 @@ __global__ void __launch_bounds__(192)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kRowsTmem) : "memory");
 }
 
-// out from the partial sums of `splits` stretches, added in order.  A block takes 8 columns of a tile: thread = row
-// reads 128 consecutive floats a warp group, and the values leave through shared memory along out's rows.
-template <typename T>
-__global__ void __launch_bounds__(256) k_matmul_join(MatmulArgs g, int bn) {
+// out from the partial sums of `splits` stretches. A block takes 8 columns of a tile, each of its GROUPS groups of
+// eight warps every GROUPS-th stretch: a warp reads a column's 128 rows, eight stretches in flight; the groups' sums
+// are added in order (the same every time), and the values leave through shared memory along out's rows.  What bounds
+// it is the time of its loads, one after another. Four groups from ten stretches on, one below, where three would be
+// idle and tiles many: the whole product at 76 stretches (128 x 64 x 160000) 27 us against 44 with one, at 19 (512 x
+// 256 x 160000) 46 against 50, at 10 (1792 x 256 x 40000) 42 against 44, at 9 (512 x 256 x 9300) 19 against 17, at 3
+// (2000 x 700 x 10000) 40 against 31.
+constexpr int kManySplits = 10;
+template <typename T, int GROUPS>
+__global__ void __launch_bounds__(256 * GROUPS) k_matmul_join(MatmulArgs g, int bn) {
     RS_PDL_ENTER();
-    __shared__ float sm[8][129];
+    constexpr int kAtOnce = 8;
+    __shared__ __align__(16) float sm[GROUPS][8][132];  // 132: the reads of 8 columns x 4 rows hit different banks
     const int groups = bn / 8, half = blockIdx.x / groups, tile = half >> 1, c0 = blockIdx.x % groups * 8;
-    const int row = threadIdx.x & 127, cc = (threadIdx.x >> 7) * 4;
-    const float* p = g.part + (size_t(half) * bn + c0 + cc) * 128 + row;
+    const int lane = threadIdx.x & 31, cc = threadIdx.x >> 5 & 7, group = threadIdx.x >> 8;
+    const float* p = g.part + (size_t(half) * bn + c0 + cc) * 128 + lane * 4;
     const size_t step = size_t(g.tiles) * 2 * bn * 128;
-    float v[4] = {};
-#pragma unroll 4
-    for (int s = 0; s < g.splits; ++s)
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = group; s < g.splits; s += GROUPS * kAtOnce) {
+        float4 w[kAtOnce];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] += p[s * step + j * 128];
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int at = s + i * GROUPS;
+            w[i] = at < g.splits ? *reinterpret_cast<const float4*>(p + at * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sm[cc + j][row] = g.relu ? relu(v[j]) : v[j];
+        for (int i = 0; i < kAtOnce; ++i) v.x += w[i].x, v.y += w[i].y, v.z += w[i].z, v.w += w[i].w;
+    }
+    *reinterpret_cast<float4*>(&sm[group][cc][lane * 4]) = v;
     __syncthreads();
     const int c = threadIdx.x & 7;
     const long long col = (long long)(tile % g.tiles_n) * bn + c0 + c;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 32 + int(threadIdx.x >> 3);
-        const long long gr = (long long)(tile / g.tiles_n * 2 + (half & 1)) * 128 + r;
-        if (gr < g.m && col < g.n) static_cast<T*>(g.out)[gr * g.os + col] = from_f<T>(sm[c][r]);
+    for (int i = 0; i < 128; i += 32 * GROUPS) {
+        const int r = i + int(threadIdx.x >> 3);
+        const long long row = (long long)(tile / g.tiles_n * 2 + (half & 1)) * 128 + r;
+        float x = sm[0][c][r];
+#pragma unroll
+        for (int j = 1; j < GROUPS; ++j) x += sm[j][c][r];
+        if (row < g.m && col < g.n) static_cast<T*>(g.out)[row * g.os + col] = from_f<T>(g.relu ? relu(x) : x);
     }
 }
 
@@ -711,10 +726,11 @@ struct Plan {
 //  - 256 columns a tile move the fewest bytes and cost the fewest instructions a product, but with few tiles and
 //    little work for each pair of SMs, 128 columns spread it further: 2000 x 1000 x 2000 (32 wide tiles, 7 blocks a
 //    pair) 11.7 against 16.5 us, 1000 x 1000 x 3000 14.7 against 17.7; with more of either the other way, 4000 x 1000
-//    x 700 (64 tiles) 10.9 against 9.4, 2000 x 700 x 10000 (25 blocks a pair) 41.2 against 33.3.  With one or two
-//    wide tiles the split sums count: 512 x 256 x 160000 45 against 50.
-//  - Fewer tiles than pairs: the blocks are split among them, at least 8 to a stretch (4: 256 x 256 x 20000 23
-//    against 13 us).
+//    x 700 (64 tiles) 10.9 against 9.4, 2000 x 700 x 10000 (25 blocks a pair) 41.2 against 33.3.  With one wide tile
+//    the split sums count: 256 x 256 x 160000 35 against 38 to 40 us; with two (512 x 256 x 160000) both take 45, and
+//    128 columns half of the workspace.
+//  - Fewer tiles than pairs: the blocks are split among them, at least 8 to a stretch (256 x 256 x 20000 17 us, with
+//    4 19 to 20, with 16 19).
 Plan plan_matmul(int m, int n, int k) {
     Plan p{};
     const int blocks = ceil_div(k, kBlock);
@@ -874,7 +890,10 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     });
     if (e == cudaSuccess && need > 0)
         e = with_dtype(out_dtype, [&](auto v) {
-            return pdl_launch(k_matmul_join<decltype(v)>, unsigned(p.tiles) * 2 * (p.bn / 8), 256, 0, s, g, p.bn);
+            using T = decltype(v);
+            const bool many = p.splits >= kManySplits;
+            return pdl_launch(many ? k_matmul_join<T, 4> : k_matmul_join<T, 1>, unsigned(p.tiles) * 2 * (p.bn / 8),
+                              many ? 1024 : 256, 0, s, g, p.bn);
         });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }

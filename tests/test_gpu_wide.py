@@ -368,6 +368,25 @@ def test_matmul(m, n, k, blocks):
     close(matmul(a, sa, b, sb, relu=True), want.clamp_min(0), tol)
 
 
+# long contractions of few tiles are split and joined: 9, 10, 38 and 76 stretches of blocks
+@pytest.mark.parametrize("m,n,k", [(300, 140, 10100), (300, 140, 10300), (130, 60, 39000), (70, 50, 80001)])
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+def test_matmul_split_sums(m, n, k, dt):
+    g = gen(m + n * 3 + k * 5)
+    a, sa, b, sb = operands(g, m, n, k, False)
+    sb = sb * (1 / max(1.0, float(product(a, sa, b, sb)[0].abs().max()))) * 100     # inside float16's range
+    want, mags = product(a, sa, b, sb)
+    tol = (128 + k / 128 + 4) * 2 * U * mags
+    if dt != "f32":
+        tol = tol + HALF_ULP[dt] * want.abs() * 1.01 + 2.0 ** -24
+    wide = torch.full((m, n + 3), 7.0, dtype=DT[dt], device="cuda")
+    got = matmul(a, sa, b, sb, dt, out=wide[:, 1:1 + n])
+    close(got, want, tol)
+    assert bool((wide[:, :1] == 7.0).all()) and bool((wide[:, 1 + n:] == 7.0).all())
+    assert torch.equal(got, matmul(a, sa, b, sb, dt))
+    assert torch.equal(matmul(a, sa, b, sb, dt, relu=True), got.clamp_min(0))
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 100, 200), (40, 100, 200), (300, 260, 200)])
 def test_matmul_strides_and_untouched_memory(m, n, k):
     g = gen(3)
