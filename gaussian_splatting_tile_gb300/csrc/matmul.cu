@@ -219,6 +219,11 @@ struct TileSmem {
     uint8_t b[kStages][BN / 2 * 128];
     uint8_t stage[kSumWarps][2][32 * 128];  // a warp's way out: twice 32 rows of 128 bytes
 };
+// A pair holds all of tensor memory of an SM while it waits for its other half to get the same.  No other pair may be in
+// its way: two CTAs of them do not fit an SM's shared memory.  (Whatever else holds tensor memory frees it without waiting
+// for another CTA.)
+constexpr size_t kSmemSm = 228 * 1024;
+static_assert(2 * sizeof(TileSmem<128>) > kSmemSm && 2 * sizeof(TileSmem<256>) > kSmemSm, "one pair's CTA an SM");
 
 // The blocks of a stretch.  Between tiles every warp asks for them, so no division of 64 bits stands here, and unsplit
 // products divide once for a tile: 160,000 x 512 x 512 bfloat16 out 66 -> 60 to 62 us, float32 out 91 -> 85.
@@ -633,8 +638,14 @@ __global__ void __launch_bounds__(192)
         if (g.relu) v = relu(v);
         static_cast<T*>(g.out)[size_t(j) * g.os + n] = from_f<T>(v);
     };
-    // every role is done with the operands' memory after this barrier: the sums take their place
+    // Every role is done with the operands' memory and with tensor memory after this barrier.  The sums take the former's
+    // place; the latter goes back before the first wait for the cluster, whose other CTAs may still be asking for theirs
+    // on SMs where such CTAs of other launches hold it.
+    tc_before();
     const bool all = __syncthreads_and(ok);
+    tc_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kRowsTmem) : "memory");
     if (g.splits == 1) {
         if (warp >= 2 && all && n < g.n) {
 #pragma unroll
@@ -662,11 +673,6 @@ __global__ void __launch_bounds__(192)
         }
         cluster_sync();  // no CTA's memory goes while another reads it
     }
-    tc_before();
-    __syncthreads();
-    tc_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kRowsTmem) : "memory");
 }
 
 // out from the partial sums of `splits` stretches. A block takes 8 columns of a tile, each of its GROUPS groups of

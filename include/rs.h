@@ -517,9 +517,11 @@ int rs_quantize_fp8_blocks(int32_t rows, int32_t cols, int32_t dtype, const void
  * backward is the same product: dL_dx = dY W with the transposed weights of
  * rs_quantize_fp8_blocks, dW = dY^T X with the transposed forms of rs_quantize_fp8. m, n, k >= 0;
  * k = 0 gives zeros.  d_workspace: rs_matmul_fp8_workspace_size bytes (0: none needed, may be
- * NULL), 16-byte aligned, contents undefined on entry and exit.  The kernels' waits are bounded;
- * one that gives up leaves its part of the output unwritten and raises the flag rs_device_error
- * reports. Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
+ * NULL), 16-byte aligned, contents undefined on entry and exit.  The kernels' waits for
+ * their own copies and products are bounded; one that gives up leaves its part of the output
+ * unwritten and raises the flag rs_device_error reports.  (For tensor memory a kernel waits as
+ * long as kernels of other streams hold it; none of this library's holds it while it waits for
+ * one that may still be asking.)  Errors: RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
 size_t rs_matmul_fp8_workspace_size(int32_t m, int32_t n, int32_t k);
 int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride,
                   const float* d_a_scales, const uint8_t* d_b, size_t b_stride, const float* d_b_scales,
