@@ -7,12 +7,10 @@
 
 #include <cmath>
 
+#include "matmul_plan.h"
 #include "rs_internal.cuh"
 
 namespace rs {
-
-constexpr int kBlock = RS_FP8_BLOCK;
-constexpr int kSms = 152;
 
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
@@ -254,7 +252,6 @@ inline bool rows16(const void* p, size_t stride, size_t size) {
 inline bool fp8_rows_ok(const void* p, size_t stride, int32_t cols) {
     return ptr_ok(p, 16) && stride % 16 == 0 && stride >= size_t(cols);
 }
-inline int ceil_div(long long a, long long b) { return int((a + b - 1) / b); }
 
 // Calls f with a value of the element type.
 template <typename F>
