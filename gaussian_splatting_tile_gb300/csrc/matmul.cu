@@ -32,7 +32,7 @@ struct MatmulArgs {
     const float* sb;            // [blocks][n], or [blocks][ceil(n / 128)]
     int relu;
     void* out; size_t os;
-    int vec;                    // rows of out take 16-byte stores
+    int tma_cols;               // columns of out that TMA writes, a multiple of 16 bytes (0: none)
     int splits, tiles_n, tiles;
     int each, extra;            // blocks a stretch; the first `extra` stretches have one more
     float* part;                // splits > 1: [split][tile][column][128 rows]
@@ -265,6 +265,16 @@ __device__ __forceinline__ void copy_rows(const uint8_t* st, T* o, size_t os, lo
                 o[r * os + c] =
                     *reinterpret_cast<const T*>(st + r * 128 + (((c / kPer) ^ (r & 7)) << 4) + c % kPer * sizeof(T));
 }
+// The last columns [first, cols) of this lane's row, fewer than 16 bytes, where the row ends inside these 128 bytes.
+template <typename T>
+__device__ __forceinline__ void copy_rest(const uint8_t* st, T* o, int first, int cols, int lane) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (first < 0 || first >= 8 * kPer || first >= cols) return;
+    const T* w = reinterpret_cast<const T*>(st + lane * 128 + (((first / kPer) ^ (lane & 7)) << 4));
+    for (int c = first; c < cols; ++c) o[c] = w[c - first];
+}
+// TMA leaves out the box's columns past the tensor's only in whole words of 16 bytes: the map of out ends with the last
+// whole word (tma_cols), and copy_rest writes what is left.
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* src, int x, int y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
@@ -473,7 +483,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kPasses; c += kTogether) {
                     // what was copied out of the buffers before has left them
-                    if (g.vec && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    if (g.tma_cols && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                     __syncwarp();
 #pragma unroll
                     for (int q = 0; q < kTogether; ++q) {
@@ -492,18 +502,23 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         }
                         stage_rows(sm.stage[w8][q], w, lane);
                     }
-                    if (g.vec) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (g.tma_cols) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
 #pragma unroll
                     for (int q = 0; q < kTogether; ++q) {
                         const int x = col + (c + q) * kOnce;
-                        if (!g.vec)
+                        if (!g.tma_cols) {
                             copy_rows(sm.stage[w8][q], static_cast<T*>(g.out) + row0 * g.os + x, g.os, g.m - row0,
                                       g.n - x, lane);
-                        else if (lane == 0 && row0 < g.m && x < g.n)
-                            tma_store(&map_out, sm.stage[w8][q], x, int(row0));
+                        } else {
+                            if (lane == 0 && row0 < g.m && x < g.tma_cols)
+                                tma_store(&map_out, sm.stage[w8][q], x, int(row0));
+                            if (row0 + lane < g.m)
+                                copy_rest(sm.stage[w8][q], static_cast<T*>(g.out) + (row0 + lane) * g.os + x,
+                                          g.tma_cols - x, g.n - x, lane);
+                        }
                     }
-                    if (g.vec && lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    if (g.tma_cols && lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
         }
@@ -771,7 +786,8 @@ cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const Matmul
     CUtensorMap out{};
     constexpr CUtensorMapDataType type =
         sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
-    if (g.vec && g.splits == 1 && !encode(&out, type, sizeof(T), g.out, g.os, g.m, g.n, 32)) return cudaErrorUnknown;
+    if (g.tma_cols && g.splits == 1 && !encode(&out, type, sizeof(T), g.out, g.os, g.m, g.tma_cols, 32))
+        return cudaErrorUnknown;
     constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
     // the kernel's register split counts on what it is launched with
     static const bool enough = [] {
@@ -840,8 +856,9 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
         !encode(&mb, bytes, 1, d_b, b_stride, n, k, p.rows ? 128 : p.bn / 2))
         return RS_ERR_CUDA;
     const int blocks = ceil_div(k, kBlock);
-    const bool vec = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40);
-    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, vec,
+    const int whole = n / int(16 / z) * int(16 / z);  // columns in whole words of 16 bytes
+    const int tma_cols = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40) ? whole : 0;
+    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, tma_cols,
                  p.splits, p.tiles_n, p.tiles, blocks / p.splits, blocks % p.splits, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
