@@ -19,6 +19,8 @@
 // x 4096 x 4096 9 us, the call itself.
 #include <cuda.h>
 
+#include <cfloat>
+
 #include "wide.cuh"
 
 namespace rs {
@@ -28,6 +30,8 @@ __device__ unsigned int g_matmul_error;  // set when a bounded wait gave up
 
 struct MatmulArgs {
     int m, n, k;
+    const uint8_t* a; size_t as;
+    const uint8_t* b; size_t bs;
     const float* sa;            // [blocks][m]
     const float* sb;            // [blocks][n], or [blocks][ceil(n / 128)]
     int relu;
@@ -196,7 +200,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA
 // holds 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is
 // fetched and stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warp 2 of each
-// fetches the scales, warps 4 to 11 of both add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a
+// fetches the scales, warp 3 checks them, warps 4 to 11 of both add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a
 // half of the columns. Tensor memory holds kAcc accumulators of BN columns: the products of the next blocks run while
 // a block is read.
 //
@@ -280,10 +284,89 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
                  ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
+// ---- scales whose product is no normal float32
+// With a scale per 128 rows of b the two scales are multiplied first, once for a row and block.  Where that leaves the
+// normal numbers (below 2^-126 bits are lost, above 2^128 it is infinite) though the block's sum would bring the result
+// back, the row's results are formed anew by its thread after the tiles, one scale after the other.  Warp 3 looks
+// for such products as the scales pass by, and back to back that costs nothing (160,000 x 512 x 512 55.8 against 56.0 us
+// without, 65536 x 2048 x 2048 223 against 224); from a cold L2 the longer code takes a microsecond or two to come.
+// A second way through the loop that adds the blocks up cost 10 to 20 percent of wide products, remembering there that
+// such a product was met 3 to 5.
+__device__ __forceinline__ bool normal(float f) { return fabsf(f) >= FLT_MIN && fabsf(f) <= FLT_MAX; }
+
+// Whether some block of a stretch needs that: the product of its scales is not normal, and not only small because all of
+// the row's values are zero (their scale is 2^-109: with small weights that is common, and the sum is zero either way).
+__device__ __forceinline__ bool scales_apart(const MatmulArgs& g, Range r, long long row, int col) {
+    const int per = (g.n + kBlock - 1) / kBlock;
+#pragma unroll 1
+    for (int b = r.first; b < r.last; ++b) {
+        const float fa = g.sa[size_t(b) * g.m + row], fb = g.sb[size_t(b) * per + col / kBlock];
+        if (normal(fa * fb) || fa == 0.f || fb == 0.f) continue;
+        if (!(fabsf(fa * fb) < FLT_MIN)) return true;
+        const uint8_t* a = g.a + row * g.as + size_t(b) * kBlock;
+        const int len = min(kBlock, g.k - b * kBlock);
+        uint32_t any = 0;
+#pragma unroll
+        for (int t = 0; t < kBlock; t += 16)
+            if (t + 16 <= len) {
+                const uint4 w = *reinterpret_cast<const uint4*>(a + t);
+                any |= w.x | w.y | w.z | w.w;
+            }
+        for (int t = len & ~15; t < len; ++t) any |= a[t];
+        if (any & 0x7f7f7f7fu) return true;
+    }
+    return false;
+}
+
+// Calls put(j, value) for this row's columns col + j, j < cols.
+template <typename Put>
+__device__ __forceinline__ void row_anew(const MatmulArgs& g, Range r, long long row, int col, int cols, Put&& put) {
+    const int per = (g.n + kBlock - 1) / kBlock;
+#pragma unroll 1
+    for (int j = 0; j < cols && col + j < g.n; ++j) {
+        float v = 0.f;
+#pragma unroll 1
+        for (int b = r.first; b < r.last; ++b) {
+            const uint8_t* x = g.a + row * g.as + size_t(b) * kBlock;
+            const uint8_t* y = g.b + (col + j) * g.bs + size_t(b) * kBlock;
+            const int len = min(kBlock, g.k - b * kBlock);
+            float sum = 0.f;
+#pragma unroll 1
+            for (int t = 0; t < len; ++t) {
+                uint32_t xy;  // the two values as halves
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(xy) : "h"(uint16_t(x[t] | y[t] << 8)));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&xy));
+                sum = fmaf(f.x, f.y, sum);
+            }
+            v = fmaf(sum * g.sb[size_t(b) * per + (col + j) / kBlock], g.sa[size_t(b) * g.m + row], v);
+        }
+        put(j, v);
+    }
+}
+
+// A thread's row and columns of the pair's tiles, where they need it.  Out of line: rarely called, and inlined it lies in
+// the way of the code that always runs.
+template <typename T, int BN>
+__device__ __noinline__ void units_anew(const MatmulArgs& g, int pair, int pairs, int rank, int lane_row, int half) {
+    constexpr int kCols = BN / (kSumWarps / 4);
+    for (int u = pair; u < g.tiles * g.splits; u += pairs) {
+        const auto [tile, r] = unit_of(g, u);
+        const int ty = tile / g.tiles_n, col = (tile - ty * g.tiles_n) * BN + half * kCols;
+        const long long row = (long long)(ty * 2 + rank) * 128 + lane_row;
+        if (row >= g.m || col >= g.n || !scales_apart(g, r, row, col)) continue;
+        float* part = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + lane_row;
+        T* out = static_cast<T*>(g.out) + row * g.os + col;
+        row_anew(g, r, row, col, kCols, [&](int j, float x) {
+            if (g.splits > 1) part[size_t(j) * 128] = x;
+            else out[j] = from_f<T>(g.relu ? relu(x) : x);
+        });
+    }
+}
+
 template <typename T, int BN, bool ROWS>
 __global__ void __launch_bounds__(kTileThreads, 1)
     k_matmul_tile(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const __grid_constant__ CUtensorMap map_out, MatmulArgs g) {
+                  const __grid_constant__ CUtensorMap map_out, const __grid_constant__ MatmulArgs g) {
     RS_PDL_ENTER();
     using Smem = TileSmem<BN>;
     constexpr int kStages = Smem::kStages, kAcc = Smem::kAcc, kCols = BN / (kSumWarps / 4);
@@ -296,11 +379,12 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     constexpr int kRing = 16, kGroups = kRing / 4, kScales = 128 + (ROWS ? BN : 4);
     __shared__ __align__(16) float scales[kRing][kScales];
     __shared__ uint64_t sc_full[kGroups], sc_empty[kGroups];
+    __shared__ bool apart_met;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rank = blockIdx.x & 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
         for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 2 * kSumWarps);
-        for (int i = 0; i < kGroups; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps);
+        for (int i = 0; i < kGroups; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps + !ROWS);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -401,6 +485,35 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (count % 4 != 0) done();
             asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (!ROWS && warp == 3) {
+            // The largest and smallest magnitudes of four rows and of b's scales bound the products of a block.
+            uint32_t count = 0;
+            bool ok = true;
+            float least = 1.f, most = 1.f;
+            for (int u = pair; u < units && ok; u += pairs) {
+                const Range r = unit_of(g, u).r;
+                for (int b = r.first; b < r.last; ++b, ++count) {
+                    const uint32_t group = (count >> 2) % kGroups;
+                    if (count % 4 == 0 &&
+                        !(ok = __all_sync(0xffffffffu, bar_wait(&sc_full[group], count / kRing & 1))))
+                        break;
+                    const float* sc = scales[count % kRing];
+                    const float4 a = reinterpret_cast<const float4*>(sc)[lane];
+                    const float2 s = *reinterpret_cast<const float2*>(sc + 128);
+                    const float lo = fminf(fminf(fabsf(a.x), fabsf(a.y)), fminf(fabsf(a.z), fabsf(a.w)));
+                    const float hi = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
+                    least = fminf(least, lo * fminf(fabsf(s.x), fabsf(s.y)));
+                    most = fmaxf(most, hi * fmaxf(fabsf(s.x), fabsf(s.y)));
+                    if (count % 4 == 3) {
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(smem_u32(&sc_empty[group]));
+                    }
+                }
+            }
+            const bool met = __any_sync(0xffffffffu, !(least >= FLT_MIN && most <= FLT_MAX));
+            if (lane == 0) apart_met = met;
+            __syncwarp();
+            asm volatile("bar.arrive 1, %0;" ::"n"(32 + 32 * kSumWarps) : "memory");
         }
         __syncwarp();
     } else {
@@ -524,6 +637,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // no copy outlasts the CTA
         __syncwarp();
+        if constexpr (!ROWS) {
+            asm volatile("bar.sync 1, %0;" ::"n"(32 + 32 * kSumWarps) : "memory");
+            if (ok && apart_met) units_anew<T, BN>(g, pair, pairs, rank, wrow + lane, half);
+            __syncwarp();
+        }
     }
     tc_before();
     __syncthreads();
@@ -858,7 +976,7 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     const int blocks = ceil_div(k, kBlock);
     const int whole = n / int(16 / z) * int(16 / z);  // columns in whole words of 16 bytes
     const int tma_cols = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40) ? whole : 0;
-    MatmulArgs g{m, n, k, d_a_scales, d_b_scales, relu, d_out, out_stride, tma_cols,
+    MatmulArgs g{m, n, k, d_a, a_stride, d_b, b_stride, d_a_scales, d_b_scales, relu, d_out, out_stride, tma_cols,
                  p.splits, p.tiles_n, p.tiles, blocks / p.splits, blocks % p.splits, static_cast<float*>(d_workspace)};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);

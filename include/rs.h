@@ -513,7 +513,9 @@ int rs_quantize_fp8_blocks(int32_t rows, int32_t cols, int32_t dtype, const void
  * a [m][k], b [n][k] (a linear layer's weights as they are stored), out [m][n] of out_dtype.
  * b_scale_rows: 1 when d_b_scales is [ceil(k / 128)][n] (a scale per row of b, as a's), 128 when
  * it is [ceil(k / 128)][ceil(n / 128)] (a scale per 128 rows).  relu != 0: negative results
- * become zero (NaN stays). The sums are float32, in an order that the sizes alone fix.  A layer's
+ * become zero (NaN stays). The sums are float32, in an order that the sizes alone fix; a block's
+ * sum is multiplied by its two scales so that their product may leave float32's range as long as
+ * the sum times either scale stays in it (scales from 2^-109 to 2^102 always do).  A layer's
  * backward is the same product: dL_dx = dY W with the transposed weights of
  * rs_quantize_fp8_blocks, dW = dY^T X with the transposed forms of rs_quantize_fp8. m, n, k >= 0;
  * k = 0 gives zeros.  d_workspace: rs_matmul_fp8_workspace_size bytes (0: none needed, may be
