@@ -185,6 +185,7 @@ uint64_t fill(ClipTable<N>& T, const rs_grad_tensor* t, int n, int first) {
 }
 
 int launches(int n) { return std::max(1, ceil_div(n, kTable)); }
+size_t parts_bytes(int n) { return size_t(launches(n)) * kNormBlocks * sizeof(float); }
 
 // Partial sums of every launch, kNormBlocks each at most; *parts tells how many were written.
 template <int N>
@@ -246,7 +247,7 @@ int check(const rs_grad_tensor* t, int32_t n, bool outs, const float* d_norm, co
 extern "C" {
 
 size_t rs_grad_norm_workspace_size(int32_t n_tensors) {
-    return n_tensors < 0 ? 0 : size_t(rs::launches(n_tensors)) * rs::kNormBlocks * sizeof(float);
+    return n_tensors < 0 ? 0 : rs::parts_bytes(n_tensors) + 16;  // 16: the counted step's
 }
 
 int rs_grad_norm(const rs_grad_tensor* tensors, int32_t n_tensors, float* d_norm, void* d_workspace,
@@ -277,9 +278,9 @@ int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_nor
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
-int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
-                         int32_t step, float max_norm, float* d_norm, void* d_workspace, size_t workspace_bytes,
-                         void* stream) {
+static int adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
+                             int32_t step, int32_t* d_steps, float max_norm, float* d_norm, void* d_workspace,
+                             size_t workspace_bytes, void* stream) {
     using namespace rs;
     if (!adam_args_ok(segs, n_segs, beta1, beta2, eps, step) || !(max_norm > 0.f)) return RS_ERR_INVALID_ARG;
     if (!ptr_ok(d_norm, 4) || !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
@@ -289,9 +290,24 @@ int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double bet
         t[i] = {segs[i].d_grad, nullptr, segs[i].d_param, segs[i].count, RS_F32, segs[i].activation};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     float* ws = static_cast<float*>(d_workspace);
-    ClipBy by{ws, 0, max_norm, d_norm};
+    ClipBy by{ws, 0, max_norm, d_norm, d_steps, static_cast<char*>(d_workspace) + parts_bytes(n_segs)};
     if (norm_parts(t, n_segs, ws, &by.parts, s) != cudaSuccess) return RS_ERR_CUDA;
     return launch_adam(segs, n_segs, beta1, beta2, eps, step, s, &by) == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
+                         int32_t step, float max_norm, float* d_norm, void* d_workspace, size_t workspace_bytes,
+                         void* stream) {
+    return adam_step_clipped(segs, n_segs, beta1, beta2, eps, step, nullptr, max_norm, d_norm, d_workspace,
+                             workspace_bytes, stream);
+}
+
+int rs_adam_step_clipped_counted(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2, double eps,
+                                 int32_t* d_steps, float max_norm, float* d_norm, void* d_workspace,
+                                 size_t workspace_bytes, void* stream) {
+    if (!rs::ptr_ok(d_steps, 4)) return RS_ERR_INVALID_ARG;
+    return adam_step_clipped(segs, n_segs, beta1, beta2, eps, 1, d_steps, max_norm, d_norm, d_workspace,
+                             workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -13,6 +13,12 @@
 namespace rs {
 namespace {
 
+// What k_adam_begin leaves for the counted step.
+struct StepState {
+    float coef, rc1, rc2;
+    int32_t go;  // 0: the norm is not finite
+};
+
 // Per group: `quads` runs of four elements moved with 16-byte loads and stores (when every
 // pointer of the group is 16-byte aligned), then the remaining elements one at a time.
 struct AdamTable {
@@ -26,10 +32,11 @@ struct AdamTable {
     int parts;                                      // how many, the limit, and where the norm goes
     float max_norm;
     float* norm;
+    const StepState* state;                         // the counted step
 };
 
-__device__ __forceinline__ float adam_one(const AdamTable& T, int act, float lr, float& p, float g, float& m,
-                                          float& v) {
+__device__ __forceinline__ float adam_one(const AdamTable& T, float rc1, float rc2, int act, float lr, float& p, float g,
+                                          float& m, float& v) {
     if (act == RS_ACT_EXP) {
         g *= expf(p);                       // d exp(p)/dp = exp(p)
     } else if (act == RS_ACT_SIGMOID) {
@@ -40,19 +47,55 @@ __device__ __forceinline__ float adam_one(const AdamTable& T, int act, float lr,
     // float32 when it is small next to g^2 (as in the first steps)
     m = fmaf(T.beta1, m, T.omb1 * g);
     v = fmaf(T.beta2, v, T.omb2 * (g * g));
-    p -= lr * (m * T.rc1) / (sqrtf(v * T.rc2) + T.eps);
+    p -= lr * (m * rc1) / (sqrtf(v * rc2) + T.eps);
     return act == RS_ACT_EXP ? expf(p) : act == RS_ACT_SIGMOID ? 1.0f / (1.0f + expf(-p)) : p;
 }
 
-// CLIP: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by
+// 1 / (1 - beta^t), beta^t by repeated squaring: its relative error is about t 2^-53, that of 1 - beta^t at most
+// 2^-53 / (1 - beta), far below float32's.
+__device__ __forceinline__ float bias_correction(double beta, int t) {
+    double power = 1.0;
+    for (; t; t >>= 1, beta *= beta)
+        if (t & 1) power *= beta;
+    return float(1.0 / (1.0 - power));
+}
+
+// The counted step's beginning: norm, clipping factor and, where the norm is finite, the step's number and its bias
+// corrections.  A launch of its own, one block: the count is written before any block of the step reads what came of it.
+__global__ void __launch_bounds__(256) k_adam_begin(const float* part, int parts, float max_norm, float* d_norm,
+                                                    int32_t* steps, double beta1, double beta2, StepState* state) {
+    RS_PDL_ENTER();
+    const float norm = norm_of_parts(part, parts);
+    if (threadIdx.x != 0) return;
+    *d_norm = norm;
+    StepState s{clip_factor(max_norm, norm), 0.f, 0.f, isfinite(norm) ? 1 : 0};
+    if (s.go) {
+        const int before = max(*steps, 0), t = before < 0x7fffffff ? before + 1 : before;
+        *steps = t;
+        s.rc1 = bias_correction(beta1, t);
+        s.rc2 = bias_correction(beta2, t);
+    }
+    *state = s;
+}
+
+// kClip: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by
 // itself (a few KB in L2; a launch fewer than a kernel between); a norm that is not finite leaves everything as it
 // is.  Six blocks an SM as without it: 1M Gaussians 306 us with the norm's 52, 312 us with five blocks; going
 // backwards, where L2 might still hold the norm's last reads, gave nothing (308).
-template <bool CLIP>
-__global__ void __launch_bounds__(256, CLIP ? 6 : 1) k_adam(const __grid_constant__ AdamTable T) {
+// kCounted: the same from what k_adam_begin left.
+enum AdamMode { kPlain, kClip, kCounted };
+template <AdamMode MODE>
+__global__ void __launch_bounds__(256, MODE == kPlain ? 1 : 6) k_adam(const __grid_constant__ AdamTable T) {
     RS_PDL_ENTER();
-    float coef = 1.f;
-    if constexpr (CLIP) {
+    constexpr bool CLIP = MODE != kPlain;
+    float coef = 1.f, rc1 = T.rc1, rc2 = T.rc2;
+    if constexpr (MODE == kCounted) {
+        const StepState s = *T.state;
+        if (!s.go) return;
+        coef = s.coef;
+        rc1 = s.rc1;
+        rc2 = s.rc2;
+    } else if constexpr (MODE == kClip) {
         const float norm = norm_of_parts(T.part, T.parts);
         if (blockIdx.x == 0 && threadIdx.x == 0) *T.norm = norm;
         if (!isfinite(norm)) return;
@@ -71,10 +114,10 @@ __global__ void __launch_bounds__(256, CLIP ? 6 : 1) k_adam(const __grid_constan
         float4 m = reinterpret_cast<const float4*>(S.d_m)[k];
         float4 v = reinterpret_cast<const float4*>(S.d_v)[k];
         float4 a;
-        a.x = adam_one(T, S.activation, S.lr, p.x, g.x, m.x, v.x);
-        a.y = adam_one(T, S.activation, S.lr, p.y, g.y, m.y, v.y);
-        a.z = adam_one(T, S.activation, S.lr, p.z, g.z, m.z, v.z);
-        a.w = adam_one(T, S.activation, S.lr, p.w, g.w, m.w, v.w);
+        a.x = adam_one(T, rc1, rc2, S.activation, S.lr, p.x, g.x, m.x, v.x);
+        a.y = adam_one(T, rc1, rc2, S.activation, S.lr, p.y, g.y, m.y, v.y);
+        a.z = adam_one(T, rc1, rc2, S.activation, S.lr, p.z, g.z, m.z, v.z);
+        a.w = adam_one(T, rc1, rc2, S.activation, S.lr, p.w, g.w, m.w, v.w);
         reinterpret_cast<float4*>(S.d_m)[k] = m;
         reinterpret_cast<float4*>(S.d_v)[k] = v;
         reinterpret_cast<float4*>(S.d_param)[k] = p;
@@ -87,7 +130,7 @@ __global__ void __launch_bounds__(256, CLIP ? 6 : 1) k_adam(const __grid_constan
         const rs_adam_segment& S = T.seg[s];
         const size_t k = 4 * T.quads[s] + (i - T.tstart[s]);
         float p = S.d_param[k], m = S.d_m[k], v = S.d_v[k];
-        const float a = adam_one(T, S.activation, S.lr, p, CLIP ? S.d_grad[k] * coef : S.d_grad[k], m, v);
+        const float a = adam_one(T, rc1, rc2, S.activation, S.lr, p, CLIP ? S.d_grad[k] * coef : S.d_grad[k], m, v);
         S.d_m[k] = m;
         S.d_v[k] = v;
         S.d_param[k] = p;
@@ -140,9 +183,14 @@ cudaError_t launch_adam(const rs_adam_segment* segs, int n, double beta1, double
         T.parts = clip->parts;
         T.max_norm = clip->max_norm;
         T.norm = clip->norm;
-        return pdl_launch(k_adam<true>, blocks, 256, 0, s, T);
+        if (!clip->steps) return pdl_launch(k_adam<kClip>, blocks, 256, 0, s, T);
+        StepState* state = static_cast<StepState*>(clip->state);
+        T.state = state;
+        const cudaError_t e = pdl_launch(k_adam_begin, 1, 256, 0, s, clip->part, clip->parts, clip->max_norm, clip->norm,
+                                         clip->steps, beta1, beta2, state);
+        return e != cudaSuccess ? e : pdl_launch(k_adam<kCounted>, blocks, 256, 0, s, T);
     }
-    pdl_launch(k_adam<false>, blocks, 256, 0, s, T);
+    pdl_launch(k_adam<kPlain>, blocks, 256, 0, s, T);
     return cudaGetLastError();
 }
 

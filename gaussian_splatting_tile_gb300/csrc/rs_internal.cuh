@@ -317,6 +317,8 @@ struct ClipBy {
     int parts;
     float max_norm;
     float* norm;
+    int32_t* steps = nullptr;   // the number of steps taken, on the device (its step is one more) ...
+    void* state = nullptr;      // ... and 16 bytes for what is formed of it; nullptr: the host's step number counts
 };
 cudaError_t launch_adam(const rs_adam_segment* segs, int n, double beta1, double beta2, double eps, int step,
                         cudaStream_t s, const ClipBy* clip = nullptr);

@@ -333,7 +333,7 @@ class WideAppearance:
         self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.moments = None
-        self.steps = 0
+        self.steps = torch.zeros(1, dtype=torch.int32, device=dev)  # taken so far: skipped ones do not count
 
     def _product(self, a, b, b_scales, out, relu=False):
         rs.rs_matmul_fp8(*a, b, b_scales, out, self.workspace, relu=relu)
@@ -390,12 +390,15 @@ class WideAppearance:
 
     def step(self, max_norm: float, lr: float = 1e-3, groups=(), stream=None):
         """One clipped Adam step over the network and `groups` (rs.AdamGroup, e.g. the geometry's); the norm before
-        clipping is in self.norm."""
+        clipping is in self.norm.  In a captured step `lr`, `max_norm` and the groups' rates are those of the capture; the
+        step's number is counted on the device."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
             if self.moments is None:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("the moments have to exist before a step is captured (each replay would begin with "
+                                       "zeros): take one step first")
                 self.moments = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _ in self.parameters()]
             own = [rs.AdamGroup(p, g, m, v, lr) for (p, g), (m, v) in zip(self.parameters(), self.moments)]
-            self.steps += 1
             rs.rs_adam_step_clipped([*own, *groups], self.steps, max_norm, self.norm, self.workspace)
             for layer in (*self.up, *self.down, self.head):
                 layer.refresh()

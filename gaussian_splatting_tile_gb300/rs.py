@@ -163,6 +163,8 @@ def lib():
         L.rs_grad_clip.argtypes = [_VP, i32, ctypes.c_float, _VP, _VP, sz, _VP]
         L.rs_adam_step_clipped.argtypes = [ctypes.POINTER(rs_adam_segment), i32, ctypes.c_double, ctypes.c_double,
                                            ctypes.c_double, i32, ctypes.c_float, _VP, _VP, sz, _VP]
+        L.rs_adam_step_clipped_counted.argtypes = [ctypes.POINTER(rs_adam_segment), i32, ctypes.c_double, ctypes.c_double,
+                                                   ctypes.c_double, _VP, ctypes.c_float, _VP, _VP, sz, _VP]
         for ret, name in declared_signatures():
             getattr(L, name).restype = _RESTYPES[ret]
         _lib = L
@@ -900,12 +902,16 @@ def rs_grad_clip(tensors, max_norm: float, norm: torch.Tensor, workspace: torch.
                                               _stream(stream)))
 
 
-def rs_adam_step_clipped(groups, step: int, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor,
+def rs_adam_step_clipped(groups, step, max_norm: float, norm: torch.Tensor, workspace: torch.Tensor,
                          beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-15, stream=None):
     """rs_adam_step on the gradients clipped to the global norm max_norm (nothing waits on the host; a norm that is not
-    finite skips the step)."""
+    finite skips the step).  step: the step's number, or an int32 CUDA tensor [1] that counts the steps taken, which the
+    call raises by one unless it skips the step (needed in a captured call, whose number would stay the same)."""
     arr = _adam_segments(groups)
-    _check("rs_adam_step_clipped", lib().rs_adam_step_clipped(
-        arr, len(groups), float(beta1), float(beta2), float(eps), int(step), float(max_norm),
+    counted = isinstance(step, torch.Tensor)
+    name = "rs_adam_step_clipped_counted" if counted else "rs_adam_step_clipped"
+    _check(name, getattr(lib(), name)(
+        arr, len(groups), float(beta1), float(beta2), float(eps),
+        _vec(step, torch.int32, 1, "step") if counted else int(step), float(max_norm),
         _vec(norm, torch.float32, 1, "norm"), _vec(workspace, torch.uint8, 0, "workspace"), workspace.numel(),
         _stream(stream)))

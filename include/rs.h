@@ -562,10 +562,18 @@ int rs_grad_clip(const rs_grad_tensor* tensors, int32_t n_tensors, float max_nor
  * c as in rs_grad_clip (d_grad itself is not changed).  A norm that is not finite skips the step:
  * parameters, moments and activated values stay as they are, and *d_norm tells.  Nothing waits on
  * the host. d_workspace: rs_grad_norm_workspace_size(n_segs) bytes.  Errors: as rs_adam_step,
- * RS_ERR_WORKSPACE. */
+ * RS_ERR_WORKSPACE.
+ *
+ * `step` fixes the bias corrections at the call: a captured call repeats them at every replay, and
+ * a host that counts calls does not know which were skipped.  rs_adam_step_clipped_counted takes
+ * the number from the device instead: *d_steps holds the steps taken so far (0 before the first),
+ * the call is step *d_steps + 1, and *d_steps goes up by one unless the step is skipped. */
 int rs_adam_step_clipped(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2,
                          double eps, int32_t step, float max_norm, float* d_norm, void* d_workspace,
                          size_t workspace_bytes, void* stream);
+int rs_adam_step_clipped_counted(const rs_adam_segment* segs, int32_t n_segs, double beta1, double beta2,
+                                 double eps, int32_t* d_steps, float max_norm, float* d_norm,
+                                 void* d_workspace, size_t workspace_bytes, void* stream);
 
 /* Allocation-free variant of rs_bin.  The source pages have no counterpart: this entry point
  * exists for callers of this library that cannot allocate device memory -- for example a plug-in
