@@ -361,27 +361,46 @@ class WideAppearance:
         rs.rs_quantize_fp8(x, qt=scratch_t[0], scales_t=scratch_t[1])
         self._product(grad_t, *scratch_t, layer.dw)
 
+    @staticmethod
+    def _powers(x):
+        """The power of two that brings the largest |x| into [0.5, 1), and its inverse, as device scalars."""
+        e = torch.frexp(x.abs().amax()).exponent.clamp(-125, 125)  # any in range will do where it is not finite
+        return ((127 - e) << 23).view(torch.float32), ((127 + e) << 23).view(torch.float32)
+
     def backward(self, dL_dcolors: torch.Tensor, stream=None):
-        """Gradients of every weight (dnorms, the layers' dw) and of the features from dL/dcolours [3, n]."""
+        """Gradients of every weight (dnorms, the layers' dw) and of the features from dL/dcolours [3, n].
+
+        float16 activations hold nothing much below 6e-8, and a loss over an image has gradients of that size: between the
+        layers they then carry a power of two, exact in every step, that is taken out of what leaves."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
             dz = (dL_dcolors * self.colors * (1 - self.colors)).t().contiguous()
             last = len(self.up)
+            undo = lambda t: t
+            if self.dtype is torch.float16 and self.n > 0:
+                up, down = self._powers(dz)
+                dz.mul_(up)
+                undo = lambda t: t.mul_(down)
             rs.rs_quantize_fp8(dz, *self.q3, *self.q3t)
+            undo(self.q3t[1])  # a weight's gradient takes it out with the scales of the gradient's transposed form
             self._weight_grad(self.q3t, self.y[last], self.qct, self.head)
             self._product(self.q3, self.head.qt, self.head.st, self.dy)
             rs.rs_rms_norm_bwd(self.h[last], self.norms[last], self.rstd[last], self.dy, self.dh, self.dnorms[last],
                                self.workspace)
+            undo(self.dnorms[last])
             for b in reversed(range(last)):
                 # dh is the gradient of h_{b+1} = h_b + r_b: of r_b as it is, of h_b with what comes through the block
                 rs.rs_quantize_fp8(self.dh, *self.qc, *self.qct)
+                undo(self.qct[1])
                 self._weight_grad(self.qct, self.u[b], self.qht, self.down[b])
                 self._product(self.qc, self.down[b].qt, self.down[b].st, self.du)
                 rs.rs_quantize_fp8(self.du, *self.qh, *self.qht, relu=self.u[b])
+                undo(self.qht[1])
                 self._weight_grad(self.qht, self.y[b], self.qct, self.up[b])
                 self._product(self.qh, self.up[b].qt, self.up[b].st, self.dy)
                 rs.rs_rms_norm_bwd(self.h[b], self.norms[b], self.rstd[b], self.dy, self.dh, self.dnorms[b],
                                    self.workspace, dL_dsum=self.dh)
-            self.dfeatures.copy_(self.dh)
+                undo(self.dnorms[b])
+            undo(self.dfeatures.copy_(self.dh))
 
     def parameters(self):
         """(parameter, gradient) of every group: the features, the norms, the layers."""
