@@ -200,7 +200,7 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // A pair of CTAs takes 256 x BN tiles of out (and one of `splits` stretches of the blocks), persistently: each CTA
 // holds 128 rows of a and half of b's rows, and one product instruction (cta_group::2) uses both, so that b is
 // fetched and stored once a pair.  Warp 0 of each CTA loads, warp 1 of the first issues the products, warp 2 of each
-// fetches the scales, warp 3 checks them, warps 4 to 11 of both add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a
+// fetches the scales, warps 4 to 11 of both add the blocks up: warp w reads tensor-memory lanes 32 (w mod 4) on and a
 // half of the columns. Tensor memory holds kAcc accumulators of BN columns: the products of the next blocks run while
 // a block is read.
 //
@@ -287,11 +287,11 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, const void* sr
 // ---- scales whose product is no normal float32
 // With a scale per 128 rows of b the two scales are multiplied first, once for a row and block.  Where that leaves the
 // normal numbers (below 2^-126 bits are lost, above 2^128 it is infinite) though the block's sum would bring the result
-// back, the row's results are formed anew by its thread after the tiles, one scale after the other.  Warp 3 looks
-// for such products as the scales pass by, and back to back that costs nothing (160,000 x 512 x 512 55.8 against 56.0 us
-// without, 65536 x 2048 x 2048 223 against 224); from a cold L2 the longer code takes a microsecond or two to come.
-// A second way through the loop that adds the blocks up cost 10 to 20 percent of wide products, remembering there that
-// such a product was met 3 to 5.
+// back, the row's results are formed anew by its thread after the tiles, one scale after the other.  The warp that
+// fetches the scales looks for such products before it overwrites them, which costs nothing: 160,000 x 512 x 512 56.0
+// us back to back with it and without, 65536 x 2048 x 2048 224 and 225.  A warp of its own was 2 us slower a call where
+// its code had to come from memory, a second way through the loop that adds the blocks up 10 to 20 percent on
+// wide products, remembering there that such a product was met 3 to 5.
 __device__ __forceinline__ bool normal(float f) { return fabsf(f) >= FLT_MIN && fabsf(f) <= FLT_MAX; }
 
 // Whether some block of a stretch needs that: the product of its scales is not normal, and not only small because all of
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) bar_init(&full[i], 1), bar_init(&empty[i], 1);
         for (int i = 0; i < kAcc; ++i) bar_init(&acc_full[i], 1), bar_init(&acc_empty[i], 2 * kSumWarps);
-        for (int i = 0; i < kGroups; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps + !ROWS);
+        for (int i = 0; i < kGroups; ++i) bar_init(&sc_full[i], 32), bar_init(&sc_empty[i], kSumWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -458,6 +458,20 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const uint32_t bar = smem_u32(&sc_full[(count >> 2) % kGroups]);
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(bar) : "memory");
             };
+            // Before scales are overwritten, and at the end: the largest and smallest magnitudes of four rows and of b's
+            // two bound the products of a block.
+            float least = 1.f, most = 1.f;
+            const auto look = [&](uint32_t first, uint32_t last) {
+#pragma unroll 1
+                for (uint32_t i = first; i < last; ++i) {
+                    const float4 v = reinterpret_cast<const float4*>(scales[i])[lane];
+                    const float2 s = *reinterpret_cast<const float2*>(scales[i] + 128);
+                    const float lo = fminf(fminf(fabsf(v.x), fabsf(v.y)), fminf(fabsf(v.z), fabsf(v.w)));
+                    const float hi = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+                    least = fminf(least, lo * fminf(fabsf(s.x), fabsf(s.y)));
+                    most = fmaxf(most, hi * fmaxf(fabsf(s.x), fabsf(s.y)));
+                }
+            };
             for (int u = pair; u < units && ok; u += pairs) {
                 const auto [tile, r] = unit_of(g, u);
                 const int ty = tile / g.tiles_n, x = (tile - ty * g.tiles_n) * BN;
@@ -469,6 +483,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         const uint32_t parity = (count / kRing & 1) ^ 1;
                         ok = __all_sync(0xffffffffu, bar_wait(&sc_empty[(count >> 2) % kGroups], parity));
                         if (!ok) break;
+                        if (!ROWS && count >= kRing) {
+                            look(count % kRing, count % kRing + 4);
+                            __syncwarp();
+                        }
                     }
                     float* to = scales[count % kRing];
 #pragma unroll
@@ -485,35 +503,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             if (count % 4 != 0) done();
             asm volatile("cp.async.wait_all;" ::: "memory");
-        } else if (!ROWS && warp == 3) {
-            // The largest and smallest magnitudes of four rows and of b's scales bound the products of a block.
-            uint32_t count = 0;
-            bool ok = true;
-            float least = 1.f, most = 1.f;
-            for (int u = pair; u < units && ok; u += pairs) {
-                const Range r = unit_of(g, u).r;
-                for (int b = r.first; b < r.last; ++b, ++count) {
-                    const uint32_t group = (count >> 2) % kGroups;
-                    if (count % 4 == 0 &&
-                        !(ok = __all_sync(0xffffffffu, bar_wait(&sc_full[group], count / kRing & 1))))
-                        break;
-                    const float* sc = scales[count % kRing];
-                    const float4 a = reinterpret_cast<const float4*>(sc)[lane];
-                    const float2 s = *reinterpret_cast<const float2*>(sc + 128);
-                    const float lo = fminf(fminf(fabsf(a.x), fabsf(a.y)), fminf(fabsf(a.z), fabsf(a.w)));
-                    const float hi = fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w)));
-                    least = fminf(least, lo * fminf(fabsf(s.x), fabsf(s.y)));
-                    most = fmaxf(most, hi * fmaxf(fabsf(s.x), fabsf(s.y)));
-                    if (count % 4 == 3) {
-                        __syncwarp();
-                        if (lane == 0) bar_arrive(smem_u32(&sc_empty[group]));
-                    }
-                }
+            if constexpr (!ROWS) {
+                __syncwarp();  // the other lanes' copies
+                look(0, min(count, uint32_t(kRing)));
+                const bool met = __any_sync(0xffffffffu, !(least >= FLT_MIN && most <= FLT_MAX));
+                if (lane == 0) apart_met = met;
+                __syncwarp();
+                asm volatile("bar.arrive 1, %0;" ::"n"(32 + 32 * kSumWarps) : "memory");
             }
-            const bool met = __any_sync(0xffffffffu, !(least >= FLT_MIN && most <= FLT_MAX));
-            if (lane == 0) apart_met = met;
-            __syncwarp();
-            asm volatile("bar.arrive 1, %0;" ::"n"(32 + 32 * kSumWarps) : "memory");
         }
         __syncwarp();
     } else {
