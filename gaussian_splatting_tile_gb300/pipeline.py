@@ -363,8 +363,8 @@ class WideAppearance:
 
     @staticmethod
     def _powers(x):
-        """The power of two that brings the largest |x| into [0.5, 1), and its inverse, as device scalars."""
-        e = torch.frexp(x.abs().amax()).exponent.clamp(-125, 125)  # any in range will do where it is not finite
+        """The power of two that brings the largest |x| into [0.5, 1), and its inverse, float32 [1] on the device."""
+        e = torch.frexp(x.abs().amax().view(1)).exponent.clamp(-125, 125)  # any in range will do where it is not finite
         return ((127 - e) << 23).view(torch.float32), ((127 + e) << 23).view(torch.float32)
 
     def backward(self, dL_dcolors: torch.Tensor, stream=None):
@@ -375,7 +375,7 @@ class WideAppearance:
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
             dz = (dL_dcolors * self.colors * (1 - self.colors)).t().contiguous()
             last = len(self.up)
-            undo = lambda t: t
+            undo, down = lambda t: t, None
             if self.dtype is torch.float16 and self.n > 0:
                 up, down = self._powers(dz)
                 dz.mul_(up)
@@ -400,7 +400,10 @@ class WideAppearance:
                 rs.rs_rms_norm_bwd(self.h[b], self.norms[b], self.rstd[b], self.dy, self.dh, self.dnorms[b],
                                    self.workspace, dL_dsum=self.dh)
                 undo(self.dnorms[b])
-            undo(self.dfeatures.copy_(self.dh))
+            if down is None:
+                self.dfeatures.copy_(self.dh)
+            else:
+                torch.mul(self.dh, down, out=self.dfeatures)  # in float32: down is a tensor of one dimension
 
     def parameters(self):
         """(parameter, gradient) of every group: the features, the norms, the layers."""
