@@ -13,10 +13,11 @@
 // takes each of their schedulers 8192 multiply-adds, 390 clocks at the rate that two warps reach.  The two overlap,
 // but each accumulator's way round (products, word to the readers, reading, word back) is longer than both, and there
 // is room for two: that, and every instruction between the readers' loads, is what large products wait for.  Products
-// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 245 us (2.2 PFLOP/s;
-// without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 57
-// us (4.3 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us from a cold cache, 1
-// x 4096 x 4096 9 us, the call itself.
+// with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 240 us (2.3 PFLOP/s;
+// without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 56
+// us (4.4 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us from a cold cache, 1
+// x 4096 x 4096 9.5 us, as long as its call.  Rows of out that are not on 16-byte boundaries leave value by value:
+// 160,000 x 501 x 512 113 us from a cold cache where 512 columns take 88.
 #include <cuda.h>
 
 #include <cfloat>
@@ -211,7 +212,8 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 // (431) and worse where tiles are short (160,000 x 512 x 512: 76); asking for the next accumulator early, nothing.
 constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;
-// Registers a thread before and after the split between warps 0-3 and the rest: 128 x 40 + 256 x 232 = 384 x 168.
+// Registers a thread before and after the split between warps 0-3 and the rest: 128 x 40 + 256 x 232 = 384 x 168.  With a
+// scale a row and 256 columns, and one a block and 128 columns, 20 bytes spill.
 constexpr int kRegsLaunch = 168, kRegsFew = 40, kRegsMany = 232;
 static_assert(128 * kRegsFew + 32 * kSumWarps * kRegsMany <= kTileThreads * kRegsLaunch, "the launch's registers");
 
@@ -650,8 +652,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---------------------------------------------------------------- few rows
 // With at most 64 rows of a the time goes into reading b once, so the roles change sides: the products' 128 rows are
-// rows of b (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks so that
-// every SM reads.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its
+// rows of b (weights), their NT columns the rows of a, and a cluster of up to 8 CTAs shares a tile's blocks: all
+// SMs read from 18 tiles on, 2305 rows of b.  Each CTA adds its blocks up as the tile kernel does (thread = row of b); the cluster then adds its
 // CTAs' sums through distributed shared memory, rank by rank, each CTA finishing some of the columns.
 constexpr int kRowsTmem = 128;  // columns of tensor memory
 

@@ -24,7 +24,9 @@ struct Plan {
 };
 
 // Which kernel and which tiles.
-//  - Up to 64 rows the rows kernel (64 x 4096 x 4096: 10.4 us; at 128 rows it took 33.8 us and the tiles 15.2).
+//  - Up to 64 rows the rows kernel (64 x 4096 x 4096: 10.4 us; at 128 rows it took 33.8 us and the tiles 15.2).  The rule
+//    looks at that alone: with few columns and a long contraction 64 rows lose to 65 on split tiles (x 256 x 160000
+//    107 against 31 us, x 512 x 160000 109 against 43).
 //  - 256 columns a tile move the fewest bytes and cost the fewest instructions a product, but with few tiles and
 //    little work for each pair of SMs, 128 columns spread it further: 2000 x 1000 x 2000 (32 wide tiles, 7 blocks a
 //    pair) 11.7 against 16.5 us, 1000 x 1000 x 3000 14.7 against 17.7; with more of either the other way, 4000 x 1000

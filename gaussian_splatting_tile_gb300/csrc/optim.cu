@@ -80,9 +80,9 @@ __global__ void __launch_bounds__(256) k_adam_begin(const float* part, int parts
 
 // kClip: every gradient is multiplied by min(1, max_norm / norm), which each block forms from the partial sums by
 // itself (a few KB in L2; a launch fewer than a kernel between); a norm that is not finite leaves everything as it
-// is.  Six blocks an SM as without it: 1M Gaussians 306 us with the norm's 52, 312 us with five blocks; going
-// backwards, where L2 might still hold the norm's last reads, gave nothing (308).
-// kCounted: the same from what k_adam_begin left.
+// is.  Six blocks an SM as without it: 1M Gaussians 298 us with the norm's 39; with five blocks 2 percent more, and going
+// backwards, where L2 might still hold the norm's last reads, gave nothing.
+// kCounted: the same from what k_adam_begin left (a launch of 6 us more, by itself).
 enum AdamMode { kPlain, kClip, kCounted };
 template <AdamMode MODE>
 __global__ void __launch_bounds__(256, MODE == kPlain ? 1 : 6) k_adam(const __grid_constant__ AdamTable T) {
