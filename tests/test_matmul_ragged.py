@@ -37,3 +37,20 @@ def test_rows_alone_are_written(dt, m, k, off, pad):
             assert torch.equal(view, base), n
             view.fill_(7.0)
             assert bool((big == 7.0).all()), (n, total)
+
+
+# the few-rows kernel, 128- and 256-column tiles
+@pytest.mark.parametrize("m,n", [(20, 300), (300, 140), (9800, 300)])
+@pytest.mark.parametrize("blocks", [True, False])
+def test_bytes_past_the_columns_do_not_count(m, n, blocks):
+    """NaN in every byte between a row's last column and the next row, for widths of every remainder by 16."""
+    for k in [*range(1, 18), 129, 131, 134, 140, 143, 255, 257, 383]:
+        a, sa, b, sb = W.operands(W.gen(k), m, n, k, blocks)
+        clean = []
+        for q in (a, b):
+            wide = torch.full((q.shape[0], -(-k // 16) * 16 + 16), 0x7f, dtype=torch.uint8, device="cuda")
+            wide[:, :k] = q.view(torch.uint8)
+            clean.append(wide[:, :k])
+        want, mags = W.product(a, sa, b, sb)
+        got = W.matmul(clean[0], sa, clean[1], sb)
+        W.close(got, want, (128 + k / 128 + 4) * 2 * W.U * mags)
