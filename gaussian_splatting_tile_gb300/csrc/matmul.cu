@@ -41,6 +41,7 @@ struct MatmulArgs {
     int splits, tiles_n, tiles;
     int each, extra;            // blocks a stretch; the first `extra` stretches have one more
     float* part;                // splits > 1: [split][tile][column][128 rows]
+    float* so;                  // out in 8 bits: its scales [ceil(n / 128)][m]
 };
 
 // ---------------------------------------------------------------- tensor cores, TMA, barriers
@@ -356,12 +357,22 @@ __device__ __noinline__ void units_anew(const MatmulArgs& g, int pair, int pairs
         const int ty = tile / g.tiles_n, col = (tile - ty * g.tiles_n) * BN + half * kCols;
         const long long row = (long long)(ty * 2 + rank) * 128 + lane_row;
         if (row >= g.m || col >= g.n || !scales_apart(g, r, row, col)) continue;
-        float* part = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + lane_row;
         T* out = static_cast<T*>(g.out) + row * g.os + col;
-        row_anew(g, r, row, col, kCols, [&](int j, float x) {
-            if (g.splits > 1) part[size_t(j) * 128] = x;
-            else out[j] = from_f<T>(g.relu ? relu(x) : x);
-        });
+        if constexpr (sizeof(T) == 1) {  // the row's 128 columns twice: for their largest magnitude, and in 8 bits
+            const auto value = [&](float x) { return g.relu ? relu(x) : x; };
+            float top = 0.f, scale, inv;
+            row_anew(g, r, row, col, kCols, [&](int, float x) { top = fmaxf(top, fabsf(value(x))); });
+            block_scale(top, scale, inv);
+            g.so[size_t(col / kBlock) * g.m + row] = scale;
+            row_anew(g, r, row, col, kCols,
+                     [&](int j, float x) { out[j] = uint8_t(e4m3x4(value(x) * inv, 0.f, 0.f, 0.f)); });
+        } else {
+            float* part = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + lane_row;
+            row_anew(g, r, row, col, kCols, [&](int j, float x) {
+                if (g.splits > 1) part[size_t(j) * 128] = x;
+                else out[j] = from_f<T>(g.relu ? relu(x) : x);
+            });
+        }
     }
 }
 
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            if (g.splits > 1) {
+            if (sizeof(T) > 1 && g.splits > 1) {
                 float* o = g.part + ((size_t(u) * 2 + rank) * BN + half * kCols) * 128 + wrow + lane;
 #pragma unroll
                 for (int j = 0; j < kCols / 2; ++j) {
@@ -591,7 +602,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
             } else if (col < g.n) {
                 // Passes of 128 bytes a row, two to a fence (half of the way out's time was the fence).
+                // In 8 bits a pass is a block: its scale is settled in the thread that holds the row's 128 sums.
                 constexpr int kOnce = 128 / sizeof(T), kPasses = kCols / kOnce, kTogether = kPasses < 2 ? kPasses : 2;
+                float inv = 1.f;
+                if constexpr (sizeof(T) == 1) {
+                    static_assert(kCols == kBlock, "a thread's columns are one block");
+                    float top = 0.f, scale;
+#pragma unroll
+                    for (int j = 0; j < kCols / 2; ++j) {
+                        float2 x = unpack2(acc[j]);
+                        if (g.relu) {
+                            x = make_float2(relu(x.x), relu(x.y));
+                            acc[j] = pack2(x.x, x.y);
+                        }
+                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    }
+                    block_scale(top, scale, inv);
+                    if (row0 + lane < g.m) g.so[size_t(col / kBlock) * g.m + row0 + lane] = scale;
+                }
 #pragma unroll
                 for (int c = 0; c < kPasses; c += kTogether) {
                     // what was copied out of the buffers before has left them
@@ -601,6 +629,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     for (int q = 0; q < kTogether; ++q) {
                         uint4 w[8];
                         uint32_t* ww = reinterpret_cast<uint32_t*>(w);
+                        if constexpr (sizeof(T) == 1) {
+#pragma unroll
+                            for (int j = 0; j < kOnce; j += 4) {
+                                const float2 x = unpack2(acc[j / 2]), y = unpack2(acc[j / 2 + 1]);
+                                ww[j / 4] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
+                            }
+                        } else
 #pragma unroll
                         for (int j = 0; j < kOnce; j += 2) {
                             float2 x = unpack2(acc[((c + q) * kOnce + j) / 2]);
@@ -901,8 +936,9 @@ cudaError_t launch_clusters(void (*kernel)(Params...), int cluster, unsigned gri
 template <typename T, int BN, bool ROWS>
 cudaError_t launch_tile(const CUtensorMap& a, const CUtensorMap& b, const MatmulArgs& g, cudaStream_t s) {
     CUtensorMap out{};
-    constexpr CUtensorMapDataType type =
-        sizeof(T) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    constexpr CUtensorMapDataType type = sizeof(T) == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                         : sizeof(T) == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     if (g.tma_cols && g.splits == 1 && !encode(&out, type, sizeof(T), g.out, g.os, g.m, g.tma_cols, 32))
         return cudaErrorUnknown;
     constexpr int smem = sizeof(TileSmem<BN>) + 1024;  // + room to align the base to 1 KB
@@ -924,6 +960,19 @@ cudaError_t launch_rows(const CUtensorMap& a, const CUtensorMap& b, const Matmul
     const unsigned grid = unsigned(g.tiles) * g.splits;
     return launch_clusters(k_matmul_rows<T, NT, ROWS>, g.splits, grid, 192, smem, s, a, b, g, stages);
 }
+
+// 8-bit zeros have their scale too.
+__global__ void k_zero_scales(float* scales, size_t n) {
+    RS_PDL_ENTER();
+    float scale, inv;
+    block_scale(0.f, scale, inv);
+    for (size_t i = blockIdx.x * size_t(blockDim.x) + threadIdx.x; i < n; i += size_t(gridDim.x) * blockDim.x)
+        scales[i] = scale;
+}
+
+// The float32 result on its way to 8 bits, where the tile kernel does not write them itself: [m][n to 16 bytes].
+size_t wide_row(int32_t n) { return (size_t(n) + 3) / 4 * 4; }
+size_t wide_bytes(int32_t m, int32_t n) { return size_t(m) * wide_row(n) * sizeof(float); }
 
 }  // namespace
 
@@ -976,7 +1025,7 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
     const int whole = n / int(16 / z) * int(16 / z);  // columns in whole words of 16 bytes
     const int tma_cols = rows16(d_out, out_stride, z) && out_stride * z < (size_t(1) << 40) ? whole : 0;
     MatmulArgs g{m, n, k, d_a, a_stride, d_b, b_stride, d_a_scales, d_b_scales, relu, d_out, out_stride, tma_cols,
-                 p.splits, p.tiles_n, p.tiles, blocks / p.splits, blocks % p.splits, static_cast<float*>(d_workspace)};
+                 p.splits, p.tiles_n, p.tiles, blocks / p.splits, blocks % p.splits, static_cast<float*>(d_workspace), nullptr};
     cudaError_t e = with_dtype(out_dtype, [&](auto v) {
         using T = decltype(v);
         const bool per_row = b_scale_rows == 1;
@@ -995,6 +1044,61 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
             return pdl_launch(many ? k_matmul_join<T, 4> : k_matmul_join<T, 1>, unsigned(p.tiles) * 2 * (p.bn / 8),
                               many ? 1024 : 256, 0, s, g, p.bn);
         });
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+size_t rs_matmul_fp8_q_workspace_size(int32_t m, int32_t n, int32_t k) {
+    using namespace rs;
+    if (m <= 0 || n <= 0 || k <= 0 || direct_8bit(m, n, k)) return 0;
+    return wide_bytes(m, n) + (rs_matmul_fp8_workspace_size(m, n, k) + 15) / 16 * 16;
+}
+
+int rs_matmul_fp8_q(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride, const float* d_a_scales,
+                    const uint8_t* d_b, size_t b_stride, const float* d_b_scales, int32_t b_scale_rows, int32_t relu,
+                    uint8_t* d_q, size_t q_stride, float* d_scales, void* d_workspace, size_t workspace_bytes,
+                    void* stream) {
+    using namespace rs;
+    if (m < 0 || n < 0 || k < 0 || (b_scale_rows != 1 && b_scale_rows != kBlock)) return RS_ERR_INVALID_ARG;
+    constexpr int32_t kMost = 0x7ffffc00;
+    if (m > kMost || n > kMost || k > kMost) return RS_ERR_INVALID_ARG;
+    if (m == 0 || n == 0) return RS_OK;
+    if (!fp8_rows_ok(d_q, q_stride, n) || !ptr_ok(d_scales, 4) || q_stride >= (size_t(1) << 40))
+        return RS_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (k == 0) {
+        const size_t count = size_t(ceil_div(n, kBlock)) * m;
+        cudaError_t e = cudaMemset2DAsync(d_q, q_stride, 0, n, m, s);
+        if (e == cudaSuccess)
+            e = pdl_launch(k_zero_scales, unsigned(std::min<size_t>(ceil_div(count, 256), 8 * kSms)), 256, 0, s, d_scales,
+                           count);
+        return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+    }
+    if (!fp8_rows_ok(d_a, a_stride, k) || !fp8_rows_ok(d_b, b_stride, k) || !ptr_ok(d_a_scales, 4) ||
+        !ptr_ok(d_b_scales, 4) || a_stride >= (size_t(1) << 40) || b_stride >= (size_t(1) << 40))
+        return RS_ERR_INVALID_ARG;
+    if ((long long)ceil_div(m, 128) * ceil_div(n, 128) > 0x3fffffff) return RS_ERR_INVALID_ARG;
+    const size_t need = rs_matmul_fp8_q_workspace_size(m, n, k);
+    if (need > 0 && !ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return RS_ERR_WORKSPACE;
+    if (need > 0) {
+        const size_t row = wide_row(n), first = wide_bytes(m, n);
+        float* wide = static_cast<float*>(d_workspace);
+        const int e = rs_matmul_fp8(m, n, k, d_a, a_stride, d_a_scales, d_b, b_stride, d_b_scales, b_scale_rows, relu,
+                                    RS_F32, wide, row, static_cast<char*>(d_workspace) + first, workspace_bytes - first,
+                                    stream);
+        return e != RS_OK ? e
+                          : rs_quantize_fp8(m, n, RS_F32, wide, row, nullptr, 0, d_q, q_stride, d_scales, nullptr, 0,
+                                            nullptr, stream);
+    }
+    CUtensorMap ma, mb;
+    constexpr CUtensorMapDataType bytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    if (!encode(&ma, bytes, 1, d_a, a_stride, m, k, 128) || !encode(&mb, bytes, 1, d_b, b_stride, n, k, 128))
+        return RS_ERR_CUDA;
+    const int blocks = ceil_div(k, kBlock), tiles_n = ceil_div(n, 256), tiles = ceil_div(m, 256) * tiles_n;
+    const MatmulArgs g{m, n, k, d_a, a_stride, d_b, b_stride, d_a_scales, d_b_scales, relu, d_q, q_stride, n / 16 * 16, 1,
+                       tiles_n, tiles, blocks, 0, nullptr, d_scales};
+    const cudaError_t e = b_scale_rows == 1 ? launch_tile<uint8_t, 256, true>(ma, mb, g, s)
+                                            : launch_tile<uint8_t, 256, false>(ma, mb, g, s);
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 

@@ -57,4 +57,11 @@ inline Plan plan_matmul(int m, int n, int k) {
     return p;
 }
 
+// Whether a product with an 8-bit result is the tile kernel's alone: its threads hold a row's 128 sums of 256 columns a
+// tile, unsplit.  Otherwise the result goes to the workspace in float32 and from there to 8 bits.
+inline bool direct_8bit(int m, int n, int k) {
+    const Plan p = plan_matmul(m, n, k);
+    return p.rows == 0 && p.splits == 1;
+}
+
 }  // namespace rs

@@ -14,7 +14,7 @@ namespace {
 struct QuantArgs {
     int rows, cols;
     const void* x; size_t xs;
-    const void* relu; size_t relus;
+    const void* relu; size_t relus;   // of x's type, or (relu8) in 8 bits
     uint8_t* q; size_t qs;
     float* scales;
     uint8_t* qt; size_t qts;
@@ -28,8 +28,8 @@ struct QuantArgs {
 __device__ __forceinline__ int tile_unit(int c, int u) { return c * 16 + (u ^ ((c >> 3) & 15)); }
 
 // The 8 x 8 values of one thread, scaled by column (inv[j]), to the transposed bytes.
-template <typename T>
-__device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<T> (&v)[8], const float (&inv)[8],
+template <typename V>
+__device__ __forceinline__ void store_transposed(const QuantArgs& a, const V (&v)[8], const float (&inv)[8],
                                                  uint2* tile, int tx, int ty, int c0, long long r0) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -66,10 +66,11 @@ __device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<
 
 // 16-bit values leave registers for three blocks an SM; with a mask beside x two, so that both tiles are in flight at
 // once.
-enum Form { kRowsCols, kRowsColsRelu, kBlocks };
+enum Form { kRowsCols, kRowsColsRelu, kRowsColsRelu8, kBlocks };
 // FULL: 16-byte rows, and no tile ends inside its columns.
 template <typename T, bool VEC, bool FULL, Form FORM>
-__global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ? 2 : 3) k_quantize(QuantArgs a) {
+__global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu || FORM == kRowsColsRelu8 ? 2 : 3)
+    k_quantize(QuantArgs a) {
     constexpr bool BLOCKS = FORM == kBlocks;
     RS_PDL_ENTER();
     __shared__ float cmax[16][kBlock];
@@ -92,6 +93,16 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ?
             const bool in = r + i < a.rows;
             const T* p = static_cast<const T*>(a.relu) + (in ? r + i : 0) * a.relus + c;
             u[i].template load<VEC>(p, in ? left : 0, c > 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i].mask(u[i]);
+    }
+    if constexpr (FORM == kRowsColsRelu8) {
+        Bytes8 u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const bool in = r + i < a.rows;
+            u[i].load(static_cast<const uint8_t*>(a.relu) + (in ? r + i : 0) * a.relus + c, in ? left : 0);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i].mask(u[i]);
@@ -170,7 +181,60 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu ?
     }
 }
 
-int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s) {
+// The transposed form of a checkpoint: the same tile, the same thread for the same 8 x 8 values, which are a byte times
+// their row's scale.  Bound by memory: one byte in, one out.
+struct ScaledBytes8 {
+    Bytes8 v;
+    float scale;
+    __device__ __forceinline__ float2 pair(int p) const {
+        const float2 f = v.pair(p);
+        return make_float2(f.x * scale, f.y * scale);
+    }
+};
+
+__global__ void __launch_bounds__(256) k_transpose(QuantArgs a) {
+    RS_PDL_ENTER();
+    __shared__ float cmax[16][kBlock];
+    __shared__ __align__(16) uint2 tile[kBlock * 16];
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int ct = blockIdx.x % a.ctiles, rt = blockIdx.x / a.ctiles;
+    const int c0 = ct * kBlock, c = c0 + tx * 8;
+    const long long r0 = (long long)rt * kBlock, r = r0 + ty * 8;
+    const int left = a.cols - c;
+    ScaledBytes8 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const bool in = r + i < a.rows;
+        v[i].v.load(static_cast<const uint8_t*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
+        v[i].scale = in ? a.scales[size_t(ct) * a.rows + r + i] : 0.f;
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        float2 m = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = v[i].pair(p);
+            m = make_float2(fmaxf(m.x, fabsf(f.x)), fmaxf(m.y, fabsf(f.y)));
+        }
+        *reinterpret_cast<float2*>(&cmax[ty][tx * 8 + 2 * p]) = m;
+    }
+    __syncthreads();
+    if (threadIdx.x < kBlock) {
+        float m = 0.f, scale, inv;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = fmaxf(m, cmax[i][threadIdx.x]);
+        block_scale(m, scale, inv);
+        if (c0 + int(threadIdx.x) < a.cols) a.scales_t[size_t(rt) * a.cols + c0 + threadIdx.x] = scale;
+        cmax[0][threadIdx.x] = inv;
+    }
+    __syncthreads();
+    float invs[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) invs[j] = cmax[0][tx * 8 + j];
+    store_transposed(a, v, invs, tile, tx, ty, c0, r0);
+}
+
+int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s, bool relu8 = false) {
     if (a.rows < 0 || a.cols < 0 || !dtype_ok(dtype)) return RS_ERR_INVALID_ARG;
     if ((a.q == nullptr) != (a.scales == nullptr) || (a.qt == nullptr) != (a.scales_t == nullptr))
         return RS_ERR_INVALID_ARG;
@@ -178,13 +242,15 @@ int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s) {
     if (!a.q && !a.qt) return RS_ERR_INVALID_ARG;
     const size_t z = dtype_size(dtype);
     if (!ptr_ok(a.x, z) || a.xs < size_t(a.cols)) return RS_ERR_INVALID_ARG;
-    if (a.relu && (!ptr_ok(a.relu, z) || a.relus < size_t(a.cols))) return RS_ERR_INVALID_ARG;
+    if (relu8 ? !fp8_rows_ok(a.relu, a.relus, a.cols)
+              : a.relu && (!ptr_ok(a.relu, z) || a.relus < size_t(a.cols)))
+        return RS_ERR_INVALID_ARG;
     if (a.q && (!fp8_rows_ok(a.q, a.qs, a.cols) || !ptr_ok(a.scales, 4))) return RS_ERR_INVALID_ARG;
     if (a.qt && (!fp8_rows_ok(a.qt, a.qts, a.rows) || !ptr_ok(a.scales_t, 4))) return RS_ERR_INVALID_ARG;
     a.ctiles = ceil_div(a.cols, kBlock);
     a.rtiles = ceil_div(a.rows, kBlock);
     if ((long long)a.ctiles * a.rtiles > 0x7fffffffLL) return RS_ERR_INVALID_ARG;
-    const bool vec = rows16(a.x, a.xs, z) && (!a.relu || rows16(a.relu, a.relus, z));
+    const bool vec = rows16(a.x, a.xs, z) && (relu8 || !a.relu || rows16(a.relu, a.relus, z));
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         const unsigned g = unsigned(a.ctiles) * a.rtiles;
@@ -194,6 +260,9 @@ int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s) {
         if (blocks)
             return launch(k_quantize<T, false, false, kBlocks>, k_quantize<T, true, false, kBlocks>,
                           k_quantize<T, true, true, kBlocks>);
+        if (relu8)
+            return launch(k_quantize<T, false, false, kRowsColsRelu8>, k_quantize<T, true, false, kRowsColsRelu8>,
+                          k_quantize<T, true, true, kRowsColsRelu8>);
         if (a.relu)
             return launch(k_quantize<T, false, false, kRowsColsRelu>, k_quantize<T, true, false, kRowsColsRelu>,
                           k_quantize<T, true, true, kRowsColsRelu>);
@@ -220,6 +289,29 @@ int rs_quantize_fp8_blocks(int32_t rows, int32_t cols, int32_t dtype, const void
                            void* stream) {
     return rs::quantize({rows, cols, d_x, x_stride, nullptr, 0, d_q, q_stride, d_scales, d_qt, qt_stride, d_scales_t,
                          0, 0}, dtype, true, static_cast<cudaStream_t>(stream));
+}
+
+int rs_quantize_fp8_relu8(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
+                          const uint8_t* d_relu, size_t relu_stride, uint8_t* d_q, size_t q_stride, float* d_scales,
+                          uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream) {
+    return rs::quantize({rows, cols, d_x, x_stride, d_relu, relu_stride, d_q, q_stride, d_scales, d_qt, qt_stride,
+                         d_scales_t, 0, 0}, dtype, false, static_cast<cudaStream_t>(stream), true);
+}
+
+int rs_transpose_fp8(int32_t rows, int32_t cols, const uint8_t* d_q, size_t q_stride, const float* d_scales,
+                     uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream) {
+    using namespace rs;
+    if (rows < 0 || cols < 0) return RS_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return RS_OK;
+    if (!fp8_rows_ok(d_q, q_stride, cols) || !ptr_ok(d_scales, 4) || !fp8_rows_ok(d_qt, qt_stride, rows) ||
+        !ptr_ok(d_scales_t, 4))
+        return RS_ERR_INVALID_ARG;
+    const int ctiles = ceil_div(cols, kBlock), rtiles = ceil_div(rows, kBlock);
+    if ((long long)ctiles * rtiles > 0x7fffffffLL) return RS_ERR_INVALID_ARG;
+    const QuantArgs a{rows, cols, d_q, q_stride, nullptr, 0, nullptr, 0, const_cast<float*>(d_scales), d_qt, qt_stride,
+                      d_scales_t, ctiles, rtiles};
+    const cudaError_t e = pdl_launch(k_transpose, unsigned(ctiles) * rtiles, 256, 0, static_cast<cudaStream_t>(stream), a);
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -20,6 +20,31 @@ template <> __device__ __forceinline__ float from_f<float>(float x) { return x; 
 template <> __device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// Two e4m3 bytes (the lower first) as floats: exact.
+__device__ __forceinline__ float2 e4m3x2_to_floats(uint32_t bytes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(uint16_t(bytes)));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// Eight consecutive bytes of a row of an 8-bit matrix, of which the first `left` exist (the others read as zero).  A row
+// starts on a 16-byte boundary and runs of eight on multiples of 8.
+struct Bytes8 {
+    uint2 w;
+    __device__ __forceinline__ void load(const uint8_t* p, int left) {
+        if (left >= 8) {
+            w = *reinterpret_cast<const uint2*>(p);
+        } else {
+            uint32_t b[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i] = i < left ? p[i] : 0u;
+            w = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+        }
+    }
+    __device__ __forceinline__ float2 pair(int p) const { return e4m3x2_to_floats((p < 2 ? w.x : w.y) >> (p & 1 ? 16 : 0)); }
+};
+// 0xff in every byte that is an e4m3 value above zero or NaN.
+__device__ __forceinline__ uint32_t above_zero4(uint32_t w) { return __vcmpgts4(w, 0u) | __vcmpeq4(w, 0xffffffffu); }
+
 // Eight consecutive values as they are stored, of which the first `left` exist (the others read as zero).  VEC: the
 // place is aligned to 16 bytes, and a whole run is one or two 16-byte accesses; else a run of 16-bit values is read
 // as aligned words where its neighbours on both sides exist (`inner`).  16-bit types stay packed in four registers,
@@ -43,6 +68,12 @@ struct Run8 {
     __device__ __forceinline__ void mask(const Run8& u) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = u.v[i] <= 0.f ? 0.f : v[i];
+    }
+    // zero where u, in e4m3, is <= 0
+    __device__ __forceinline__ void mask(const Bytes8& u) {
+        const uint32_t lo = above_zero4(u.w.x), hi = above_zero4(u.w.y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (i < 4 ? lo : hi) >> (8 * (i & 3)) & 1 ? v[i] : 0.f;
     }
     // m = max(m, |values|), pair by pair
     struct Max { float x = 0.f, y = 0.f; };
@@ -86,6 +117,11 @@ struct PackedRun8 {
     }
     __device__ __forceinline__ void mask(const PackedRun8& u) {
         w = make_uint4(kept(w.x, u.w.x), kept(w.y, u.w.y), kept(w.z, u.w.z), kept(w.w, u.w.w));
+    }
+    __device__ __forceinline__ void mask(const Bytes8& u) {
+        const uint32_t lo = above_zero4(u.w.x), hi = above_zero4(u.w.y);
+        w = make_uint4(w.x & __byte_perm(lo, 0u, 0x1100), w.y & __byte_perm(lo, 0u, 0x3322),
+                       w.z & __byte_perm(hi, 0u, 0x1100), w.w & __byte_perm(hi, 0u, 0x3322));
     }
     struct Max { T2 h = {T(0.f), T(0.f)}; };
     __device__ __forceinline__ void max_into(Max& m, int p) const {

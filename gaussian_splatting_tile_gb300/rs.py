@@ -77,6 +77,36 @@ class rs_adam_segment(ctypes.Structure):
                 ("lr", ctypes.c_float), ("activation", ctypes.c_int32)]
 
 
+class rs_fp8_matrix(ctypes.Structure):
+    _fields_ = [("d_q", ctypes.c_void_p), ("stride", ctypes.c_size_t), ("d_scales", ctypes.c_void_p)]
+
+
+class rs_sandwich(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gate_cols", ctypes.c_int32),
+                ("d_x", ctypes.c_void_p), ("x_stride", ctypes.c_size_t), ("d_x_scales", ctypes.c_void_p),
+                ("d_r", ctypes.c_void_p), ("r_stride", ctypes.c_size_t), ("d_r_scales", ctypes.c_void_p),
+                ("d_gate", ctypes.c_void_p), ("gate_stride", ctypes.c_size_t), ("d_gate_scales", ctypes.c_void_p),
+                ("d_residual_scale", ctypes.c_void_p), ("d_post_weight", ctypes.c_void_p),
+                ("d_pre_weight", ctypes.c_void_p)]
+
+
+class rs_sandwich_out(ctypes.Structure):
+    _fields_ = [("d_sum", ctypes.c_void_p), ("sum_stride", ctypes.c_size_t), ("d_y", ctypes.c_void_p),
+                ("y_stride", ctypes.c_size_t), ("q", rs_fp8_matrix), ("kept_x", rs_fp8_matrix),
+                ("kept_r", rs_fp8_matrix), ("kept_gate", rs_fp8_matrix), ("d_rstd_r", ctypes.c_void_p),
+                ("d_rstd_s", ctypes.c_void_p)]
+
+
+class rs_sandwich_grads(ctypes.Structure):
+    _fields_ = [("d_rstd_r", ctypes.c_void_p), ("d_rstd_s", ctypes.c_void_p), ("d_dL_dy", ctypes.c_void_p),
+                ("dy_stride", ctypes.c_size_t), ("d_dL_dsum", ctypes.c_void_p), ("dsum_stride", ctypes.c_size_t),
+                ("d_dL_dx", ctypes.c_void_p), ("dx_stride", ctypes.c_size_t), ("d_dL_dr", ctypes.c_void_p),
+                ("dr_stride", ctypes.c_size_t), ("d_dL_dgate", ctypes.c_void_p), ("dgate_stride", ctypes.c_size_t),
+                ("d_dL_dresidual_scale", ctypes.c_void_p), ("d_dL_dpost_weight", ctypes.c_void_p),
+                ("d_dL_dpre_weight", ctypes.c_void_p)]
+
+
 RS_ACT_IDENTITY, RS_ACT_EXP, RS_ACT_SIGMOID = 0, 1, 2
 RS_ADAM_MAX_SEGMENTS = 16
 
@@ -165,6 +195,14 @@ def lib():
                                            ctypes.c_double, i32, ctypes.c_float, _VP, _VP, sz, _VP]
         L.rs_adam_step_clipped_counted.argtypes = [ctypes.POINTER(rs_adam_segment), i32, ctypes.c_double, ctypes.c_double,
                                                    ctypes.c_double, _VP, ctypes.c_float, _VP, _VP, sz, _VP]
+        L.rs_sandwich_norm_fwd.argtypes = [ctypes.POINTER(rs_sandwich), ctypes.c_float, ctypes.POINTER(rs_sandwich_out),
+                                           _VP]
+        L.rs_sandwich_norm_bwd_workspace_size.argtypes = [i32, i32]
+        L.rs_sandwich_norm_bwd.argtypes = [ctypes.POINTER(rs_sandwich), ctypes.POINTER(rs_sandwich_grads), _VP, sz, _VP]
+        L.rs_quantize_fp8_relu8.argtypes = [i32, i32, i32, _VP, sz, _VP, sz, _VP, sz, _VP, _VP, sz, _VP, _VP]
+        L.rs_transpose_fp8.argtypes = [i32, i32, _VP, sz, _VP, _VP, sz, _VP, _VP]
+        L.rs_matmul_fp8_q_workspace_size.argtypes = [i32, i32, i32]
+        L.rs_matmul_fp8_q.argtypes = [i32, i32, i32, _VP, sz, _VP, _VP, sz, _VP, i32, i32, _VP, sz, _VP, _VP, sz, _VP]
         for ret, name in declared_signatures():
             getattr(L, name).restype = _RESTYPES[ret]
         _lib = L
@@ -843,6 +881,138 @@ def rs_matmul_fp8(a, a_scales, b, b_scales, out, workspace=None, relu: bool = Fa
         m, n, k, pa, sa, _scales(a_scales, "a_scales", kb, m), pb, sb,
         _scales(b_scales, "b_scales", kb, n if per_row else _blocks(n)), 1 if per_row else RS_FP8_BLOCK, int(relu),
         _dtype(out, "out"), po, so, _vec(workspace, torch.uint8, 0, "workspace"),
+        0 if workspace is None else workspace.numel(), _stream(stream)))
+
+
+def _gate_cols(gate, shape) -> int:
+    """Of a gate (a matrix or a kept (q, scales)): 0 none, 1 one a row, else one an element."""
+    if gate is None:
+        return 0
+    m = gate[0] if type(gate) is tuple else gate
+    if m.dim() != 2 or m.shape[0] != shape[0] or m.shape[1] not in (1, shape[1]):
+        raise ValueError(f"the gate is {tuple(m.shape)}, needs {tuple(shape)} or {(shape[0], 1)}")
+    return int(m.shape[1])
+
+
+def _form(pair, name, shape):
+    """A place for an 8-bit matrix, (q, scales) as fp8_empty gives them."""
+    if pair is None:
+        return _NO_FORM
+    q, scales = pair
+    p, stride = _mat(q, name, _FP8, shape)
+    return p, stride, _scales(scales, f"{name}'s scales", _blocks(shape[1]), shape[0])
+
+
+_NO_FORM = (None, 0, None)
+
+
+def _operand(t, name, dtype, shape):
+    """(pointer, stride, scales) of a matrix, or of a kept one (q, scales)."""
+    if type(t) is tuple:
+        got = _form(t, name, shape)
+        if got[2] is None:
+            raise ValueError(f"{name} needs its scales")
+        return got
+    return (*_mat(t, name, dtype, shape), None)
+
+
+def _sandwich(x, r, gate, dtype, shape, post_weight, pre_weight, residual_scale):
+    cols = shape[1]
+    gate_cols = _gate_cols(gate, shape)
+    f32 = torch.float32
+    return rs_sandwich(
+        shape[0], cols, _DTYPES[dtype], gate_cols, *_operand(x, "x", dtype, shape), *_operand(r, "r", dtype, shape),
+        *(_operand(gate, "gate", dtype, (shape[0], gate_cols)) if gate_cols else _NO_FORM),
+        _vec(residual_scale, f32, cols, "residual_scale"), _vec(post_weight, f32, cols, "post_weight"),
+        _vec(pre_weight, f32, cols, "pre_weight"))
+
+
+def rs_sandwich_norm_fwd(x, r, post_weight, pre_weight, q=None, scales=None, gate=None, residual_scale=None, sum=None,
+                         y=None, rstd_r=None, rstd_s=None, kept_x=None, kept_r=None, kept_gate=None, eps: float = 1e-6,
+                         stream=None):
+    """The end of a residual block: sum = residual_scale x + sigmoid(gate) norm(r) post_weight, and q, scales = the 8-bit
+    form of y = norm(sum) pre_weight.  x, r, sum, y [rows, cols] float32 / float16 / bfloat16 CUDA; gate [rows, cols] or
+    [rows, 1] of the same type; weights and residual_scale float32 [cols]; rstd_r, rstd_s float32 [rows].  kept_x, kept_r
+    and kept_gate, (q, scales) as fp8_empty(rows, cols) gives them, receive the operands in 8 bits for the backward."""
+    shape = rows, cols = x.shape
+    dt = x.dtype
+    _dtype(x, "x")
+    block = _sandwich(x, r, gate, dt, shape, post_weight, pre_weight, residual_scale)
+    out = rs_sandwich_out(
+        *_mat(sum, "sum", dt, shape), *_mat(y, "y", dt, shape),
+        _form(None if q is None and scales is None else (q, scales), "q", shape), _form(kept_x, "kept_x", shape),
+        _form(kept_r, "kept_r", shape), _form(kept_gate, "kept_gate", shape),
+        _vec(rstd_r, torch.float32, rows, "rstd_r"), _vec(rstd_s, torch.float32, rows, "rstd_s"))
+    _check("rs_sandwich_norm_fwd", lib().rs_sandwich_norm_fwd(block, eps, out, _stream(stream)))
+
+
+def rs_sandwich_norm_bwd_workspace_size(rows: int, cols: int) -> int:
+    return int(lib().rs_sandwich_norm_bwd_workspace_size(int(rows), int(cols)))
+
+
+def rs_sandwich_norm_bwd(x, r, post_weight, pre_weight, rstd_r, rstd_s, dL_dy, dL_dx, dL_dr, workspace, gate=None,
+                         dL_dgate=None, residual_scale=None, dL_dsum=None, dL_dpost_weight=None, dL_dpre_weight=None,
+                         dL_dresidual_scale=None, stream=None):
+    """Gradients of rs_sandwich_norm_fwd.  x, r and gate: the forward's matrices, or what it kept of them, (q, scales);
+    a gate of one a row always is the matrix.  The vectors' gradients and dL_dgate may be None."""
+    shape = rows, cols = dL_dy.shape
+    dt = dL_dy.dtype
+    _dtype(dL_dy, "dL_dy")
+    f32 = torch.float32
+    block = _sandwich(x, r, gate, dt, shape, post_weight, pre_weight, residual_scale)
+    grads = rs_sandwich_grads(
+        _vec(rstd_r, f32, rows, "rstd_r"), _vec(rstd_s, f32, rows, "rstd_s"), *_mat(dL_dy, "dL_dy", dt, shape),
+        *_mat(dL_dsum, "dL_dsum", dt, shape), *_mat(dL_dx, "dL_dx", dt, shape), *_mat(dL_dr, "dL_dr", dt, shape),
+        *_mat(dL_dgate, "dL_dgate", dt, (rows, block.gate_cols)),
+        _vec(dL_dresidual_scale, f32, cols, "dL_dresidual_scale"), _vec(dL_dpost_weight, f32, cols, "dL_dpost_weight"),
+        _vec(dL_dpre_weight, f32, cols, "dL_dpre_weight"))
+    _check("rs_sandwich_norm_bwd", lib().rs_sandwich_norm_bwd(
+        block, grads, _vec(workspace, torch.uint8, 0, "workspace"), 0 if workspace is None else workspace.numel(),
+        _stream(stream)))
+
+
+def rs_quantize_fp8_relu8(x, relu, q=None, scales=None, qt=None, scales_t=None, stream=None):
+    """rs_quantize_fp8 through a relu whose output was kept in 8 bits: x counts as zero where relu [rows, cols] (e4m3) is
+    <= 0."""
+    shape = rows, cols = x.shape
+    code = _dtype(x, "x")
+    px, sx = _mat(x, "x", x.dtype, shape)
+    pr, sr = _mat(relu, "relu", _FP8, shape)
+    pq, sq = _mat(q, "q", _FP8, shape)
+    pt, st = _mat(qt, "qt", _FP8, (cols, rows))
+    _check("rs_quantize_fp8_relu8", lib().rs_quantize_fp8_relu8(
+        rows, cols, code, px, sx, pr, sr, pq, sq, _scales(scales, "scales", _blocks(cols), rows), pt, st,
+        _scales(scales_t, "scales_t", _blocks(rows), cols), _stream(stream)))
+
+
+def rs_transpose_fp8(q, scales, qt, scales_t, stream=None):
+    """A kept matrix q [rows, cols] with scales [ceil(cols / 128), rows] as the operand of a weight's gradient: qt, scales_t
+    as fp8_empty(cols, rows), the 8-bit form of the transposed values."""
+    shape = rows, cols = q.shape
+    pq, sq = _mat(q, "q", _FP8, shape)
+    pt, st = _mat(qt, "qt", _FP8, (cols, rows))
+    _check("rs_transpose_fp8", lib().rs_transpose_fp8(
+        rows, cols, pq, sq, _scales(scales, "scales", _blocks(cols), rows), pt, st,
+        _scales(scales_t, "scales_t", _blocks(rows), cols), _stream(stream)))
+
+
+def rs_matmul_fp8_q_workspace_size(m: int, n: int, k: int) -> int:
+    return int(lib().rs_matmul_fp8_q_workspace_size(int(m), int(n), int(k)))
+
+
+def rs_matmul_fp8_q(a, a_scales, b, b_scales, q, scales, workspace=None, relu: bool = False, stream=None):
+    """rs_matmul_fp8 with its result in 8 bits: q [m, n], scales [ceil(n / 128), m] as fp8_empty(m, n) gives them."""
+    m, k = a.shape
+    n = b.shape[0]
+    kb = _blocks(k)
+    pa, sa = _mat(a, "a", _FP8, (m, k))
+    pb, sb = _mat(b, "b", _FP8, (n, k))
+    pq, sq = _mat(q, "q", _FP8, (m, n))
+    per_row = b_scales.shape == (kb, n)
+    _check("rs_matmul_fp8_q", lib().rs_matmul_fp8_q(
+        m, n, k, pa, sa, _scales(a_scales, "a_scales", kb, m), pb, sb,
+        _scales(b_scales, "b_scales", kb, n if per_row else _blocks(n)), 1 if per_row else RS_FP8_BLOCK, int(relu),
+        pq, sq, _scales(scales, "scales", _blocks(n), m), _vec(workspace, torch.uint8, 0, "workspace"),
         0 if workspace is None else workspace.numel(), _stream(stream)))
 
 

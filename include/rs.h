@@ -530,6 +530,128 @@ int rs_matmul_fp8(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_
                   int32_t b_scale_rows, int32_t relu, int32_t out_dtype, void* d_out, size_t out_stride,
                   void* d_workspace, size_t workspace_bytes, void* stream);
 
+/* One 8-bit matrix [rows][cols] with its scales [ceil(cols / 128)][rows]. */
+typedef struct rs_fp8_matrix {
+    uint8_t* d_q;
+    size_t stride;
+    float* d_scales;
+} rs_fp8_matrix;
+
+/* The end of a residual block: the norm after it, its gate, the residual's scale and sum, and the
+ * norm before what follows.  Per row, in float32, with x the residual stream, r the block's result
+ * and z its gate:
+ *   rstd_r = 1 / sqrt(mean(r^2) + eps),  rh = r rstd_r,  g = 1 / (1 + exp(-z)),
+ *   s = residual_scale x + g rh post_weight,
+ *   rstd_s = 1 / sqrt(mean(s^2) + eps),  y = s rstd_s pre_weight, and q = the 8-bit form of y.
+ * gate_cols: 0 (no gate, g = 1; d_gate is not read), 1 (one gate a row: z [rows][1]) or cols (one
+ * an element).  A gate below 2^-115 counts as exp(-80).  Weights and residual_scale [cols] are
+ * float32; residual_scale may be NULL (1).  The norm is taken of the sum before its rounding.
+ *
+ * x, r and an element's gate are matrices of `dtype`, or (in the backward alone) the 8-bit forms
+ * that the forward kept: then d_x_scales, d_r_scales and, for an element's gate, d_gate_scales are
+ * their scales; all of them or none.  A gate a row is always of `dtype`.
+ * 1 <= cols <= RS_NORM_MAX_COLS; rows = 0 is valid. */
+typedef struct rs_sandwich {
+    int32_t rows, cols;
+    int32_t dtype;
+    int32_t gate_cols;
+    const void* d_x;
+    size_t x_stride;
+    const float* d_x_scales;
+    const void* d_r;
+    size_t r_stride;
+    const float* d_r_scales;
+    const void* d_gate;
+    size_t gate_stride;
+    const float* d_gate_scales;
+    const float* d_residual_scale;
+    const float* d_post_weight;
+    const float* d_pre_weight;
+} rs_sandwich;
+
+/* What the forward writes; every pointer may be NULL, but not both d_y and q.d_q.  d_sum and d_y
+ * receive s and y in the block's type; kept_x, kept_r and kept_gate (an element's gate only) the
+ * 8-bit forms of the operands, for the backward.  d_rstd_r and d_rstd_s [rows] are the backward's
+ * statistics.  d_sum may be d_x or d_r (same stride).  Nothing else may overlap. */
+typedef struct rs_sandwich_out {
+    void* d_sum;
+    size_t sum_stride;
+    void* d_y;
+    size_t y_stride;
+    rs_fp8_matrix q;
+    rs_fp8_matrix kept_x;
+    rs_fp8_matrix kept_r;
+    rs_fp8_matrix kept_gate;
+    float* d_rstd_r;
+    float* d_rstd_s;
+} rs_sandwich_out;
+
+/* eps >= 0; with eps = 0 a row of zeros gives NaN.  Errors: RS_ERR_INVALID_ARG, RS_ERR_CUDA. */
+int rs_sandwich_norm_fwd(const rs_sandwich* block, float eps, const rs_sandwich_out* out, void* stream);
+
+/* Gradients of the block's operands from dL_dy and, where the sum has other uses, dL_dsum (may be
+ * NULL), the rounding to 8 bits taken as the identity.  With the operands as they are handed over
+ * (kept ones stand for q times scale), the forward's statistics, t = dL_dy pre_weight, sh = s rstd_s
+ * and n = rh post_weight:
+ *   ds = rstd_s (t - sh mean(t sh)) + dL_dsum,
+ *   dL_dx = residual_scale ds,   dL_dresidual_scale = sum over rows of ds x,
+ *   dL_dr = rstd_r (ds g post_weight - rh mean(ds g n)),   dL_dpost_weight = sum over rows of ds g rh,
+ *   dL_dgate = ds n g (1 - g), summed along the row for one gate a row,
+ *   dL_dpre_weight = sum over rows of dL_dy sh.
+ * All matrices have the block's type.  dL_dgate may be NULL, and so may each vector's gradient
+ * (float32 [cols], summed in a fixed order); with rows = 0 those given become zero.  An output
+ * matrix of cols columns may be d_dL_dy or d_dL_dsum (same stride); otherwise nothing overlaps.
+ * d_workspace: rs_sandwich_norm_bwd_workspace_size bytes (0 for invalid sizes), 16-byte aligned,
+ * contents undefined on entry and exit; not read when no vector's gradient is wanted.  Errors:
+ * RS_ERR_INVALID_ARG, RS_ERR_WORKSPACE, RS_ERR_CUDA. */
+typedef struct rs_sandwich_grads {
+    const float* d_rstd_r;
+    const float* d_rstd_s;
+    const void* d_dL_dy;
+    size_t dy_stride;
+    const void* d_dL_dsum;
+    size_t dsum_stride;
+    void* d_dL_dx;
+    size_t dx_stride;
+    void* d_dL_dr;
+    size_t dr_stride;
+    void* d_dL_dgate;
+    size_t dgate_stride;
+    float* d_dL_dresidual_scale;
+    float* d_dL_dpost_weight;
+    float* d_dL_dpre_weight;
+} rs_sandwich_grads;
+
+size_t rs_sandwich_norm_bwd_workspace_size(int32_t rows, int32_t cols);
+int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grads, void* d_workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* rs_quantize_fp8 through a relu whose output was kept in 8 bits: d_relu [rows][cols] are e4m3 bytes
+ * (rows on 16-byte boundaries); x counts as zero where they hold a value <= 0.  (A positive value
+ * that was rounded to zero when it was kept counts as zero here too, as it did in the products that
+ * read it.)  Scales do not matter and are not asked for. */
+int rs_quantize_fp8_relu8(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
+                          const uint8_t* d_relu, size_t relu_stride, uint8_t* d_q, size_t q_stride,
+                          float* d_scales, uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream);
+
+/* A kept matrix as the operand of a weight's gradient: d_q [rows][cols] with d_scales [ceil(cols /
+ * 128)][rows] becomes d_qt [cols][rows] with d_scales_t [ceil(rows / 128)][cols], the 8-bit form of
+ * the transposed float32 values q * scale.  rows or cols = 0 is valid.  Input and output must not
+ * overlap.  Errors: RS_ERR_INVALID_ARG, RS_ERR_CUDA. */
+int rs_transpose_fp8(int32_t rows, int32_t cols, const uint8_t* d_q, size_t q_stride, const float* d_scales,
+                     uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream);
+
+/* rs_matmul_fp8 with its result in 8 bits: d_q [m][n] with d_scales [ceil(n / 128)][m], the 8-bit
+ * form of the float32 sums (after the relu, where asked for), ready to be the next product's
+ * operand and to be kept for the backward.  k = 0 gives the form of zeros.  Operands, relu and
+ * errors as rs_matmul_fp8; d_workspace: rs_matmul_fp8_q_workspace_size bytes (0: none needed, may
+ * be NULL). */
+size_t rs_matmul_fp8_q_workspace_size(int32_t m, int32_t n, int32_t k);
+int rs_matmul_fp8_q(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride,
+                    const float* d_a_scales, const uint8_t* d_b, size_t b_stride, const float* d_b_scales,
+                    int32_t b_scale_rows, int32_t relu, uint8_t* d_q, size_t q_stride, float* d_scales,
+                    void* d_workspace, size_t workspace_bytes, void* stream);
+
 /* One gradient tensor: `count` contiguous values of `dtype`.  d_out (may be NULL; may be d_grad)
  * receives the clipped values, in the same type.  With an activation (RS_ACT_*), d_param holds
  * the stored float32 parameters and the gradient counts in the norm as dL/dparam = d_grad *
