@@ -298,67 +298,151 @@ class WideAppearance:
     with root-mean-square norms, every product on 8-bit operands (float32 sums, `dtype` activations) and float32 master
     weights.  `forward` gives the planar colours that rs_project reads when sh_degree is -1, `backward` takes
     the colours' gradient that rs_rasterize_bwd returns, and `step` is one Adam step over all parameters (and the caller's own
-    groups) with their gradients clipped to a global norm; nothing in the three waits on the host."""
+    groups) with their gradients clipped to a global norm; nothing in the three waits on the host.
 
-    def __init__(self, features: torch.Tensor, hidden: int, blocks: int = 2, dtype=torch.bfloat16, seed: int = 0):
+    sandwich: a norm after every block too, and a learned scale a_b [width] of the residual stream,
+
+        h_{b+1} = a_b h_b + g_b norm'_b(r_b),
+
+    with gates g_b = sigmoid(norm_b(h_b) Wg_b^T), one for each Gaussian (gate="row") or for each of its features
+    (gate="element"), or 1 (None).
+
+    checkpoints: what the forward keeps for the backward is kept in 8 bits: the norms' and relus' outputs, which the
+    products read in that form anyway, and a sandwich block's operands, from which its backward then starts (a block of the
+    plain kind keeps its residual stream in `dtype`).  The forward's colours are the same."""
+
+    def __init__(self, features: torch.Tensor, hidden: int, blocks: int = 2, dtype=torch.bfloat16, seed: int = 0,
+                 sandwich: bool = False, gate: str | None = None, checkpoints: bool = False):
         n, c = features.shape
         if 3 * blocks + 3 > rs.RS_ADAM_MAX_SEGMENTS:
             raise ValueError(f"at most {(rs.RS_ADAM_MAX_SEGMENTS - 3) // 3} blocks")
+        if gate not in (None, "row", "element") or (gate and not sandwich):
+            raise ValueError("a gate is 'row', 'element' or None, and needs sandwich blocks")
         self.n, self.width, self.hidden, self.dtype = int(n), int(c), int(hidden), dtype
+        self.sandwich, self.checkpoints = bool(sandwich), bool(checkpoints)
         self.device = dev = features.device
         g = torch.Generator(dev).manual_seed(seed)
         rand = lambda o, i: torch.randn(o, i, device=dev, generator=g) / i ** 0.5
         self.features, self.dfeatures = features, torch.empty_like(features)
-        self.norms = [torch.ones(c, device=dev) for _ in range(blocks + 1)]
-        self.dnorms = [torch.empty(c, device=dev) for _ in range(blocks + 1)]
+        if sandwich:
+            # every vector is a row of one parameter (rows on 16-byte boundaries: the columns past the width stay as they are)
+            self.vectors = torch.ones(3 * blocks + 1, -(-c // 4) * 4, device=dev)
+            self.dvectors = torch.zeros_like(self.vectors)
+            split = lambda t: (lambda r: (r[:blocks + 1], r[blocks + 1:2 * blocks + 1], r[2 * blocks + 1:]))(
+                [row[:c] for row in t])
+            (self.norms, self.posts, self.scales), (self.dnorms, self.dposts, self.dscales) = map(
+                split, (self.vectors, self.dvectors))
+        else:
+            self.norms = [torch.ones(c, device=dev) for _ in range(blocks + 1)]
+            self.dnorms = [torch.empty(c, device=dev) for _ in range(blocks + 1)]
         self.up = [_Linear(rand(hidden, c)) for _ in range(blocks)]
         self.down = [_Linear(rand(c, hidden)) for _ in range(blocks)]
         self.head = _Linear(rand(3, c))
+        gates = {None: 0, "row": 1, "element": c}[gate]
+        self.gates = [_Linear(rand(gates, c)) for _ in range(blocks)] if gate else [None] * blocks
         e = lambda r, k, d=dtype: torch.empty(r, k, dtype=d, device=dev)
-        # kept for the backward: each norm's input sum, output and statistic, each relu's output
-        self.h = [e(n, c) for _ in range(blocks + 1)]
-        self.y = [e(n, c) for _ in range(blocks + 1)]
+        q8 = lambda r, k: rs.fp8_empty(r, k, dev)
+        # kept for the backward: each norm's input sum, output and statistic, each relu's output; of a sandwich block also
+        # its result, its gate and their statistic
+        fewer = checkpoints and sandwich
+        self.h = [e(n, c)] * (blocks + 1) if fewer else [e(n, c) for _ in range(blocks + 1)]
         self.rstd = [torch.empty(n, dtype=torch.float32, device=dev) for _ in range(blocks + 1)]
-        self.u = [e(n, hidden) for _ in range(blocks)]
+        if checkpoints:
+            self.yq, self.uq = [q8(n, c) for _ in range(blocks + 1)], [q8(n, hidden) for _ in range(blocks)]
+        else:
+            self.y, self.u = [e(n, c) for _ in range(blocks + 1)], [e(n, hidden) for _ in range(blocks)]
+        if sandwich:
+            self.rstd_r = [torch.empty(n, dtype=torch.float32, device=dev) for _ in range(blocks)]
+            self.results = [e(n, c)] * blocks if fewer else [e(n, c) for _ in range(blocks)]
+            self.zs = [None] * blocks
+            if gate:
+                self.zs = [e(n, gates)] * blocks if fewer and gate == "element" else [e(n, gates) for _ in range(blocks)]
+            if fewer:
+                kept = ("x", "r") + (("gate",) if gate == "element" else ())
+                self.kept = [{k: q8(n, c) for k in kept} for _ in range(blocks)]
         # scratch: 8-bit operands by rows and by columns, gradients, results of products
-        self.qc, self.qct = rs.fp8_empty(n, c, dev), rs.fp8_empty(c, n, dev)
-        self.qh, self.qht = rs.fp8_empty(n, hidden, dev), rs.fp8_empty(hidden, n, dev)
-        self.q3, self.q3t = rs.fp8_empty(n, 3, dev), rs.fp8_empty(3, n, dev)
+        self.qc, self.qct = q8(n, c), q8(c, n)
+        self.qh, self.qht = q8(n, hidden), q8(hidden, n)
+        self.q3, self.q3t = q8(n, 3), q8(3, n)
         self.r, self.dh, self.dy, self.du = e(n, c), e(n, c), e(n, c), e(n, hidden)
+        if sandwich:
+            self.dr = e(n, c)
+            if gate:
+                self.dgate, self.qg, self.qgt = e(n, gates), q8(n, gates), q8(gates, n)
         self.z = torch.empty(n, 3, dtype=torch.float32, device=dev)
         self.colors = torch.empty(3, n, dtype=torch.float32, device=dev)
         sizes = [(n, hidden, c), (n, c, hidden), (n, 3, c), (n, c, 3), (hidden, c, n), (c, hidden, n), (3, c, n)]
+        if gate:
+            sizes += [(n, gates, c), (n, c, gates), (gates, c, n)]
         need = max([rs.rs_matmul_fp8_workspace_size(*s) for s in sizes] +
                    [rs.rs_rms_norm_bwd_workspace_size(n, c), rs.rs_grad_norm_workspace_size(rs.RS_ADAM_MAX_SEGMENTS)])
+        if checkpoints:
+            need = max(need, rs.rs_matmul_fp8_q_workspace_size(n, hidden, c))
+        if sandwich:
+            need = max(need, rs.rs_sandwich_norm_bwd_workspace_size(n, c))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
         self.moments = None
         self.steps = torch.zeros(1, dtype=torch.int32, device=dev)  # taken so far: skipped ones do not count
 
+    def kept_bytes(self) -> int:
+        """Bytes of activations that live from the forward to the backward."""
+        blocks = len(self.up)
+        rows = [*self.h[:blocks + 1], *self.rstd]
+        rows += [t for pair in (*self.yq, *self.uq) for t in pair] if self.checkpoints else [*self.y, *self.u]
+        if self.sandwich:
+            rows += [*self.rstd_r, *self.results, *(z for z in self.zs if z is not None)]
+            rows += [t for k in getattr(self, "kept", ()) for pair in k.values() for t in pair]
+        return sum({t.data_ptr(): t.numel() * t.element_size() for t in rows}.values())
+
     def _product(self, a, b, b_scales, out, relu=False):
         rs.rs_matmul_fp8(*a, b, b_scales, out, self.workspace, relu=relu)
+
+    def _hidden(self, b, y):
+        """The relu of block b's first layer in 8 bits, the second layer's operand, from the norm's output."""
+        up = self.up[b]
+        if self.checkpoints:
+            rs.rs_matmul_fp8_q(*y, up.q, up.s, *self.uq[b], self.workspace, relu=True)
+            return self.uq[b]
+        self._product(y, up.q, up.s, self.u[b], relu=True)
+        rs.rs_quantize_fp8(self.u[b], *self.qh)
+        return self.qh
 
     def forward(self, stream=None) -> torch.Tensor:
         """colours [3, n] (planar) of the features and weights as they are."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.device)):
-            x, residual = self.h[0], None
+            x, residual, last = self.h[0], None, len(self.up)
             x.copy_(self.features)
-            for b in range(len(self.up) + 1):
-                rs.rs_rms_norm_fwd(x, self.norms[b], *self.qc, residual=residual, sum=self.h[b] if b else None,
-                                   y=self.y[b], rstd=self.rstd[b])
-                if b == len(self.up):
+            y = lambda b: self.yq[b] if self.checkpoints else self.qc
+            wide = lambda b: None if self.checkpoints else self.y[b]
+            for b in range(last + 1):
+                if b == 0 or not self.sandwich:
+                    rs.rs_rms_norm_fwd(x, self.norms[b], *y(b), residual=residual, sum=self.h[b] if b else None,
+                                       y=wide(b), rstd=self.rstd[b])
+                if b == last:
                     break
-                self._product(self.qc, self.up[b].q, self.up[b].s, self.u[b], relu=True)
-                rs.rs_quantize_fp8(self.u[b], *self.qh)
-                self._product(self.qh, self.down[b].q, self.down[b].s, self.r)
-                x, residual = self.h[b], self.r
-            self._product(self.qc, self.head.q, self.head.s, self.z)
+                r = self.results[b] if self.sandwich else self.r
+                self._product(self._hidden(b, y(b)), self.down[b].q, self.down[b].s, r)
+                if self.sandwich:
+                    if self.gates[b]:
+                        self._product(y(b), self.gates[b].q, self.gates[b].s, self.zs[b])
+                    kept = {f"kept_{k}": v for k, v in self.kept[b].items()} if self.checkpoints else {}
+                    rs.rs_sandwich_norm_fwd(x, r, self.posts[b], self.norms[b + 1], *y(b + 1), gate=self.zs[b],
+                                            residual_scale=self.scales[b], sum=self.h[b + 1], y=wide(b + 1),
+                                            rstd_r=self.rstd_r[b], rstd_s=self.rstd[b + 1], **kept)
+                    x = self.h[b + 1]
+                else:
+                    x, residual = self.h[b], self.r
+            self._product(y(last), self.head.q, self.head.s, self.z)
             torch.sigmoid(self.z.t(), out=self.colors)
         return self.colors
 
     def _weight_grad(self, grad_t, x, scratch_t, layer):
-        """layer.dw = grad^T x, both in 8 bits by columns."""
-        rs.rs_quantize_fp8(x, qt=scratch_t[0], scales_t=scratch_t[1])
+        """layer.dw = grad^T x, both in 8 bits by columns; x a matrix, or one kept in 8 bits by rows."""
+        if type(x) is tuple:
+            rs.rs_transpose_fp8(*x, *scratch_t)
+        else:
+            rs.rs_quantize_fp8(x, qt=scratch_t[0], scales_t=scratch_t[1])
         self._product(grad_t, *scratch_t, layer.dw)
 
     @staticmethod
@@ -368,7 +452,8 @@ class WideAppearance:
         return ((127 - e) << 23).view(torch.float32), ((127 + e) << 23).view(torch.float32)
 
     def backward(self, dL_dcolors: torch.Tensor, stream=None):
-        """Gradients of every weight (dnorms, the layers' dw) and of the features from dL/dcolours [3, n].
+        """Gradients of every weight (dnorms, the layers' dw; of sandwich blocks dposts and dscales) and of the features from
+        dL/dcolours [3, n].
 
         float16 activations hold nothing much below 6e-8, and a loss over an image has gradients of that size: between the
         layers they then carry a power of two, exact in every step, that is taken out of what leaves."""
@@ -380,35 +465,74 @@ class WideAppearance:
                 up, down = self._powers(dz)
                 dz.mul_(up)
                 undo = lambda t: t.mul_(down)
+            y, u = (self.yq, self.uq) if self.checkpoints else (self.y, self.u)
             rs.rs_quantize_fp8(dz, *self.q3, *self.q3t)
             undo(self.q3t[1])  # a weight's gradient takes it out with the scales of the gradient's transposed form
-            self._weight_grad(self.q3t, self.y[last], self.qct, self.head)
+            self._weight_grad(self.q3t, y[last], self.qct, self.head)
             self._product(self.q3, self.head.qt, self.head.st, self.dy)
-            rs.rs_rms_norm_bwd(self.h[last], self.norms[last], self.rstd[last], self.dy, self.dh, self.dnorms[last],
-                               self.workspace)
-            undo(self.dnorms[last])
+            if not self.sandwich:
+                self._norm_backward(last, self.h[last], None, undo)
             for b in reversed(range(last)):
-                # dh is the gradient of h_{b+1} = h_b + r_b: of r_b as it is, of h_b with what comes through the block
-                rs.rs_quantize_fp8(self.dh, *self.qc, *self.qct)
+                dr = self.dh
+                if self.sandwich:
+                    dr = self.dr
+                    self._sandwich_backward(b, undo)
+                # without one, dh is the gradient of h_{b+1} = h_b + r_b: of r_b as it is, of h_b with what comes through the
+                # block
+                rs.rs_quantize_fp8(dr, *self.qc, *self.qct)
                 undo(self.qct[1])
-                self._weight_grad(self.qct, self.u[b], self.qht, self.down[b])
+                self._weight_grad(self.qct, u[b], self.qht, self.down[b])
                 self._product(self.qc, self.down[b].qt, self.down[b].st, self.du)
-                rs.rs_quantize_fp8(self.du, *self.qh, *self.qht, relu=self.u[b])
+                if self.checkpoints:
+                    rs.rs_quantize_fp8_relu8(self.du, u[b][0], *self.qh, *self.qht)
+                else:
+                    rs.rs_quantize_fp8(self.du, *self.qh, *self.qht, relu=u[b])
                 undo(self.qht[1])
-                self._weight_grad(self.qht, self.y[b], self.qct, self.up[b])
+                self._weight_grad(self.qht, y[b], self.qct, self.up[b])
                 self._product(self.qh, self.up[b].qt, self.up[b].st, self.dy)
-                rs.rs_rms_norm_bwd(self.h[b], self.norms[b], self.rstd[b], self.dy, self.dh, self.dnorms[b],
-                                   self.workspace, dL_dsum=self.dh)
-                undo(self.dnorms[b])
+                if self.gates[b]:
+                    # the block's norm feeds its gate too; dr has been read
+                    rs.rs_quantize_fp8(self.dgate, *self.qg, *self.qgt)
+                    undo(self.qgt[1])
+                    self._product(self.qg, self.gates[b].qt, self.gates[b].st, self.dr)
+                    self.dy.add_(self.dr)
+                    self._product(self.qgt, *self.qct, self.gates[b].dw)  # qct still holds the norm's output by columns
+                if not self.sandwich:
+                    self._norm_backward(b, self.h[b], self.dh, undo)
+            if self.sandwich:
+                x = self.h[0]
+                if self.checkpoints:  # the stream has moved on: the features once more
+                    x = self.r
+                    x.copy_(self.features)
+                self._norm_backward(0, x, self.dh if last else None, undo)
             if down is None:
                 self.dfeatures.copy_(self.dh)
             else:
                 torch.mul(self.dh, down, out=self.dfeatures)  # in float32: down is a tensor of one dimension
 
+    def _norm_backward(self, b, x, dsum, undo):
+        rs.rs_rms_norm_bwd(x, self.norms[b], self.rstd[b], self.dy, self.dh, self.dnorms[b], self.workspace, dL_dsum=dsum)
+        undo(self.dnorms[b])
+
+    def _sandwich_backward(self, b, undo):
+        """From dy and dh (the gradient of h_{b+1} by its later uses) to dr, dh of h_b's direct use and the gate's gradient."""
+        kept = self.kept[b] if self.checkpoints else {"x": self.h[b], "r": self.results[b]}
+        rs.rs_sandwich_norm_bwd(
+            kept["x"], kept["r"], self.posts[b], self.norms[b + 1], self.rstd_r[b], self.rstd[b + 1], self.dy, self.dh,
+            self.dr, self.workspace, gate=kept.get("gate", self.zs[b]), dL_dgate=self.dgate if self.gates[b] else None,
+            residual_scale=self.scales[b], dL_dsum=self.dh if b + 1 < len(self.up) else None,
+            dL_dpost_weight=self.dposts[b], dL_dpre_weight=self.dnorms[b + 1], dL_dresidual_scale=self.dscales[b])
+        for t in (self.dposts[b], self.dnorms[b + 1], self.dscales[b]):
+            undo(t)
+
+    def _layers(self):
+        return [l for l in (*self.up, *self.down, *self.gates, self.head) if l is not None]
+
     def parameters(self):
-        """(parameter, gradient) of every group: the features, the norms, the layers."""
-        return ([(self.features, self.dfeatures)] + list(zip(self.norms, self.dnorms)) +
-                [(l.w, l.dw) for l in (*self.up, *self.down, self.head)])
+        """(parameter, gradient) of every group: the features, the norms (of a sandwich network all vectors as one), the
+        layers."""
+        vectors = [(self.vectors, self.dvectors)] if self.sandwich else list(zip(self.norms, self.dnorms))
+        return [(self.features, self.dfeatures)] + vectors + [(l.w, l.dw) for l in self._layers()]
 
     def step(self, max_norm: float, lr: float = 1e-3, groups=(), stream=None):
         """One clipped Adam step over the network and `groups` (rs.AdamGroup, e.g. the geometry's); the norm before
@@ -422,7 +546,7 @@ class WideAppearance:
                 self.moments = [(torch.zeros_like(p), torch.zeros_like(p)) for p, _ in self.parameters()]
             own = [rs.AdamGroup(p, g, m, v, lr) for (p, g), (m, v) in zip(self.parameters(), self.moments)]
             rs.rs_adam_step_clipped([*own, *groups], self.steps, max_norm, self.norm, self.workspace)
-            for layer in (*self.up, *self.down, self.head):
+            for layer in self._layers():
                 layer.refresh()
 
 
