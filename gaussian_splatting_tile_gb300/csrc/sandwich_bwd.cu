@@ -1,0 +1,609 @@
+#include "sandwich.cuh"
+
+namespace rs {
+namespace {
+
+// ---------------------------------------------------------------- backward
+// Eight values of an operand as they are stored, or of its checkpoint.
+template <typename T, bool KEPT, bool VEC>
+struct Operand8 {
+    Run8<T> v;
+    __device__ __forceinline__ void load(const Stored& s, long long row, int, int c, int left) {
+        v.template load<VEC>(static_cast<const T*>(s.p) + row * s.stride + c, left, c > 0);
+    }
+    __device__ __forceinline__ float2 pair(int p) const { return v.pair(p); }
+};
+template <typename T, bool VEC>
+struct Operand8<T, true, VEC> {
+    Bytes8 v;
+    float scale;
+    __device__ __forceinline__ void load(const Stored& s, long long row, int rows, int c, int left) {
+        v.load(static_cast<const uint8_t*>(s.p) + row * s.stride + c, left);
+        scale = left > 0 ? s.scales[size_t(c / kBlock) * rows + row] : 0.f;
+    }
+    __device__ __forceinline__ float2 pair(int p) const {
+        const float2 f = v.pair(p);
+        return make_float2(f.x * scale, f.y * scale);
+    }
+};
+
+// Everything of eight columns that the two passes over a row need.
+template <typename T, bool KEPT, bool VEC>
+struct BwdRun {
+    Operand8<T, KEPT, VEC> x, r, z;
+    Run8<T> dy, ds;
+    __device__ __forceinline__ void load(const SandwichBwdArgs& a, long long row, int c, int left) {
+        x.load(a.x, row, a.rows, c, left);
+        r.load(a.r, row, a.rows, c, left);
+        if (a.gate == kElementGate) z.load(a.z, row, a.rows, c, left);
+        dy.template load<VEC>(static_cast<const T*>(a.dy) + row * a.dys + c, left, c > 0);
+        if (a.ds) ds.template load<VEC>(static_cast<const T*>(a.ds) + row * a.dss + c, left, c > 0);
+    }
+};
+struct BwdRow {
+    float rstd_r, rstd_s, e, g;       // e, g: of the row's gate (0, 1 without a gate)
+};
+struct BwdWeights { float post[8], pre[8], alpha[8]; };
+
+struct BwdValue { float x, rh, n, p, sh, t, e, g, dy, ds; };
+
+template <typename T, bool KEPT, bool VEC>
+__device__ __forceinline__ void values(const SandwichBwdArgs& a, const BwdRun<T, KEPT, VEC>& u, const BwdRow& w,
+                                       const BwdWeights& k, int p, BwdValue (&o)[2]) {
+    const float2 x = u.x.pair(p), r = u.r.pair(p), dy = u.dy.pair(p);
+    const float2 ds = a.ds ? u.ds.pair(p) : make_float2(0.f, 0.f);
+    const float2 z = a.gate == kElementGate ? u.z.pair(p) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        BwdValue& v = o[j];
+        v.x = j ? x.y : x.x;
+        v.e = w.e;
+        v.g = w.g;
+        if (a.gate == kElementGate) {
+            v.e = gate_e(j ? z.y : z.x);
+            v.g = gate_of(v.e);
+        }
+        v.rh = (j ? r.y : r.x) * w.rstd_r;
+        v.n = v.rh * k.post[2 * p + j];
+        v.p = v.g * v.n;
+        v.sh = fmaf(v.g, v.n, a.alpha ? v.x * k.alpha[2 * p + j] : v.x) * w.rstd_s;
+        v.dy = j ? dy.y : dy.x;
+        v.t = v.dy * k.pre[2 * p + j];
+        v.ds = j ? ds.y : ds.x;
+    }
+}
+
+// Rows of more than 4096 columns: a block's row has more values than its registers hold, so it is read twice (the second
+// time from L2) and a thread's shares of the vectors' gradients stay in shared memory.
+template <typename T, bool KEPT, bool VEC, int TPR, int RUNS>
+__global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant__ SandwichBwdArgs a) {
+    RS_PDL_ENTER();
+    __shared__ float smem[2][TPR / 32 * 3];
+    extern __shared__ float shares[];        // [3][RUNS][8][TPR]
+    const int t = threadIdx.x;
+    int turn = 0;
+    const auto share = [&](int k, int i, int j) -> float& { return shares[((k * RUNS + i) * 8 + j) * TPR + t]; };
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) share(k, i, j) = 0.f;
+    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        BwdRow w{a.rstd_r[row], a.rstd_s[row], 0.f, 1.f};
+        if (a.gate == kRowGate) {
+            w.e = gate_e(to_f(static_cast<const T*>(a.z.p)[row * a.z.stride]));
+            w.g = gate_of(w.e);
+        }
+        BwdRun<T, KEPT, VEC> u;
+        float sums[3] = {0.f, 0.f, 0.f};
+        BwdWeights k;
+        const auto load = [&](int c) {
+            const int left = a.cols - c;
+            u.load(a, row, c, left);
+            load8<float, VEC>(a.wpost + c, left, k.post);
+            load8<float, VEC>(a.wpre + c, left, k.pre);
+            if (a.alpha) load8<float, VEC>(a.alpha + c, left, k.alpha);
+        };
+#pragma unroll 1
+        for (int i = 0; i < RUNS; ++i) {
+            load((i * TPR + t) * 8);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                BwdValue v[2];
+                values<T, KEPT, VEC>(a, u, w, k, p, v);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    sums[0] = fmaf(v[j].t, v[j].sh, sums[0]);
+                    sums[1] = fmaf(fmaf(w.rstd_s, v[j].t, v[j].ds), v[j].p, sums[1]);
+                    sums[2] = fmaf(v[j].sh, v[j].p, sums[2]);
+                }
+            }
+        }
+        row_sums<TPR>(sums, smem[turn ^= 1]);
+        const float c1 = w.rstd_s * (sums[0] * a.inv_cols);
+        const float dot = fmaf(-c1, sums[2], sums[1]);           // sum of ds p
+        const float c2 = dot * a.inv_cols;
+        if (a.gate == kRowGate && a.dz && t == 0)
+            static_cast<T*>(a.dz)[row * a.dzs] = from_f<T>(dot * (w.e * w.g));
+#pragma unroll 1
+        for (int i = 0; i < RUNS; ++i) {
+            const int c = (i * TPR + t) * 8, left = a.cols - c;
+            load(c);
+            float dx[8], dr[8], dz[8];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                BwdValue v[2];
+                values<T, KEPT, VEC>(a, u, w, k, p, v);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int e = 2 * p + j;
+                    const float ds = fmaf(-c1, v[j].sh, fmaf(w.rstd_s, v[j].t, v[j].ds));
+                    const float dn = ds * v[j].g;
+                    share(0, i, e) = fmaf(v[j].dy, v[j].sh, share(0, i, e));
+                    share(1, i, e) = fmaf(dn, v[j].rh, share(1, i, e));
+                    share(2, i, e) = fmaf(ds, v[j].x, share(2, i, e));
+                    dx[e] = a.alpha ? ds * k.alpha[e] : ds;
+                    dr[e] = w.rstd_r * fmaf(-v[j].rh, c2, dn * k.post[e]);
+                    dz[e] = ds * v[j].p * (v[j].e * v[j].g);
+                }
+            }
+            if (left > 0) {
+                store8<T, VEC>(static_cast<T*>(a.dx) + row * a.dxs + c, left, dx);
+                store8<T, VEC>(static_cast<T*>(a.dr) + row * a.drs + c, left, dr);
+                if (a.gate == kElementGate && a.dz) store8<T, VEC>(static_cast<T*>(a.dz) + row * a.dzs + c, left, dz);
+            }
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + size_t(blockIdx.x) * 3 * a.cols;
+    for (int k = 0; k < 3; ++k)
+        for (int i = 0; i < RUNS; ++i)
+            for (int j = 0; j < 8; ++j) {
+                const int c = (i * TPR + t) * 8 + j;
+                if (c < a.cols) part[size_t(k) * a.cols + c] = share(k, i, j);
+            }
+}
+
+// ---- up to 4096 columns
+// The copies of a row's operands on their way: every thread copies its own runs into a place of its own and reads them
+// back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
+                 : "memory");
+}
+
+template <typename T, bool KEPT, int TPR, int RUNS>
+struct Ring {
+    static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+    static constexpr int kUnit = int(sizeof(T)) / 2;                           // 16-byte words of a run
+    static constexpr int kWide = (KEPT ? 2 : 5) * RUNS * kUnit, kNarrow = KEPT ? 3 * RUNS : 0;
+    static constexpr int kStage = kThreads * (16 * kWide + 8 * kNarrow);
+    static constexpr int kStages = kStage <= 24 * 1024 ? 3 : 2;
+    static constexpr int kBytes = kStages * kStage;
+    static constexpr int kBlocks = kThreads > 128 ? 1 : RUNS == 1 ? 3 : 2;   // an SM: registers
+    static __device__ __forceinline__ uint8_t* wide(uint8_t* ring, int stage, int u) {
+        return ring + stage * kStage + (u * kThreads + int(threadIdx.x)) * 16;
+    }
+    static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int u) {
+        return ring + stage * kStage + kWide * kThreads * 16 + (u * kThreads + int(threadIdx.x)) * 8;
+    }
+};
+
+// One run of a matrix of T on its way into the ring.
+template <typename R, typename T>
+__device__ __forceinline__ void send(uint8_t* ring, int stage, int u, const T* p, int left) {
+    if (left >= 8) {
+#pragma unroll
+        for (int i = 0; i < R::kUnit; ++i) copy16(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
+    } else if (left > 0) {
+        Run8<T> v;
+        v.template load<true>(p, left);
+        float4 w[R::kUnit];
+        memcpy(w, &v, sizeof(w));
+#pragma unroll
+        for (int i = 0; i < R::kUnit; ++i) *reinterpret_cast<float4*>(R::wide(ring, stage, u + i)) = w[i];
+    }
+}
+template <typename R, typename T>
+__device__ __forceinline__ void receive(uint8_t* ring, int stage, int u, bool live, Run8<T>& v) {
+    float4 w[R::kUnit];
+#pragma unroll
+    for (int i = 0; i < R::kUnit; ++i)
+        w[i] = live ? *reinterpret_cast<const float4*>(R::wide(ring, stage, u + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+    memcpy(&v, w, sizeof(w));
+}
+
+// A run of an operand: as it is stored, or its checkpoint's bytes and scale.
+template <typename T, bool KEPT>
+struct Held {
+    Run8<T> v;
+    __device__ __forceinline__ float2 pair(int p, float) const { return v.pair(p); }
+};
+template <typename T>
+struct Held<T, true> {
+    Bytes8 v;
+    __device__ __forceinline__ float2 pair(int p, float scale) const { return f2_mul(v.pair(p), f2(scale)); }
+};
+
+// What a row has one number of, or one for each 128 columns.
+template <int RUNS>
+struct RowNumbers {
+    float rstd_r, rstd_s, z, scales[3][RUNS];
+};
+
+// A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its shares of the
+// vectors' gradients stay in its registers and leave once per block, to be added up in a fixed order.
+template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUNS>::kBlocks))
+    k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
+    RS_PDL_ENTER();
+    using R = Ring<T, KEPT, TPR, RUNS>;
+    constexpr bool VEC = MOVE != kAny, FULL = MOVE == kFull;
+    constexpr int kThreads = R::kThreads, kRows = kThreads / TPR, kStages = R::kStages, kU = R::kUnit;
+    __shared__ float smem[2][kThreads / 32 * 3];
+    extern __shared__ __align__(16) uint8_t ring[];
+    const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const bool element = a.gate == kElementGate;
+    float2 acc[3][RUNS][4];
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+            for (int p = 0; p < 4; ++p) acc[k][i][p] = f2(0.f);
+    const auto column = [&](int i) { return (i * TPR + t) * 8; };
+    const auto rest = [&](int i) { return FULL ? 8 : a.cols - column(i); };
+    const auto numbers = [&](long long row) {
+        RowNumbers<RUNS> n{};
+        if (row >= a.rows) return n;
+        n.rstd_r = a.rstd_r[row];
+        n.rstd_s = a.rstd_s[row];
+        if (a.gate == kRowGate) n.z = to_f(static_cast<const T*>(a.z.p)[row * a.z.stride]);
+        if constexpr (KEPT) {
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i)
+                if (rest(i) > 0) {
+                    const size_t at = size_t(column(i) / kBlock) * a.rows + row;
+                    n.scales[0][i] = a.x.scales[at];
+                    n.scales[1][i] = a.r.scales[at];
+                    if (element) n.scales[2][i] = a.z.scales[at];
+                }
+        }
+        return n;
+    };
+    const auto operand = [&](const Stored& s, long long row, int stage, int k, int i) {
+        if constexpr (KEPT) {
+            const uint8_t* p = static_cast<const uint8_t*>(s.p) + row * s.stride + column(i);
+            uint8_t* to = R::narrow(ring, stage, k * RUNS + i);
+            if (rest(i) >= 8) {
+                copy8(to, p);
+            } else if (rest(i) > 0) {
+                Bytes8 b;
+                b.load(p, rest(i));
+                *reinterpret_cast<uint2*>(to) = b.w;
+            }
+        } else {
+            send<R>(ring, stage, ((2 + k) * RUNS + i) * kU, static_cast<const T*>(s.p) + row * s.stride + column(i), rest(i));
+        }
+    };
+    const auto fetch = [&](long long row, int stage) {
+        if (row < a.rows)
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                operand(a.x, row, stage, 0, i);
+                operand(a.r, row, stage, 1, i);
+                if (element) operand(a.z, row, stage, 2, i);
+                send<R>(ring, stage, i * kU, static_cast<const T*>(a.dy) + row * a.dys + column(i), rest(i));
+                if (a.ds)
+                    send<R>(ring, stage, (RUNS + i) * kU, static_cast<const T*>(a.ds) + row * a.dss + column(i), rest(i));
+            }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const long long step = (long long)gridDim.x * kRows;
+    const long long first = (long long)blockIdx.x * kRows + sub;
+    RowNumbers<RUNS> now = numbers(first);
+    if constexpr (VEC) {
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
+    }
+    int stage = 0, turn = 0;
+    for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += step) {
+        const long long row = base + sub;
+        const bool in = row < a.rows;
+        const RowNumbers<RUNS> next = numbers(row + step);
+        if constexpr (VEC) {
+            fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        }
+        float row_e = 0.f, row_g = 1.f;
+        if (a.gate == kRowGate) {
+            row_e = gate_e(now.z);
+            row_g = gate_of(row_e);
+        }
+        Held<T, KEPT> xv[RUNS];
+        float2 sh[RUNS][4], ds[RUNS][4], g[RUNS][4], rest_g[RUNS][4], rh[RUNS][4];  // rest_g: 1 - g
+        float2 s0 = f2(0.f), s1 = f2(0.f), s2 = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const bool live = in && (FULL || rest(i) > 0);
+            Held<T, KEPT> rv, zv;
+            Run8<T> dy, up;
+            const auto take = [&](const Stored& s, int k, Held<T, KEPT>& h) {
+                if constexpr (KEPT && VEC) {
+                    h.v.w = live ? *reinterpret_cast<const uint2*>(R::narrow(ring, stage, k * RUNS + i)) : make_uint2(0u, 0u);
+                } else if constexpr (KEPT) {
+                    h.v.load(static_cast<const uint8_t*>(s.p) + (in ? row : 0) * s.stride + column(i), in ? rest(i) : 0);
+                } else if constexpr (VEC) {
+                    receive<R>(ring, stage, ((2 + k) * RUNS + i) * kU, live, h.v);
+                } else {
+                    h.v.template load<false>(static_cast<const T*>(s.p) + (in ? row : 0) * s.stride + column(i),
+                                             in ? rest(i) : 0, column(i) > 0);
+                }
+            };
+            const auto take_grad = [&](const void* p, size_t stride, int k, Run8<T>& v) {
+                if constexpr (VEC)
+                    receive<R>(ring, stage, (k * RUNS + i) * kU, live, v);
+                else
+                    v.template load<false>(static_cast<const T*>(p) + (in ? row : 0) * stride + column(i), in ? rest(i) : 0,
+                                           column(i) > 0);
+            };
+            take(a.x, 0, xv[i]);
+            take(a.r, 1, rv);
+            if (element) take(a.z, 2, zv);
+            take_grad(a.dy, a.dys, 0, dy);
+            if (a.ds) take_grad(a.ds, a.dss, 1, up);
+            if (element) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const float2 e = gate_e(zv.pair(p, now.scales[2][i]));
+                    g[i][p] = gate_of(e);
+                    rest_g[i][p] = f2_mul(e, g[i][p]);
+                }
+            } else {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) g[i][p] = f2(row_g), rest_g[i][p] = f2(row_e * row_g);
+            }
+            float2 w[4];
+            load_vector<VEC>(a.wpost + column(i), rest(i), w);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                rh[i][p] = f2_mul(rv.pair(p, now.scales[1][i]), f2(now.rstd_r));
+                w[p] = f2_mul(g[i][p], f2_mul(rh[i][p], w[p]));                      // p
+            }
+            float2 al[4];
+            if (a.alpha) {
+                load_vector<VEC>(a.alpha + column(i), rest(i), al);
+            } else {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) al[p] = f2(1.f);
+            }
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                sh[i][p] = f2_mul(f2_fma(al[p], xv[i].pair(p, now.scales[0][i]), w[p]), f2(now.rstd_s));
+                s2 = f2_fma(sh[i][p], w[p], s2);
+            }
+            load_vector<VEC>(a.wpre + column(i), rest(i), al);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const float2 d = dy.pair(p), t = f2_mul(d, al[p]);
+                acc[0][i][p] = f2_fma(d, sh[i][p], acc[0][i][p]);
+                s0 = f2_fma(t, sh[i][p], s0);
+                ds[i][p] = f2_fma(f2(now.rstd_s), t, a.ds ? up.pair(p) : f2(0.f));
+                s1 = f2_fma(ds[i][p], w[p], s1);
+            }
+        }
+        float sums[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+        row_sums<TPR>(sums, smem[turn ^= 1]);
+        const float c1 = now.rstd_s * (sums[0] * a.inv_cols);
+        const float dot = fmaf(-c1, sums[2], sums[1]);           // sum of ds p
+        const float c2 = dot * a.inv_cols;
+        if (a.gate == kRowGate && a.dz && in && t == 0)
+            static_cast<T*>(a.dz)[row * a.dzs] = from_f<T>(dot * (row_e * row_g));
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            const int left = in ? rest(i) : 0;
+            float2 w[4], o[4], dn[4];
+            if (a.alpha) load_vector<VEC>(a.alpha + column(i), rest(i), w);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                ds[i][p] = f2_fma(f2(-c1), sh[i][p], ds[i][p]);
+                acc[2][i][p] = f2_fma(ds[i][p], xv[i].pair(p, now.scales[0][i]), acc[2][i][p]);
+                dn[p] = f2_mul(ds[i][p], g[i][p]);
+                acc[1][i][p] = f2_fma(dn[p], rh[i][p], acc[1][i][p]);
+                o[p] = a.alpha ? f2_mul(ds[i][p], w[p]) : ds[i][p];
+            }
+            if (left > 0) store_pairs<T, VEC>(static_cast<T*>(a.dx) + row * a.dxs + column(i), left, o);
+            load_vector<VEC>(a.wpost + column(i), rest(i), w);
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                dn[p] = f2_mul(dn[p], w[p]);
+                o[p] = f2_mul(f2(now.rstd_r), f2_fma(f2(-c2), rh[i][p], dn[p]));
+                dn[p] = f2_mul(f2_mul(dn[p], rh[i][p]), rest_g[i][p]);
+            }
+            if (left > 0) {
+                store_pairs<T, VEC>(static_cast<T*>(a.dr) + row * a.drs + column(i), left, o);
+                if (element && a.dz) store_pairs<T, VEC>(static_cast<T*>(a.dz) + row * a.dzs + column(i), left, dn);
+            }
+        }
+        now = next;
+        if (++stage == kStages) stage = 0;
+    }
+    if (!a.part) return;
+    float* part = a.part + size_t(blockIdx.x) * 3 * a.cols;
+    float2* comb = reinterpret_cast<float2*>(ring);              // no copy is on its way to it: no row is left
+    if constexpr (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int i = 0; i < RUNS; ++i) {
+            if constexpr (kRows > 1) {
+                __syncthreads();
+#pragma unroll
+                for (int p = 0; p < 4; ++p) comb[p * kThreads + threadIdx.x] = acc[k][i][p];
+                __syncthreads();
+                if (sub == 0)
+#pragma unroll
+                    for (int p = 0; p < 4; ++p)
+                        for (int o = 1; o < kRows; ++o) {
+                            const float2 v = comb[p * kThreads + o * TPR + t];
+                            acc[k][i][p] = make_float2(acc[k][i][p].x + v.x, acc[k][i][p].y + v.y);
+                        }
+            }
+            if (sub == 0)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    const int c = column(i) + 2 * p;
+                    if (c < a.cols) part[size_t(k) * a.cols + c] = acc[k][i][p].x;
+                    if (c + 1 < a.cols) part[size_t(k) * a.cols + c + 1] = acc[k][i][p].y;
+                }
+        }
+}
+
+struct Vectors { float* out[3]; };
+
+// The vectors' gradients from the blocks' sums [n][3][cols] in a fixed order: 32 columns a block, 32 threads a column.
+__global__ void __launch_bounds__(1024) k_sandwich_sums(const float* __restrict__ part, int n, int cols, Vectors v) {
+    RS_PDL_ENTER();
+    float* out = v.out[blockIdx.y];
+    if (!out) return;
+    __shared__ float sm[32][33];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
+    float s = 0.f;
+    if (c < cols)
+#pragma unroll 8
+        for (int i = g; i < n; i += 32) s += part[(size_t(i) * 3 + blockIdx.y) * cols + c];
+    sm[g][threadIdx.x & 31] = s;
+    __syncthreads();
+    s = group_sum<32>(sm[threadIdx.x & 31][g]);
+    const int oc = blockIdx.x * 32 + g;
+    if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = s;
+}
+
+// Threads a row; two runs each from 129 to 4096 columns, beyond that the wide form on 512 threads.
+int bwd_threads(int cols) {
+    if (cols > 4096) return 512;
+    const int runs = ceil_div(cols, 8);
+    for (int t = 16; t < 256; t *= 2)
+        if (runs <= 2 * t) return t;
+    return 256;
+}
+// The most blocks of a call; what it launches depends on types too.
+int bwd_blocks(int rows, int cols) {
+    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1;
+    return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * (t <= 128 ? 3 : 1)));
+}
+
+template <typename K>
+cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const SandwichBwdArgs& a, cudaStream_t s) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    return pdl_launch(kernel, grid, threads, smem, s, a);
+}
+
+template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
+cudaError_t bwd(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
+    using R = Ring<T, KEPT, TPR, RUNS>;
+    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, smem = MOVE == kAny ? comb : std::max(comb, R::kBytes);
+    grid = unsigned(std::min(bwd_blocks(a.rows, a.cols), kSms * R::kBlocks));
+    return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, smem, a, s);
+}
+template <typename T, bool KEPT, bool VEC, int RUNS>
+cudaError_t bwd_wide(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
+    grid = unsigned(bwd_blocks(a.rows, a.cols));
+    return bwd_launch(k_sandwich_bwd_wide<T, KEPT, VEC, 512, RUNS>, grid, 512, 3 * RUNS * 8 * 512 * 4, a, s);
+}
+
+template <typename T, bool KEPT, Move MOVE>
+cudaError_t bwd_width(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
+    if (a.cols > 8192) return bwd_wide<T, KEPT, MOVE != kAny, 4>(a, grid, s);
+    if (a.cols > 4096) return bwd_wide<T, KEPT, MOVE != kAny, 2>(a, grid, s);
+    switch (bwd_threads(a.cols)) {
+        case 16:
+            return a.cols <= 128 ? bwd<T, KEPT, MOVE, 16, 1>(a, grid, s) : bwd<T, KEPT, MOVE, 16, 2>(a, grid, s);
+        case 32: return bwd<T, KEPT, MOVE, 32, 2>(a, grid, s);
+        case 64: return bwd<T, KEPT, MOVE, 64, 2>(a, grid, s);
+        case 128: return bwd<T, KEPT, MOVE, 128, 2>(a, grid, s);
+    }
+    return bwd<T, KEPT, MOVE, 256, 2>(a, grid, s);
+}
+
+}  // namespace
+}  // namespace rs
+
+extern "C" {
+
+size_t rs_sandwich_norm_bwd_workspace_size(int32_t rows, int32_t cols) {
+    if (rows < 0 || cols < 1 || cols > RS_NORM_MAX_COLS) return 0;
+    return size_t(rs::bwd_blocks(rows, cols)) * 3 * cols * sizeof(float);
+}
+
+int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grads, void* d_workspace,
+                         size_t workspace_bytes, void* stream) {
+    using namespace rs;
+    if (!block || !grads) return RS_ERR_INVALID_ARG;
+    bool kept, vec;
+    if (!operands_ok(block, kept, vec)) return RS_ERR_INVALID_ARG;
+    const int32_t rows = block->rows, cols = block->cols, dtype = block->dtype;
+    const size_t z = dtype_size(dtype);
+    float* const vectors[3] = {grads->d_dL_dpre_weight, grads->d_dL_dpost_weight, grads->d_dL_dresidual_scale};
+    bool any = false;
+    for (float* v : vectors) {
+        if (v && !ptr_ok(v, 4)) return RS_ERR_INVALID_ARG;
+        any = any || v;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {
+        for (float* v : vectors)
+            if (v && cudaMemsetAsync(v, 0, size_t(cols) * 4, s) != cudaSuccess) return RS_ERR_CUDA;
+        return RS_OK;
+    }
+    if (!ptr_ok(grads->d_rstd_r, 4) || !ptr_ok(grads->d_rstd_s, 4)) return RS_ERR_INVALID_ARG;
+    struct Out { void* p; size_t stride; };
+    const Out in[2] = {{const_cast<void*>(grads->d_dL_dy), grads->dy_stride},
+                       {const_cast<void*>(grads->d_dL_dsum), grads->dsum_stride}};
+    const Out out[3] = {{grads->d_dL_dx, grads->dx_stride}, {grads->d_dL_dr, grads->dr_stride},
+                        {grads->d_dL_dgate, grads->dgate_stride}};
+    if (!matrix_ok(in[0].p, in[0].stride, cols, dtype) || (in[1].p && !matrix_ok(in[1].p, in[1].stride, cols, dtype)))
+        return RS_ERR_INVALID_ARG;
+    if (out[2].p && !block->gate_cols) return RS_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        if (i == 2 && !out[2].p) break;
+        const int32_t width = i == 2 ? block->gate_cols : cols;
+        if (!matrix_ok(out[i].p, out[i].stride, width, dtype)) return RS_ERR_INVALID_ARG;
+        for (const Out& o : in)
+            if (o.p == out[i].p && (o.stride != out[i].stride || width != cols)) return RS_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (out[j].p == out[i].p) return RS_ERR_INVALID_ARG;
+        if (width == cols) vec = vec && rows16(out[i].p, out[i].stride, z);
+    }
+    for (const Out& o : in)
+        if (o.p) vec = vec && rows16(o.p, o.stride, z);
+    if (any) {
+        if (!ptr_ok(d_workspace, 16)) return RS_ERR_INVALID_ARG;
+        if (workspace_bytes < rs_sandwich_norm_bwd_workspace_size(rows, cols)) return RS_ERR_WORKSPACE;
+    }
+    const SandwichBwdArgs a{args_of(block), grads->d_rstd_r, grads->d_rstd_s, in[0].p, in[0].stride, in[1].p,
+                            in[1].stride, out[0].p, out[0].stride, out[1].p, out[1].stride, out[2].p, out[2].stride,
+                            any ? static_cast<float*>(d_workspace) : nullptr};
+    unsigned grid = 0;
+    const bool full = full_width(cols) && cols <= 4096;
+    cudaError_t e = with_dtype(dtype, [&](auto v) {
+        using T = decltype(v);
+        const auto moved = [&](auto any, auto ragged, auto whole) { return (!vec ? any : full ? whole : ragged)(a, grid, s); };
+        if (kept) return moved(bwd_width<T, true, kAny>, bwd_width<T, true, kVec>, bwd_width<T, true, kFull>);
+        return moved(bwd_width<T, false, kAny>, bwd_width<T, false, kVec>, bwd_width<T, false, kFull>);
+    });
+    if (e == cudaSuccess && any)
+        e = pdl_launch(k_sandwich_sums, dim3(ceil_div(cols, 32), 3), 1024, 0, s, static_cast<const float*>(a.part),
+                       int(grid), cols, Vectors{{vectors[0], vectors[1], vectors[2]}});
+    return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
+}
+
+}  // extern "C"
