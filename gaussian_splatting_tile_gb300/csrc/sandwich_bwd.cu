@@ -236,6 +236,8 @@ struct RowNumbers {
     float rstd_r, rstd_s, z, scales[3][RUNS];
 };
 
+enum Vector { kPost, kPre, kAlpha };
+
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its shares of the
 // vectors' gradients stay in its registers and leave once per block, to be added up in a fixed order.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
@@ -249,6 +251,26 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
     extern __shared__ __align__(16) uint8_t ring[];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const bool element = a.gate == kElementGate;
+    // The vectors, where their loads do not wait: halves of runs apart, so that neighbours hit different banks.
+    float4* vectors = reinterpret_cast<float4*>(ring + (VEC ? R::kBytes : 0));
+    const auto vector = [&](int k, int i, float2 (&w)[4]) {
+        const float4 lo = vectors[(k * 2 * RUNS + i) * TPR + t], hi = vectors[(k * 2 * RUNS + RUNS + i) * TPR + t];
+        w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w);
+        w[2] = make_float2(hi.x, hi.y), w[3] = make_float2(hi.z, hi.w);
+    };
+    if (sub == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                const float* v = k == kPost ? a.wpost : k == kPre ? a.wpre : a.alpha;
+                float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+                if (v) load8<float, VEC>(v + (i * TPR + t) * 8, a.cols - (i * TPR + t) * 8, w);
+                vectors[(k * 2 * RUNS + i) * TPR + t] = make_float4(w[0], w[1], w[2], w[3]);
+                vectors[(k * 2 * RUNS + RUNS + i) * TPR + t] = make_float4(w[4], w[5], w[6], w[7]);
+            }
+    }
+    __syncthreads();
     float2 acc[3][RUNS][4];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -369,25 +391,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
                 for (int p = 0; p < 4; ++p) g[i][p] = f2(row_g), rest_g[i][p] = f2(row_e * row_g);
             }
             float2 w[4];
-            load_vector<VEC>(a.wpost + column(i), rest(i), w);
+            vector(kPost, i, w);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 rh[i][p] = f2_mul(rv.pair(p, now.scales[1][i]), f2(now.rstd_r));
                 w[p] = f2_mul(g[i][p], f2_mul(rh[i][p], w[p]));                      // p
             }
             float2 al[4];
-            if (a.alpha) {
-                load_vector<VEC>(a.alpha + column(i), rest(i), al);
-            } else {
-#pragma unroll
-                for (int p = 0; p < 4; ++p) al[p] = f2(1.f);
-            }
+            vector(kAlpha, i, al);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 sh[i][p] = f2_mul(f2_fma(al[p], xv[i].pair(p, now.scales[0][i]), w[p]), f2(now.rstd_s));
                 s2 = f2_fma(sh[i][p], w[p], s2);
             }
-            load_vector<VEC>(a.wpre + column(i), rest(i), al);
+            vector(kPre, i, al);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 const float2 d = dy.pair(p), t = f2_mul(d, al[p]);
@@ -408,17 +425,17 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
         for (int i = 0; i < RUNS; ++i) {
             const int left = in ? rest(i) : 0;
             float2 w[4], o[4], dn[4];
-            if (a.alpha) load_vector<VEC>(a.alpha + column(i), rest(i), w);
+            vector(kAlpha, i, w);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 ds[i][p] = f2_fma(f2(-c1), sh[i][p], ds[i][p]);
                 acc[2][i][p] = f2_fma(ds[i][p], xv[i].pair(p, now.scales[0][i]), acc[2][i][p]);
                 dn[p] = f2_mul(ds[i][p], g[i][p]);
                 acc[1][i][p] = f2_fma(dn[p], rh[i][p], acc[1][i][p]);
-                o[p] = a.alpha ? f2_mul(ds[i][p], w[p]) : ds[i][p];
+                o[p] = f2_mul(ds[i][p], w[p]);
             }
             if (left > 0) store_pairs<T, VEC>(static_cast<T*>(a.dx) + row * a.dxs + column(i), left, o);
-            load_vector<VEC>(a.wpost + column(i), rest(i), w);
+            vector(kPost, i, w);
 #pragma unroll
             for (int p = 0; p < 4; ++p) {
                 dn[p] = f2_mul(dn[p], w[p]);
@@ -500,7 +517,7 @@ int bwd_blocks(int rows, int cols) {
 
 template <typename K>
 cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const SandwichBwdArgs& a, cudaStream_t s) {
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {  // with what is static, more than needs no leave
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
     }
@@ -510,7 +527,8 @@ cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const San
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 cudaError_t bwd(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
     using R = Ring<T, KEPT, TPR, RUNS>;
-    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, smem = MOVE == kAny ? comb : std::max(comb, R::kBytes);
+    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, kVectors = 3 * RUNS * TPR * 32;
+    constexpr int smem = std::max(comb, (MOVE == kAny ? 0 : R::kBytes) + kVectors);
     grid = unsigned(std::min(bwd_blocks(a.rows, a.cols), kSms * R::kBlocks));
     return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, smem, a, s);
 }
