@@ -28,8 +28,8 @@ struct QuantArgs {
 __device__ __forceinline__ int tile_unit(int c, int u) { return c * 16 + (u ^ ((c >> 3) & 15)); }
 
 // The 8 x 8 values of one thread, scaled by column (inv[j]), to the transposed bytes.
-template <typename V>
-__device__ __forceinline__ void store_transposed(const QuantArgs& a, const V (&v)[8], const float (&inv)[8],
+template <typename T>
+__device__ __forceinline__ void store_transposed(const QuantArgs& a, const Run8<T> (&v)[8], const float (&inv)[8],
                                                  uint2* tile, int tx, int ty, int c0, long long r0) {
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
@@ -181,57 +181,82 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu |
     }
 }
 
-// The transposed form of a checkpoint: the same tile, the same thread for the same 8 x 8 values, which are a byte times
-// their row's scale.  Bound by memory: one byte in, one out.
-struct ScaledBytes8 {
-    Bytes8 v;
-    float scale;
-    __device__ __forceinline__ float2 pair(int p) const {
-        const float2 f = v.pair(p);
-        return make_float2(f.x * scale, f.y * scale);
-    }
-};
+// The transposed form of a checkpoint: 128 rows x 64 columns a block, a thread 8 x 8 values, which are a byte times
+// their row's scale.  They stay bytes and are widened twice, for the columns' maxima and for their new bytes: that leaves
+// registers for ten blocks an SM, which load, compute and store in turn.  Bound by memory: one byte in, one out.
+constexpr int kHalf = kBlock / 2;
 
-__global__ void __launch_bounds__(256) k_transpose(QuantArgs a) {
+__global__ void __launch_bounds__(128, 10) k_transpose(QuantArgs a) {
     RS_PDL_ENTER();
-    __shared__ float cmax[16][kBlock];
-    __shared__ __align__(16) uint2 tile[kBlock * 16];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    __shared__ __align__(8) float cmax[4][kHalf];
+    __shared__ __align__(16) uint2 tile[kHalf * 16];  // eight bytes of column c, rows 8 u on: at 16 c + (u ^ 2 (c / 8))
+    const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
     const int ct = blockIdx.x % a.ctiles, rt = blockIdx.x / a.ctiles;
-    const int c0 = ct * kBlock, c = c0 + tx * 8;
+    const int c0 = ct * kHalf, c = c0 + tx * 8;
     const long long r0 = (long long)rt * kBlock, r = r0 + ty * 8;
     const int left = a.cols - c;
-    ScaledBytes8 v[8];
+    Bytes8 v[8];
+    float scale[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool in = r + i < a.rows;
-        v[i].v.load(static_cast<const uint8_t*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
-        v[i].scale = in ? a.scales[size_t(ct) * a.rows + r + i] : 0.f;
+        v[i].load(static_cast<const uint8_t*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0);
+        scale[i] = in ? a.scales[size_t(ct >> 1) * a.rows + r + i] : 0.f;
     }
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-        float2 m = make_float2(0.f, 0.f);
+        float2 m = f2(0.f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 f = v[i].pair(p);
+            const float2 f = f2_mul(v[i].pair(p), f2(scale[i]));
             m = make_float2(fmaxf(m.x, fabsf(f.x)), fmaxf(m.y, fabsf(f.y)));
         }
-        *reinterpret_cast<float2*>(&cmax[ty][tx * 8 + 2 * p]) = m;
+#pragma unroll
+        for (int o = 8; o < 32; o *= 2) {
+            m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+            m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+        }
+        if (!(ty & 3)) *reinterpret_cast<float2*>(&cmax[ty >> 2][tx * 8 + 2 * p]) = m;
     }
     __syncthreads();
-    if (threadIdx.x < kBlock) {
-        float m = 0.f, scale, inv;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) m = fmaxf(m, cmax[i][threadIdx.x]);
-        block_scale(m, scale, inv);
-        if (c0 + int(threadIdx.x) < a.cols) a.scales_t[size_t(rt) * a.cols + c0 + threadIdx.x] = scale;
-        cmax[0][threadIdx.x] = inv;
+    if (threadIdx.x < kHalf) {
+        float out, inv;
+        const float m = fmaxf(fmaxf(cmax[0][threadIdx.x], cmax[1][threadIdx.x]),
+                              fmaxf(cmax[2][threadIdx.x], cmax[3][threadIdx.x]));
+        block_scale(m, out, inv);
+        if (c0 + int(threadIdx.x) < a.cols) a.scales_t[size_t(rt) * a.cols + c0 + threadIdx.x] = out;
+        cmax[0][threadIdx.x] = inv;  // this column of row 0 is read by this thread alone
     }
     __syncthreads();
-    float invs[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) invs[j] = cmax[0][tx * 8 + j];
-    store_transposed(a, v, invs, tile, tx, ty, c0, r0);
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(v[i].w.x), "+r"(v[i].w.y));  // widened anew, not kept wide
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const float2 inv = *reinterpret_cast<const float2*>(&cmax[0][tx * 8 + 2 * p]);
+        float2 f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f2_mul(f2_mul(v[i].pair(p), f2(scale[i])), inv);
+        uint2* at = tile + (tx * 8 + 2 * p) * 16 + (ty ^ 2 * tx);
+        at[0] = make_uint2(e4m3x4(f[0].x, f[1].x, f[2].x, f[3].x), e4m3x4(f[4].x, f[5].x, f[6].x, f[7].x));
+        at[16] = make_uint2(e4m3x4(f[0].y, f[1].y, f[2].y, f[3].y), e4m3x4(f[4].y, f[5].y, f[6].y, f[7].y));
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        const int tc = p * 16 + ty, k = tx, tr = k * 16;
+        if (c0 + tc >= a.cols || r0 + tr >= a.rows) continue;
+        uint8_t* o = a.qt + size_t(c0 + tc) * a.qts + r0 + tr;
+        const uint4 w = *reinterpret_cast<const uint4*>(tile + tc * 16 + (2 * k ^ 2 * (tc >> 3)));
+        const long long rest = a.rows - (r0 + tr);
+        if (rest >= 16) {
+            *reinterpret_cast<uint4*>(o) = w;
+        } else {
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < rest) o[i] = uint8_t(ws[i >> 2] >> (8 * (i & 3)));
+        }
+    }
 }
 
 int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s, bool relu8 = false) {
@@ -306,11 +331,11 @@ int rs_transpose_fp8(int32_t rows, int32_t cols, const uint8_t* d_q, size_t q_st
     if (!fp8_rows_ok(d_q, q_stride, cols) || !ptr_ok(d_scales, 4) || !fp8_rows_ok(d_qt, qt_stride, rows) ||
         !ptr_ok(d_scales_t, 4))
         return RS_ERR_INVALID_ARG;
-    const int ctiles = ceil_div(cols, kBlock), rtiles = ceil_div(rows, kBlock);
+    const int ctiles = ceil_div(cols, kHalf), rtiles = ceil_div(rows, kBlock);
     if ((long long)ctiles * rtiles > 0x7fffffffLL) return RS_ERR_INVALID_ARG;
     const QuantArgs a{rows, cols, d_q, q_stride, nullptr, 0, nullptr, 0, const_cast<float*>(d_scales), d_qt, qt_stride,
                       d_scales_t, ctiles, rtiles};
-    const cudaError_t e = pdl_launch(k_transpose, unsigned(ctiles) * rtiles, 256, 0, static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = pdl_launch(k_transpose, unsigned(ctiles) * rtiles, 128, 0, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 
