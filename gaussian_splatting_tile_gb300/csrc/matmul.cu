@@ -608,14 +608,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 if constexpr (sizeof(T) == 1) {
                     static_assert(kCols == kBlock, "a thread's columns are one block");
                     float top = 0.f, scale;
+                    if (g.relu) {  // which the conversion does, too
 #pragma unroll
-                    for (int j = 0; j < kCols / 2; ++j) {
-                        float2 x = unpack2(acc[j]);
-                        if (g.relu) {
-                            x = make_float2(relu(x.x), relu(x.y));
-                            acc[j] = pack2(x.x, x.y);
-                        }
-                        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+                        for (int j = 0; j < kCols / 2; ++j) top = max3(top, unpack2(acc[j]).x, unpack2(acc[j]).y);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < kCols / 2; ++j)
+                            top = max3(top, fabsf(unpack2(acc[j]).x), fabsf(unpack2(acc[j]).y));
                     }
                     block_scale(top, scale, inv);
                     if (row0 + lane < g.m) g.so[size_t(col / kBlock) * g.m + row0 + lane] = scale;
@@ -630,11 +629,18 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                         uint4 w[8];
                         uint32_t* ww = reinterpret_cast<uint32_t*>(w);
                         if constexpr (sizeof(T) == 1) {
+                            const uint64_t by = pack2(inv, inv);
 #pragma unroll
-                            for (int j = 0; j < kOnce; j += 4) {
-                                const float2 x = unpack2(acc[j / 2]), y = unpack2(acc[j / 2 + 1]);
-                                ww[j / 4] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
-                            }
+                            for (int j = 0; j < kOnce / 2; ++j) acc[j] = mul2(acc[j], by);
+                            const auto words = [&](auto convert) {
+#pragma unroll
+                                for (int j = 0; j < kOnce; j += 4) {
+                                    const float2 x = unpack2(acc[j / 2]), y = unpack2(acc[j / 2 + 1]);
+                                    ww[j / 4] = convert(x.x, x.y, y.x, y.y);
+                                }
+                            };
+                            if (g.relu) words([](float a, float b, float c, float d) { return e4m3x4<true>(a, b, c, d); });
+                            else words([](float a, float b, float c, float d) { return e4m3x4(a, b, c, d); });
                         } else
 #pragma unroll
                         for (int j = 0; j < kOnce; j += 2) {

@@ -36,6 +36,12 @@ __device__ __forceinline__ float2 f2_mul(float2 a, float2 b) {
         : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
+// The largest of three in one instruction, NaN left out as fmaxf leaves it.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 __device__ __forceinline__ float2 f2(float a) { return make_float2(a, a); }
 
 // Two e4m3 bytes (the lower first) as floats: exact.
@@ -151,9 +157,16 @@ struct PackedRun8 {
 template <> struct Run8<__half> : PackedRun8<__half, __half2> {};
 template <> struct Run8<__nv_bfloat16> : PackedRun8<__nv_bfloat16, __nv_bfloat162> {};
 
-// Four floats as e4m3 bytes, lowest first (round to nearest even; finite values past 448 become 448, NaN stays).
+// Four floats as e4m3 bytes, lowest first (round to nearest even; finite values past 448 become 448, NaN stays; RELU:
+// negative values become zero).
+template <bool RELU = false>
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
     uint16_t lo, hi;
+    if constexpr (RELU) {
+        asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.relu.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+        return uint32_t(lo) | (uint32_t(hi) << 16);
+    }
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
     return uint32_t(lo) | (uint32_t(hi) << 16);
