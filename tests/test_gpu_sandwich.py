@@ -433,3 +433,26 @@ def test_streams_and_graphs():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[1][3], 2 * want[9]) and torch.equal(outs[0][0], (2 * want[0].float()).to(torch.bfloat16))
+
+
+def test_parameters_and_missing_operands():
+    """Tensors of a subclass are tensors; an operand that is missing is refused by the library, not by accident."""
+    g = gen(41)
+    b = Block(g, 5, 64, "f32")
+    o = b.forward()
+    want = rs.fp8_empty(5, 64)
+    rs.rs_sandwich_norm_fwd(b.x, b.r, b.wpost, b.wpre, *want, gate=b.gate, residual_scale=b.alpha)
+    P = lambda t: torch.nn.Parameter(t, requires_grad=False)
+    got = rs.fp8_empty(5, 64)
+    rs.rs_sandwich_norm_fwd(P(b.x), P(b.r), P(b.wpost), P(b.wpre), *got, gate=P(b.gate), residual_scale=P(b.alpha))
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+    for x, r, w in ((b.x, None, b.wpost), (b.x, b.r, None)):
+        with pytest.raises(rs.RsError):
+            rs.rs_sandwich_norm_fwd(x, r, w, b.wpre, *got)
+    dy = torch.ones_like(b.x)
+    with pytest.raises(rs.RsError):
+        rs.rs_sandwich_norm_bwd(b.x, b.r, b.wpost, b.wpre, o["rstd_r"], None, dy, dy.clone(), dy.clone(), None)
+    with pytest.raises(TypeError):    # float32 is no 8-bit matrix
+        rs.rs_sandwich_norm_bwd((b.x, None), b.r, b.wpost, b.wpre, o["rstd_r"], o["rstd_s"], dy, dy.clone(), dy.clone(), None)
+    with pytest.raises(ValueError):   # nor is one complete without its scales
+        rs.rs_sandwich_norm_bwd((got[0], None), b.r, b.wpost, b.wpre, o["rstd_r"], o["rstd_s"], dy, dy.clone(), dy.clone(), None)
