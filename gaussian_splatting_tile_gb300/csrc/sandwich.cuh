@@ -102,9 +102,9 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* smem) {
     }
 }
 
-// How a row is moved: value by value or word by word, in 16-byte accesses with a ragged end, or all of it in such
-// accesses (the width is 8 TPR RUNS).
-enum Move { kAny, kVec, kFull };
+// How a row is moved: value by value or word by word; in 16-byte accesses (rows on such boundaries, whole runs of eight:
+// a thread has a run or has none); or in such accesses by threads that all have theirs (the width is 8 TPR RUNS).
+enum Move { kAny, kRuns, kFull };
 
 template <bool VEC>
 __device__ __forceinline__ void load_vector(const float* p, int left, float2 (&v)[4]) {
@@ -133,7 +133,7 @@ bool form_ok(const rs_fp8_matrix& f, int32_t cols) {
     return fp8_rows_ok(f.d_q, f.stride, cols) && ptr_ok(f.d_scales, 4);
 }
 
-// The block's operands; `kept`: whether they are checkpoints.
+// The block's operands; `kept`: whether they are checkpoints, `vec`: whether runs can move in 16-byte accesses.
 bool operands_ok(const rs_sandwich* b, bool& kept, bool& vec) {
     if (b->rows < 0 || b->cols < 1 || b->cols > RS_NORM_MAX_COLS || !dtype_ok(b->dtype)) return false;
     if (b->gate_cols != 0 && b->gate_cols != 1 && b->gate_cols != b->cols) return false;
@@ -159,7 +159,7 @@ bool operands_ok(const rs_sandwich* b, bool& kept, bool& vec) {
             return false;
         }
     }
-    vec = ptr_ok(b->d_post_weight, 16) && ptr_ok(b->d_pre_weight, 16) &&
+    vec = b->cols % 8 == 0 && ptr_ok(b->d_post_weight, 16) && ptr_ok(b->d_pre_weight, 16) &&
           (!b->d_residual_scale || ptr_ok(b->d_residual_scale, 16));
     if (!kept)
         vec = vec && rows16(b->d_x, b->x_stride, z) && rows16(b->d_r, b->r_stride, z) &&

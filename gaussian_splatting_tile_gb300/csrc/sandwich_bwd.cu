@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant
 // The copies of a row's operands on their way: every thread copies its own runs into a place of its own and reads them
 // back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
                  : "memory");
 }
 __device__ __forceinline__ void copy8(void* dst, const void* src) {
@@ -194,20 +194,11 @@ struct Ring {
     }
 };
 
-// One run of a matrix of T on its way into the ring.
+// One run of a matrix of T on its way into the ring, and out of it.
 template <typename R, typename T>
-__device__ __forceinline__ void send(uint8_t* ring, int stage, int u, const T* p, int left) {
-    if (left >= 8) {
+__device__ __forceinline__ void send(uint8_t* ring, int stage, int u, const T* p) {
 #pragma unroll
-        for (int i = 0; i < R::kUnit; ++i) copy16(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
-    } else if (left > 0) {
-        Run8<T> v;
-        v.template load<true>(p, left);
-        float4 w[R::kUnit];
-        memcpy(w, &v, sizeof(w));
-#pragma unroll
-        for (int i = 0; i < R::kUnit; ++i) *reinterpret_cast<float4*>(R::wide(ring, stage, u + i)) = w[i];
-    }
+    for (int i = 0; i < R::kUnit; ++i) copy16(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
 }
 template <typename R, typename T>
 __device__ __forceinline__ void receive(uint8_t* ring, int stage, int u, bool live, Run8<T>& v) {
@@ -279,7 +270,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
 #pragma unroll
             for (int p = 0; p < 4; ++p) acc[k][i][p] = f2(0.f);
     const auto column = [&](int i) { return (i * TPR + t) * 8; };
-    const auto rest = [&](int i) { return FULL ? 8 : a.cols - column(i); };
+    // of a run: how many of its values exist
+    const auto rest = [&](int i) {
+        return FULL ? 8 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
+    };
     const auto numbers = [&](long long row) {
         RowNumbers<RUNS> n{};
         if (row >= a.rows) return n;
@@ -299,31 +293,23 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
         return n;
     };
     const auto operand = [&](const Stored& s, long long row, int stage, int k, int i) {
-        if constexpr (KEPT) {
-            const uint8_t* p = static_cast<const uint8_t*>(s.p) + row * s.stride + column(i);
-            uint8_t* to = R::narrow(ring, stage, k * RUNS + i);
-            if (rest(i) >= 8) {
-                copy8(to, p);
-            } else if (rest(i) > 0) {
-                Bytes8 b;
-                b.load(p, rest(i));
-                *reinterpret_cast<uint2*>(to) = b.w;
-            }
-        } else {
-            send<R>(ring, stage, ((2 + k) * RUNS + i) * kU, static_cast<const T*>(s.p) + row * s.stride + column(i), rest(i));
-        }
+        if constexpr (KEPT)
+            copy8(R::narrow(ring, stage, k * RUNS + i), static_cast<const uint8_t*>(s.p) + row * s.stride + column(i));
+        else
+            send<R>(ring, stage, ((2 + k) * RUNS + i) * kU, static_cast<const T*>(s.p) + row * s.stride + column(i));
     };
     const auto fetch = [&](long long row, int stage) {
-        if (row < a.rows)
+        if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < RUNS; ++i) {
+                if (rest(i) <= 0) continue;
                 operand(a.x, row, stage, 0, i);
                 operand(a.r, row, stage, 1, i);
                 if (element) operand(a.z, row, stage, 2, i);
-                send<R>(ring, stage, i * kU, static_cast<const T*>(a.dy) + row * a.dys + column(i), rest(i));
-                if (a.ds)
-                    send<R>(ring, stage, (RUNS + i) * kU, static_cast<const T*>(a.ds) + row * a.dss + column(i), rest(i));
+                send<R>(ring, stage, i * kU, static_cast<const T*>(a.dy) + row * a.dys + column(i));
+                if (a.ds) send<R>(ring, stage, (RUNS + i) * kU, static_cast<const T*>(a.ds) + row * a.dss + column(i));
             }
+        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const long long step = (long long)gridDim.x * kRows;
@@ -527,8 +513,8 @@ cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const San
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 cudaError_t bwd(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
     using R = Ring<T, KEPT, TPR, RUNS>;
-    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, kVectors = 3 * RUNS * TPR * 32;
-    constexpr int smem = std::max(comb, (MOVE == kAny ? 0 : R::kBytes) + kVectors);
+    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, kRunstors = 3 * RUNS * TPR * 32;
+    constexpr int smem = std::max(comb, (MOVE == kAny ? 0 : R::kBytes) + kRunstors);
     grid = unsigned(std::min(bwd_blocks(a.rows, a.cols), kSms * R::kBlocks));
     return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, smem, a, s);
 }
@@ -611,12 +597,13 @@ int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grad
                             in[1].stride, out[0].p, out[0].stride, out[1].p, out[1].stride, out[2].p, out[2].stride,
                             any ? static_cast<float*>(d_workspace) : nullptr};
     unsigned grid = 0;
-    const bool full = full_width(cols) && cols <= 4096;
     cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
-        const auto moved = [&](auto any, auto ragged, auto whole) { return (!vec ? any : full ? whole : ragged)(a, grid, s); };
-        if (kept) return moved(bwd_width<T, true, kAny>, bwd_width<T, true, kVec>, bwd_width<T, true, kFull>);
-        return moved(bwd_width<T, false, kAny>, bwd_width<T, false, kVec>, bwd_width<T, false, kFull>);
+        if (kept) {
+            if (!vec) return bwd_width<T, true, kAny>(a, grid, s);
+            return full_width(cols) ? bwd_width<T, true, kFull>(a, grid, s) : bwd_width<T, true, kRuns>(a, grid, s);
+        }
+        return vec ? bwd_width<T, false, kRuns>(a, grid, s) : bwd_width<T, false, kAny>(a, grid, s);
     });
     if (e == cudaSuccess && any)
         e = pdl_launch(k_sandwich_sums, dim3(ceil_div(cols, 32), 3), 1024, 0, s, static_cast<const float*>(a.part),

@@ -50,7 +50,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
     const T* r = static_cast<const T*>(a.r.p) + at * a.r.stride;
     const T* z = a.gate ? static_cast<const T*>(a.z.p) + at * a.z.stride : nullptr;
     const auto column = [&](int i) { return (i * TPR + t) * 8; };
-    const auto rest = [&](int i) { return FULL ? 8 : in ? a.cols - column(i) : 0; };
+    // of a run: how many of its values exist
+    const auto rest = [&](int i) {
+        return FULL ? 8 : !in ? 0 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
+    };
     Run8<T> xv[RUNS], rv[RUNS], zv[RUNS];
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) rv[i].template load<VEC>(r + column(i), rest(i), column(i) > 0);
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
                 if (of == first && in && (FULL || c - of * 8 < a.cols))
                     f.scales[size_t(c / kBlock) * a.rows + row] = scale;
                 const float2 w[4] = {v[i].pair(0), v[i].pair(1), v[i].pair(2), v[i].pair(3)};
-                if (in && (FULL || a.cols - c > 0)) store_e4m3(f.q + row * f.stride + c, FULL ? 8 : a.cols - c, w, by);
+                if (in && rest(i) > 0) store_e4m3(f.q + row * f.stride + c, rest(i), w, by);
             }
         };
         keep(a.kx, xv, 0);
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
     if (a.sum && in) {
 #pragma unroll
         for (int i = 0; i < RUNS; ++i)
-            store_pairs<T, VEC>(static_cast<T*>(a.sum) + row * a.sums + column(i), FULL ? 8 : a.cols - column(i), v[i]);
+            store_pairs<T, VEC>(static_cast<T*>(a.sum) + row * a.sums + column(i), rest(i), v[i]);
     }
     float top[kForms];
 #pragma unroll
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
         const int c = column(i);
         const float by = __shfl_sync(0xffffffffu, inv, i * kEach, 16);
         if (of == i * kEach && in && (FULL || c - of * 8 < a.cols)) a.q.scales[size_t(c / kBlock) * a.rows + row] = scale;
-        if (in && (FULL || a.cols - c > 0)) store_e4m3(a.q.q + row * a.q.stride + c, FULL ? 8 : a.cols - c, v[i], by);
+        if (in && rest(i) > 0) store_e4m3(a.q.q + row * a.q.stride + c, rest(i), v[i], by);
     }
 }
 
@@ -221,7 +224,7 @@ int rs_sandwich_norm_fwd(const rs_sandwich* block, float eps, const rs_sandwich_
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         if (!vec) return fwd_width<T, kAny>(a, s);
-        return full_width(cols) ? fwd_width<T, kFull>(a, s) : fwd_width<T, kVec>(a, s);
+        return full_width(cols) ? fwd_width<T, kFull>(a, s) : fwd_width<T, kRuns>(a, s);
     });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
