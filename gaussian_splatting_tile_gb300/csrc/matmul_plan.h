@@ -57,11 +57,19 @@ inline Plan plan_matmul(int m, int n, int k) {
     return p;
 }
 
-// Whether a product with an 8-bit result is the tile kernel's alone: its threads hold a row's 128 sums of 256 columns a
-// tile, unsplit.  Otherwise the result goes to the workspace in float32 and from there to 8 bits.
+// Whether a product with an 8-bit result is the tile kernel's alone: a thread of it holds a row's 128 sums of one block in
+// 256 columns a tile, unsplit.  Otherwise the result goes to the workspace in float32 and from there to 8 bits, in two
+// more launches at most.
+//  - From 65 rows on alone, unless the plan splits a contraction of more than 16 blocks: 160,000 x 512 x 512 58 against
+//    181 us, x 128 x 512 32 against 53, 1000 x 512 x 512 6.8 against 9.0 in a graph, 256 x 2048 x 2048 12.8 against 18.6;
+//    the other way 512 x 256 x 9300 37 against 19.
+//  - Fewer rows alone up to 8 blocks, where a call saves the host a launch: 37 x 1001 x 777 11.8 against 17.4 us, 1 x
+//    1024 x 1024 11.0 against 15.8 (in a graph 8.4 against 5.4); beyond, the rows kernel is worth two launches: 64 x 4096
+//    x 4096 20 against 16.
 inline bool direct_8bit(int m, int n, int k) {
-    const Plan p = plan_matmul(m, n, k);
-    return p.rows == 0 && p.splits == 1;
+    const int blocks = ceil_div(k, kBlock);
+    if (m <= 64) return blocks <= 8;
+    return blocks <= 16 || plan_matmul(m, n, k).splits == 1;
 }
 
 }  // namespace rs

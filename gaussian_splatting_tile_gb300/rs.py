@@ -901,7 +901,7 @@ def _form(pair, name, shape):
         return _NO_FORM
     q, scales = pair
     p, stride = _mat(q, name, _FP8, shape)
-    return p or 0, stride, _scales(scales, f"{name}'s scales", _blocks(shape[1]), shape[0]) or 0
+    return p or 0, stride, _scales(scales, name, _blocks(shape[1]), shape[0]) or 0
 
 
 _NO_FORM = (0, 0, 0)
@@ -950,9 +950,9 @@ def rs_sandwich_norm_fwd(x, r, post_weight, pre_weight, q=None, scales=None, gat
     ps, ss = _mat(sum, "sum", dt, shape)
     py, sy = _mat(y, "y", dt, shape)
     form = _NO_FORM if q is None and scales is None else _form((q, scales), "q", shape)
-    kept = [_form(f, n, shape) for f, n in ((kept_x, "kept_x"), (kept_r, "kept_r"), (kept_gate, "kept_gate"))]
+    kx, kr, kz = _form(kept_x, "kept_x", shape), _form(kept_r, "kept_r", shape), _form(kept_gate, "kept_gate", shape)
     out = rs_sandwich_out.from_buffer_copy(_SANDWICH_OUT.pack(
-        ps or 0, ss, py or 0, sy, *form, *kept[0], *kept[1], *kept[2], _vec(rstd_r, f32, rows, "rstd_r") or 0,
+        ps or 0, ss, py or 0, sy, *form, *kx, *kr, *kz, _vec(rstd_r, f32, rows, "rstd_r") or 0,
         _vec(rstd_s, f32, rows, "rstd_s") or 0))
     _check("rs_sandwich_norm_fwd", lib().rs_sandwich_norm_fwd(block, eps, out, _stream(stream)))
 

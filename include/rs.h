@@ -643,7 +643,8 @@ int rs_transpose_fp8(int32_t rows, int32_t cols, const uint8_t* d_q, size_t q_st
 
 /* rs_matmul_fp8 with its result in 8 bits: d_q [m][n] with d_scales [ceil(n / 128)][m], the 8-bit
  * form of the float32 sums (after the relu, where asked for), ready to be the next product's
- * operand and to be kept for the backward.  k = 0 gives the form of zeros.  Operands, relu and
+ * operand and to be kept for the backward.  (The sums' roundings may be other ones than
+ * rs_matmul_fp8's for the same sizes.)  k = 0 gives the form of zeros.  Operands, relu and
  * errors as rs_matmul_fp8; d_workspace: rs_matmul_fp8_q_workspace_size bytes (0: none needed, may
  * be NULL). */
 size_t rs_matmul_fp8_q_workspace_size(int32_t m, int32_t n, int32_t k);

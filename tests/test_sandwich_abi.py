@@ -112,12 +112,12 @@ def test_transpose_refusals(L):
 
 
 def test_matmul_q_refusals(L):
-    need = rs.rs_matmul_fp8_q_workspace_size(64, 256, 128)
+    need = rs.rs_matmul_fp8_q_workspace_size(64, 256, 1280)
     assert need >= 64 * 256 * 4
-    base = dict(m=64, n=256, k=128, a=P, as_=128, sa=P, b=P, bs=128, sb=P, rows=128, relu=0, q=P, qs=256, sc=P, ws=P,
+    base = dict(m=64, n=256, k=1280, a=P, as_=1280, sa=P, b=P, bs=1280, sb=P, rows=128, relu=0, q=P, qs=256, sc=P, ws=P,
                 bytes=need)
     call = lambda **c: L.rs_matmul_fp8_q(*(base | c).values(), None)
-    for c in (dict(m=-1), dict(n=-1), dict(k=-1), dict(a=None), dict(a=ODD), dict(as_=120), dict(as_=136), dict(sa=None),
+    for c in (dict(m=-1), dict(n=-1), dict(k=-1), dict(a=None), dict(a=ODD), dict(as_=1264), dict(as_=1288), dict(sa=None),
               dict(b=None), dict(bs=100), dict(sb=ODD), dict(rows=64), dict(q=None), dict(q=0x10008), dict(qs=255), dict(qs=240),
               dict(sc=None), dict(sc=ODD), dict(ws=None), dict(ws=ODD), dict(m=0x7ffffc01)):
         assert call(**c) == BAD, c
