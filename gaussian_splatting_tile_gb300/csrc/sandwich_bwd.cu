@@ -167,46 +167,80 @@ __global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant
 
 // ---- up to 4096 columns
 // The copies of a row's operands on their way: every thread copies its own runs into a place of its own and reads them
-// back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
-                 : "memory");
-}
-__device__ __forceinline__ void copy8(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src)
-                 : "memory");
+// back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.  Through L1, where the
+// two halves of a float32 run's sectors meet (160,000 x 512 float32: 383 against 626 us past it).
+//
+// `bytes` of SIZE are read, the rest becomes zero.
+template <int SIZE>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes = SIZE) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
+                 ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "n"(SIZE), "r"(bytes) : "memory");
 }
 
-template <typename T, bool KEPT, int TPR, int RUNS>
+template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 struct Ring {
+    static constexpr bool kWhole = MOVE != kAny;                               // runs on 16-byte boundaries
     static constexpr int kThreads = TPR < 128 ? 128 : TPR;
-    static constexpr int kUnit = int(sizeof(T)) / 2;                           // 16-byte words of a run
-    static constexpr int kWide = (KEPT ? 2 : 5) * RUNS * kUnit, kNarrow = KEPT ? 3 * RUNS : 0;
-    static constexpr int kStage = kThreads * (16 * kWide + 8 * kNarrow);
+    // A run's words: of 16 bytes, or of 4 with one more where it may start in the middle of one.
+    static constexpr int kWord = kWhole ? 16 : 4, kWords = kWhole ? int(sizeof(T)) / 2 : sizeof(T) == 2 ? 5 : 8;
+    static constexpr int kWide = (KEPT ? 2 : 5) * RUNS * kWords, kNarrow = KEPT ? 3 * RUNS : 0;
+    static constexpr int kStage = kThreads * (kWord * kWide + 8 * kNarrow);
     static constexpr int kStages = kStage <= 24 * 1024 ? 3 : 2;
     static constexpr int kBytes = kStages * kStage;
+    static constexpr int kVectors = 3 * RUNS * TPR * 32;                       // behind the ring
+    static constexpr int kShared = kBytes + kVectors;                          // what a block is launched with
+    static_assert(kShared >= kThreads * 32 && kShared <= 226 * 1024, "room to join the rows' sums, and for the block");
     static constexpr int kBlocks = kThreads > 128 ? 1 : RUNS == 1 ? 3 : 2;   // an SM: registers
     static __device__ __forceinline__ uint8_t* wide(uint8_t* ring, int stage, int u) {
-        return ring + stage * kStage + (u * kThreads + int(threadIdx.x)) * 16;
+        return ring + stage * kStage + kNarrow * kThreads * 8 + (u * kThreads + int(threadIdx.x)) * kWord;
     }
     static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int u) {
-        return ring + stage * kStage + kWide * kThreads * 16 + (u * kThreads + int(threadIdx.x)) * 8;
+        return ring + stage * kStage + (u * kThreads + int(threadIdx.x)) * 8;
     }
 };
 
-// One run of a matrix of T on its way into the ring, and out of it.
+// One run of a matrix of T, of which `left` values exist (whole runs: all), on its way into the ring.  Of a 16-bit run
+// that starts in the middle of a word the whole word is read: it holds the value before, or what lies before the row.
 template <typename R, typename T>
-__device__ __forceinline__ void send(uint8_t* ring, int stage, int u, const T* p) {
+__device__ __forceinline__ void send(uint8_t* ring, int stage, int run, const T* p, int left) {
+    const int u = run * R::kWords;
+    if constexpr (R::kWhole) {
 #pragma unroll
-    for (int i = 0; i < R::kUnit; ++i) copy16(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
+        for (int i = 0; i < R::kWords; ++i) copy_async<16>(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
+    } else {
+        const uint8_t* q = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+        const int end = int(reinterpret_cast<const uint8_t*>(p) - q) + min(left, 8) * int(sizeof(T));
+#pragma unroll
+        for (int i = 0; i < R::kWords; ++i) {
+            const int bytes = min(max(end - 4 * i, 0), 4);
+            copy_async<4>(R::wide(ring, stage, u + i), bytes > 0 ? q + 4 * i : q, bytes);
+        }
+    }
 }
+// The same run out of it, zero where it is not `live`; p as it was sent from, for where in a word it starts.
 template <typename R, typename T>
-__device__ __forceinline__ void receive(uint8_t* ring, int stage, int u, bool live, Run8<T>& v) {
-    float4 w[R::kUnit];
+__device__ __forceinline__ void receive(uint8_t* ring, int stage, int run, const T* p, bool live, Run8<T>& v) {
+    const int u = run * R::kWords;
+    if constexpr (R::kWhole) {
+        float4 w[R::kWords];
 #pragma unroll
-    for (int i = 0; i < R::kUnit; ++i)
-        w[i] = live ? *reinterpret_cast<const float4*>(R::wide(ring, stage, u + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-    memcpy(&v, w, sizeof(w));
+        for (int i = 0; i < R::kWords; ++i)
+            w[i] = live ? *reinterpret_cast<const float4*>(R::wide(ring, stage, u + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        memcpy(&v, w, sizeof(w));
+    } else {
+        uint32_t w[R::kWords];
+#pragma unroll
+        for (int i = 0; i < R::kWords; ++i)
+            w[i] = live ? *reinterpret_cast<const uint32_t*>(R::wide(ring, stage, u + i)) : 0u;
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t shift = reinterpret_cast<uintptr_t>(p) & 2 ? 16 : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift);
+            memcpy(&v, w, 16);
+        } else {
+            memcpy(&v, w, 32);
+        }
+    }
 }
 
 // A run of an operand: as it is stored, or its checkpoint's bytes and scale.
@@ -232,18 +266,18 @@ enum Vector { kPost, kPre, kAlpha };
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its shares of the
 // vectors' gradients stay in its registers and leave once per block, to be added up in a fixed order.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUNS>::kBlocks))
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
     k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
     RS_PDL_ENTER();
-    using R = Ring<T, KEPT, TPR, RUNS>;
+    using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
     constexpr bool VEC = MOVE != kAny, FULL = MOVE == kFull;
-    constexpr int kThreads = R::kThreads, kRows = kThreads / TPR, kStages = R::kStages, kU = R::kUnit;
+    constexpr int kThreads = R::kThreads, kRows = kThreads / TPR, kStages = R::kStages;
     __shared__ float smem[2][kThreads / 32 * 3];
     extern __shared__ __align__(16) uint8_t ring[];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const bool element = a.gate == kElementGate;
     // The vectors, where their loads do not wait: halves of runs apart, so that neighbours hit different banks.
-    float4* vectors = reinterpret_cast<float4*>(ring + (VEC ? R::kBytes : 0));
+    float4* vectors = reinterpret_cast<float4*>(ring + R::kBytes);
     const auto vector = [&](int k, int i, float2 (&w)[4]) {
         const float4 lo = vectors[(k * 2 * RUNS + i) * TPR + t], hi = vectors[(k * 2 * RUNS + RUNS + i) * TPR + t];
         w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w);
@@ -292,11 +326,15 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
         }
         return n;
     };
+    const auto run_of = [&](const void* p, size_t stride, long long row, int i) {
+        return static_cast<const T*>(p) + row * stride + column(i);
+    };
     const auto operand = [&](const Stored& s, long long row, int stage, int k, int i) {
         if constexpr (KEPT)
-            copy8(R::narrow(ring, stage, k * RUNS + i), static_cast<const uint8_t*>(s.p) + row * s.stride + column(i));
+            copy_async<8>(R::narrow(ring, stage, k * RUNS + i),
+                          static_cast<const uint8_t*>(s.p) + row * s.stride + column(i), min(rest(i), 8));
         else
-            send<R>(ring, stage, ((2 + k) * RUNS + i) * kU, static_cast<const T*>(s.p) + row * s.stride + column(i));
+            send<R>(ring, stage, (2 + k) * RUNS + i, run_of(s.p, s.stride, row, i), rest(i));
     };
     const auto fetch = [&](long long row, int stage) {
         if (row < a.rows) {
@@ -306,8 +344,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
                 operand(a.x, row, stage, 0, i);
                 operand(a.r, row, stage, 1, i);
                 if (element) operand(a.z, row, stage, 2, i);
-                send<R>(ring, stage, i * kU, static_cast<const T*>(a.dy) + row * a.dys + column(i));
-                if (a.ds) send<R>(ring, stage, (RUNS + i) * kU, static_cast<const T*>(a.ds) + row * a.dss + column(i));
+                send<R>(ring, stage, i, run_of(a.dy, a.dys, row, i), rest(i));
+                if (a.ds) send<R>(ring, stage, RUNS + i, run_of(a.ds, a.dss, row, i), rest(i));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -315,19 +353,15 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
     const long long step = (long long)gridDim.x * kRows;
     const long long first = (long long)blockIdx.x * kRows + sub;
     RowNumbers<RUNS> now = numbers(first);
-    if constexpr (VEC) {
 #pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
-    }
+    for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
     int stage = 0, turn = 0;
     for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += step) {
         const long long row = base + sub;
         const bool in = row < a.rows;
         const RowNumbers<RUNS> next = numbers(row + step);
-        if constexpr (VEC) {
-            fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-        }
+        fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         float row_e = 0.f, row_g = 1.f;
         if (a.gate == kRowGate) {
             row_e = gate_e(now.z);
@@ -342,29 +376,16 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
             Held<T, KEPT> rv, zv;
             Run8<T> dy, up;
             const auto take = [&](const Stored& s, int k, Held<T, KEPT>& h) {
-                if constexpr (KEPT && VEC) {
+                if constexpr (KEPT)
                     h.v.w = live ? *reinterpret_cast<const uint2*>(R::narrow(ring, stage, k * RUNS + i)) : make_uint2(0u, 0u);
-                } else if constexpr (KEPT) {
-                    h.v.load(static_cast<const uint8_t*>(s.p) + (in ? row : 0) * s.stride + column(i), in ? rest(i) : 0);
-                } else if constexpr (VEC) {
-                    receive<R>(ring, stage, ((2 + k) * RUNS + i) * kU, live, h.v);
-                } else {
-                    h.v.template load<false>(static_cast<const T*>(s.p) + (in ? row : 0) * s.stride + column(i),
-                                             in ? rest(i) : 0, column(i) > 0);
-                }
-            };
-            const auto take_grad = [&](const void* p, size_t stride, int k, Run8<T>& v) {
-                if constexpr (VEC)
-                    receive<R>(ring, stage, (k * RUNS + i) * kU, live, v);
                 else
-                    v.template load<false>(static_cast<const T*>(p) + (in ? row : 0) * stride + column(i), in ? rest(i) : 0,
-                                           column(i) > 0);
+                    receive<R>(ring, stage, (2 + k) * RUNS + i, run_of(s.p, s.stride, row, i), live, h.v);
             };
             take(a.x, 0, xv[i]);
             take(a.r, 1, rv);
             if (element) take(a.z, 2, zv);
-            take_grad(a.dy, a.dys, 0, dy);
-            if (a.ds) take_grad(a.ds, a.dss, 1, up);
+            receive<R>(ring, stage, i, run_of(a.dy, a.dys, row, i), live, dy);
+            if (a.ds) receive<R>(ring, stage, RUNS + i, run_of(a.ds, a.dss, row, i), live, up);
             if (element) {
 #pragma unroll
                 for (int p = 0; p < 4; ++p) {
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, TPR, RUN
     if (!a.part) return;
     float* part = a.part + size_t(blockIdx.x) * 3 * a.cols;
     float2* comb = reinterpret_cast<float2*>(ring);              // no copy is on its way to it: no row is left
-    if constexpr (VEC) asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < 3; ++k)
 #pragma unroll
@@ -512,11 +533,9 @@ cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const San
 
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 cudaError_t bwd(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
-    using R = Ring<T, KEPT, TPR, RUNS>;
-    constexpr int comb = R::kThreads > TPR ? R::kThreads * 32 : 0, kRunstors = 3 * RUNS * TPR * 32;
-    constexpr int smem = std::max(comb, (MOVE == kAny ? 0 : R::kBytes) + kRunstors);
+    using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
     grid = unsigned(std::min(bwd_blocks(a.rows, a.cols), kSms * R::kBlocks));
-    return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, smem, a, s);
+    return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, R::kShared, a, s);
 }
 template <typename T, bool KEPT, bool VEC, int RUNS>
 cudaError_t bwd_wide(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
