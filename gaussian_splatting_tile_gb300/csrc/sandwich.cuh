@@ -27,6 +27,7 @@ struct SandwichArgs {
     const float* wpost;
     const float* wpre;
     float inv_cols;
+    bool wide;                            // the vectors start on 16-byte boundaries
 };
 
 struct SandwichFwdArgs : SandwichArgs {
@@ -106,10 +107,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* smem) {
 // a thread has a run or has none); or in such accesses by threads that all have theirs (the width is 8 TPR RUNS).
 enum Move { kAny, kRuns, kFull };
 
+// Eight values of a vector; `wide`: it starts on a 16-byte boundary (value by value a load of neighbours' runs takes eight
+// times the L1's turns: 100,000 x 777 float16 forward MEASURE).
 template <bool VEC>
-__device__ __forceinline__ void load_vector(const float* p, int left, float2 (&v)[4]) {
+__device__ __forceinline__ void load_vector(const float* p, int left, bool wide, float2 (&v)[4]) {
     float w[8];
-    load8<float, VEC>(p, left, w);
+    if (VEC || wide) load8<float, true>(p, left, w);
+    else load8<float, false>(p, left, w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_float2(w[2 * i], w[2 * i + 1]);
 }
@@ -131,6 +135,11 @@ bool matrix_ok(const void* p, size_t stride, int32_t cols, int32_t dtype) {
 bool form_ok(const rs_fp8_matrix& f, int32_t cols) {
     if (!f.d_q && !f.d_scales) return true;
     return fp8_rows_ok(f.d_q, f.stride, cols) && ptr_ok(f.d_scales, 4);
+}
+
+bool wide_vectors(const rs_sandwich* b) {
+    return ptr_ok(b->d_post_weight, 16) && ptr_ok(b->d_pre_weight, 16) &&
+           (!b->d_residual_scale || ptr_ok(b->d_residual_scale, 16));
 }
 
 // The block's operands; `kept`: whether they are checkpoints, `vec`: whether runs can move in 16-byte accesses.
@@ -159,8 +168,7 @@ bool operands_ok(const rs_sandwich* b, bool& kept, bool& vec) {
             return false;
         }
     }
-    vec = b->cols % 8 == 0 && ptr_ok(b->d_post_weight, 16) && ptr_ok(b->d_pre_weight, 16) &&
-          (!b->d_residual_scale || ptr_ok(b->d_residual_scale, 16));
+    vec = b->cols % 8 == 0 && wide_vectors(b);
     if (!kept)
         vec = vec && rows16(b->d_x, b->x_stride, z) && rows16(b->d_r, b->r_stride, z) &&
               (!element || rows16(b->d_gate, b->gate_stride, z));
@@ -171,7 +179,7 @@ SandwichArgs args_of(const rs_sandwich* b) {
     return {b->rows, b->cols, b->gate_cols == 0 ? kNoGate : b->gate_cols == 1 ? kRowGate : kElementGate,
             {b->d_x, b->x_stride, b->d_x_scales}, {b->d_r, b->r_stride, b->d_r_scales},
             {b->d_gate, b->gate_stride, b->d_gate_scales}, b->d_residual_scale, b->d_post_weight, b->d_pre_weight,
-            1.0f / float(b->cols)};
+            1.0f / float(b->cols), wide_vectors(b)};
 }
 
 }  // namespace

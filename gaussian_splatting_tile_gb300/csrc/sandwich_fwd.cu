@@ -116,11 +116,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
 #pragma unroll
             for (int p = 0; p < 4; ++p) g[p] = f2(row_gate);
         }
-        load_vector<VEC>(a.wpost + column(i), rest(i), w);
+        load_vector<VEC>(a.wpost + column(i), rest(i), a.wide, w);
 #pragma unroll
         for (int p = 0; p < 4; ++p) g[p] = f2_mul(g[p], f2_mul(f2_mul(rv[i].pair(p), f2(rstd_r)), w[p]));
         if (a.alpha) {
-            load_vector<VEC>(a.alpha + column(i), rest(i), w);
+            load_vector<VEC>(a.alpha + column(i), rest(i), a.wide, w);
 #pragma unroll
             for (int p = 0; p < 4; ++p) v[i][p] = f2_fma(w[p], xv[i].pair(p), g[p]);
         } else {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
         float2 w[4];
-        load_vector<VEC>(a.wpre + column(i), rest(i), w);
+        load_vector<VEC>(a.wpre + column(i), rest(i), a.wide, w);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             v[i][p] = f2_mul(f2_mul(v[i][p], f2(rstd_s)), w[p]);
