@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu |
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const bool in = r + i < a.rows;
-        v[i].template load<VEC>(static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c, in ? left : 0, c > 0);
+        const T* p = static_cast<const T*>(a.x) + (in ? r + i : 0) * a.xs + c;
+        if constexpr (FORM == kRowsColsRelu8 && !VEC) v[i].load_words(p, in ? left : 0);
+        else v[i].template load<VEC>(p, in ? left : 0, c > 0);
     }
     if constexpr (FORM == kRowsColsRelu) {
         Run8<T> u[8];

@@ -55,12 +55,16 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
         return FULL ? 8 : !in ? 0 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
     };
     Run8<T> xv[RUNS], rv[RUNS], zv[RUNS];
+    const auto load = [&](Run8<T>& v, const T* p, int i) {
+        if constexpr (VEC) v.template load<true>(p + column(i), rest(i));
+        else v.load_words(p + column(i), rest(i));
+    };
 #pragma unroll
-    for (int i = 0; i < RUNS; ++i) rv[i].template load<VEC>(r + column(i), rest(i), column(i) > 0);
+    for (int i = 0; i < RUNS; ++i) load(rv[i], r, i);
 #pragma unroll
     for (int i = 0; i < RUNS; ++i) {
-        xv[i].template load<VEC>(x + column(i), rest(i), column(i) > 0);
-        if (a.gate == kElementGate) zv[i].template load<VEC>(z + column(i), rest(i), column(i) > 0);
+        load(xv[i], x, i);
+        if (a.gate == kElementGate) load(zv[i], z, i);
     }
     const float row_gate = a.gate == kRowGate ? gate_of(gate_e(to_f(z[0]))) : 1.f;
     float2 ss = f2(0.f);

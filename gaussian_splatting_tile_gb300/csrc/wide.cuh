@@ -88,6 +88,7 @@ struct Run8 {
             for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
         }
     }
+    __device__ __forceinline__ void load_words(const T* p, int left) { load<false>(p, left); }
     // zero where u <= 0
     __device__ __forceinline__ void mask(const Run8& u) {
 #pragma unroll
@@ -134,6 +135,21 @@ struct PackedRun8 {
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[i] = i < left ? q[i] : 0;
             w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
+        }
+    }
+    // The same at any even address, without a way of its own for a row's first and last run: every aligned word that
+    // holds one of the values is read whole, with the value before or after it.
+    __device__ __forceinline__ void load_words(const T* p, int left) {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
+        const int off = int(reinterpret_cast<uintptr_t>(p) & 2), end = off + 2 * min(left, 8);
+        uint32_t r[5];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) r[i] = left > 0 && 4 * i < end ? q[i] : 0u;
+        w = make_uint4(__funnelshift_r(r[0], r[1], 8 * off), __funnelshift_r(r[1], r[2], 8 * off),
+                       __funnelshift_r(r[2], r[3], 8 * off), __funnelshift_r(r[3], r[4], 8 * off));
+        if (left < 8) {
+            const auto keep = [&](uint32_t x, int i) { return left > i + 1 ? x : left > i ? x & 0xffffu : 0u; };
+            w = make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
         }
     }
     static __device__ __forceinline__ uint32_t kept(uint32_t x, uint32_t u) {
