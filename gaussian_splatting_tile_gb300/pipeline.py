@@ -339,6 +339,7 @@ class WideAppearance:
         self.down = [_Linear(rand(c, hidden)) for _ in range(blocks)]
         self.head = _Linear(rand(3, c))
         gates = {None: 0, "row": 1, "element": c}[gate]
+        elements = gates > 1  # one column is a gate a row
         self.gates = [_Linear(rand(gates, c)) for _ in range(blocks)] if gate else [None] * blocks
         e = lambda r, k, d=dtype: torch.empty(r, k, dtype=d, device=dev)
         q8 = lambda r, k: rs.fp8_empty(r, k, dev)
@@ -356,9 +357,9 @@ class WideAppearance:
             self.results = [e(n, c)] * blocks if fewer else [e(n, c) for _ in range(blocks)]
             self.zs = [None] * blocks
             if gate:
-                self.zs = [e(n, gates)] * blocks if fewer and gate == "element" else [e(n, gates) for _ in range(blocks)]
+                self.zs = [e(n, gates)] * blocks if fewer and elements else [e(n, gates) for _ in range(blocks)]
             if fewer:
-                kept = ("x", "r") + (("gate",) if gate == "element" else ())
+                kept = ("x", "r") + (("gate",) if elements else ())
                 self.kept = [{k: q8(n, c) for k in kept} for _ in range(blocks)]
         # scratch: 8-bit operands by rows and by columns, gradients, results of products
         self.qc, self.qct = q8(n, c), q8(c, n)

@@ -276,10 +276,10 @@ def test_on_a_stream_and_in_a_graph(options):
     assert int(net.steps) == 2
 
 
-def test_no_blocks_and_one_gaussian():
+def test_no_blocks_one_gaussian_and_one_feature():
     for options in OPTIONS:
-        for n, blocks in ((40, 0), (1, 1), (1, 2)):
-            net, dcol = network(n, 64, 64, blocks, torch.float32, **options)
+        for n, blocks, width in ((40, 0, 64), (1, 1, 64), (1, 2, 64), (70, 2, 1), (70, 1, 130)):
+            net, dcol = network(n, width, 64, blocks, torch.float32, **options)
             net.forward()
             net.backward(dcol)
             assert all(bool(torch.isfinite(g).all()) for _, g in net.parameters())
