@@ -16,8 +16,14 @@
 // with few blocks are bound by the results' way out. Measured: 65536 x 2048 x 2048 float16 out 240 us (2.3 PFLOP/s;
 // without any adding up the same loads and products would take 148), 8192^3 2.6 PFLOP/s, 160,000 x 512 x 512 bf16 56
 // us (4.4 TB/s; 37 at the copy's rate), dW of a layer (512 x 256 x 160,000, a scale a row) 45 us from a cold cache, 1
-// x 4096 x 4096 9.5 us, as long as its call.  Rows of out that are not on 16-byte boundaries leave value by value:
-// 160,000 x 501 x 512 113 us from a cold cache where 512 columns take 88.
+// x 4096 x 4096 9.5 us, as long as its call.  Rows of out that are not on 16-byte boundaries leave value by value: 160,000
+// x 501 x 512 113 us from a cold cache where 512 columns take 88.
+//
+// An 8-bit result: with 256 columns a tile a reader holds a row's 128 sums of one block, so it settles the block's scale
+// by itself, and a pass out is 128 bytes a row.  160,000 x 512 x 512 58 us (a float32 result and its 8-bit form: 181),
+// bound as above: of the 25 that memory and products need each, the readers' way round leaves 43%.  Results by plain
+// stores instead of TMA and the fence before it 66; loads of 32 columns from tensor memory, which do not fit the registers,
+// 69.
 #include <cuda.h>
 
 #include <cfloat>

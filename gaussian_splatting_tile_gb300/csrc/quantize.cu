@@ -6,6 +6,7 @@
 //
 // Measured: 160,000 x 512 bf16 both forms 60 us (5.4 TB/s), through a relu 85 us (5.8 TB/s), float32 5.9 TB/s; 128 x 128
 // forms both ways round of 8192 x 8192 float32 68 us (5.9 TB/s), bf16 51 us (5.2 TB/s), of 2048 x 2048 10 us, the launch.
+// Through a relu kept in 8 bits 160,000 x 512 bf16 67 us (6.1 TB/s); 80,000 x 1001, rows between words, 133 us (3.1 TB/s).
 #include "wide.cuh"
 
 namespace rs {
@@ -79,7 +80,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu |
     const int ct = blockIdx.x % a.ctiles, rt = blockIdx.x / a.ctiles;  // neighbours share the rows
     const int c0 = ct * kBlock, c = c0 + tx * 8;
     const long long r0 = (long long)rt * kBlock, r = r0 + ty * 8;
-    const int left = FULL ? 8 : a.cols - c;
+    // through a checkpoint, 16-byte rows come in whole runs of eight (80,000 x 1000 bf16: 70 us, 88 with ragged ones)
+    const int left = FULL ? 8 : FORM == kRowsColsRelu8 && VEC ? (c < a.cols ? 8 : 0) : a.cols - c;
     Run8<T> v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -185,7 +187,8 @@ __global__ void __launch_bounds__(256, sizeof(T) == 4 || FORM == kRowsColsRelu |
 
 // The transposed form of a checkpoint: 128 rows x 64 columns a block, a thread 8 x 8 values, which are a byte times
 // their row's scale.  They stay bytes and are widened twice, for the columns' maxima and for their new bytes: that leaves
-// registers for ten blocks an SM, which load, compute and store in turn.  Bound by memory: one byte in, one out.
+// registers for ten blocks an SM, which load, compute and store in turn.  One byte in, one out, and nearly enough
+// instructions to fill that time: 250,000 x 512 48.5 us (5.4 TB/s); with tiles of 128 columns 56, kept wide 63.
 constexpr int kHalf = kBlock / 2;
 
 __global__ void __launch_bounds__(128, 10) k_transpose(QuantArgs a, bool vec) {
@@ -201,7 +204,7 @@ __global__ void __launch_bounds__(128, 10) k_transpose(QuantArgs a, bool vec) {
     float scale[8];
     const uint8_t* from = static_cast<const uint8_t*>(a.x) + r * a.xs + c;
     const float* sc = a.scales + size_t(ct >> 1) * a.rows + r;
-    if (r0 + kBlock <= a.rows && c0 + kHalf <= a.cols && a.rows % 4 == 0 && vec) {  // nothing to ask, a third of the tile's time
+    if (r0 + kBlock <= a.rows && c0 + kHalf <= a.cols && a.rows % 4 == 0 && vec) {  // nothing to ask (asking: 56 us)
 #pragma unroll
         for (int i = 0; i < 8; ++i, from += a.xs) v[i].load(from, 8);
         const float4 lo = reinterpret_cast<const float4*>(sc)[0], hi = reinterpret_cast<const float4*>(sc)[1];
@@ -287,7 +290,7 @@ int quantize(QuantArgs a, int32_t dtype, bool blocks, cudaStream_t s, bool relu8
     a.ctiles = ceil_div(a.cols, kBlock);
     a.rtiles = ceil_div(a.rows, kBlock);
     if ((long long)a.ctiles * a.rtiles > 0x7fffffffLL) return RS_ERR_INVALID_ARG;
-    const bool vec = rows16(a.x, a.xs, z) && (relu8 || !a.relu || rows16(a.relu, a.relus, z));
+    const bool vec = rows16(a.x, a.xs, z) && (relu8 ? a.cols % 8 == 0 : !a.relu || rows16(a.relu, a.relus, z));
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         const unsigned g = unsigned(a.ctiles) * a.rtiles;

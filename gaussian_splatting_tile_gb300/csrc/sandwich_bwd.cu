@@ -74,7 +74,8 @@ __device__ __forceinline__ void values(const SandwichBwdArgs& a, const BwdRun<T,
 }
 
 // Rows of more than 4096 columns: a block's row has more values than its registers hold, so it is read twice (the second
-// time from L2) and a thread's shares of the vectors' gradients stay in shared memory.
+// time from L2) and a thread's shares of the vectors' gradients stay in shared memory.  10,000 x 8192 bf16 509 us (2.1 TB/s):
+// sixteen warps an SM that wait for their loads.
 template <typename T, bool KEPT, bool VEC, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant__ SandwichBwdArgs a) {
     RS_PDL_ENTER();
@@ -265,6 +266,13 @@ enum Vector { kPost, kPre, kAlpha };
 
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its shares of the
 // vectors' gradients stay in its registers and leave once per block, to be added up in a fixed order.
+//
+// With 16 columns a thread those shares and what the row's two passes share take some 230 registers, so there are eight
+// warps on an SM; the ring keeps memory busy all the same, and the vectors wait in shared memory, since eight warps do not
+// hide loads from L1 (160,000 x 512 from checkpoints 190 against 256 us).  Measured there: three blocks an SM with spills
+// 372; eight columns a thread on two warps, without the ring, 385; five rows in flight instead of two the same.  190 us is
+// 5.6 TB/s, 83% of the copy's rate, and half of the instructions' rate; as stored 200 us (6.5 TB/s), float32 383 us (6.8
+// TB/s), 10,007 x 1000 float16 35 us, whose last two microseconds are the sums' launch.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
     k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
@@ -618,6 +626,8 @@ int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grad
     unsigned grid = 0;
     cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
+        // nothing asked, as in the forward, pays from checkpoints alone (160,000 x 512: 190 us, 196 asking; as stored 214
+        // and 206)
         if (kept) {
             if (!vec) return bwd_width<T, true, kAny>(a, grid, s);
             return full_width(cols) ? bwd_width<T, true, kFull>(a, grid, s) : bwd_width<T, true, kRuns>(a, grid, s);

@@ -32,9 +32,13 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int left, const float2 (&
     store8_bytes(p, left, e4m3x4(w[0].x, w[0].y, w[1].x, w[1].y), e4m3x4(w[2].x, w[2].y, w[3].x, w[3].y));
 }
 
-// A row stays in registers between its sums, as in the plain norm: TPR threads, RUNS runs of eight values each.  Two
-// runs a thread halve what a thread does once (sums over the row, maxima, quotients), and a row of up to 512 values then
-// is a warp's own, without a barrier.
+// A row stays in registers between its sums, as in the plain norm: TPR threads, RUNS runs of eight values each.  What
+// bounds it is memory, once the instructions fit into its time: two runs a thread halve what a thread does once (sums
+// over the row, maxima, quotients), and a row of up to 512 values then is a warp's own, without a barrier; arithmetic is
+// in pairs; two operands' or three operands' maxima travel together.  That took 250,000 x 512 bf16, gated, operands kept,
+// from 384 us (103 instructions a value) to 243 (60; 6.4 TB/s, 94% of the copy's rate).  float32 160,000 x 512 233 us
+// (7.1 TB/s); 80,000 x 1000 bf16 194 us (5.0 TB/s: three of a row's 128 runs are empty, and rows of two warps wait for each
+// other); 80,000 x 1001, between words, 254 us.  One row costs the call, 11.5 us.
 template <typename T, Move MOVE, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __grid_constant__ SandwichFwdArgs a) {
     RS_PDL_ENTER();
@@ -178,7 +182,8 @@ cudaError_t fwd(const SandwichFwdArgs& a, cudaStream_t s) {
     return pdl_launch(k_sandwich_fwd<T, MOVE, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
 }
 
-// Two runs a thread from 129 columns on, on as few threads as they fit.
+// Two runs a thread from 129 columns on, on as few threads as they fit (512 columns on 64 threads with one run each: 384
+// against 243 us, with the arithmetic one by one).  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
 template <typename T, Move MOVE>
 cudaError_t fwd_width(const SandwichFwdArgs& a, cudaStream_t s) {
     const int runs = ceil_div(a.cols, 8);
