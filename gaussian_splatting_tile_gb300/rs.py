@@ -196,10 +196,10 @@ def lib():
                                            ctypes.c_double, i32, ctypes.c_float, _VP, _VP, sz, _VP]
         L.rs_adam_step_clipped_counted.argtypes = [ctypes.POINTER(rs_adam_segment), i32, ctypes.c_double, ctypes.c_double,
                                                    ctypes.c_double, _VP, ctypes.c_float, _VP, _VP, sz, _VP]
-        L.rs_sandwich_norm_fwd.argtypes = [ctypes.POINTER(rs_sandwich), ctypes.c_float, ctypes.POINTER(rs_sandwich_out),
-                                           _VP]
+        # rs_sandwich and its companions come by reference or as their packed bytes
+        L.rs_sandwich_norm_fwd.argtypes = [_VP, ctypes.c_float, _VP, _VP]
         L.rs_sandwich_norm_bwd_workspace_size.argtypes = [i32, i32]
-        L.rs_sandwich_norm_bwd.argtypes = [ctypes.POINTER(rs_sandwich), ctypes.POINTER(rs_sandwich_grads), _VP, sz, _VP]
+        L.rs_sandwich_norm_bwd.argtypes = [_VP, _VP, _VP, sz, _VP]
         L.rs_quantize_fp8_relu8.argtypes = [i32, i32, i32, _VP, sz, _VP, sz, _VP, sz, _VP, _VP, sz, _VP, _VP]
         L.rs_transpose_fp8.argtypes = [i32, i32, _VP, sz, _VP, _VP, sz, _VP, _VP]
         L.rs_matmul_fp8_q_workspace_size.argtypes = [i32, i32, i32]
@@ -889,50 +889,47 @@ def _gate_cols(gate, shape) -> int:
     """Of a gate (a matrix or a kept (q, scales)): 0 none, 1 one a row, else one an element."""
     if gate is None:
         return 0
-    m = gate[0] if type(gate) is tuple else gate
-    if m.dim() != 2 or m.shape[0] != shape[0] or m.shape[1] not in (1, shape[1]):
-        raise ValueError(f"the gate is {tuple(m.shape)}, needs {tuple(shape)} or {(shape[0], 1)}")
-    return int(m.shape[1])
+    m = (gate[0] if type(gate) is tuple else gate).shape
+    if m == shape:
+        return shape[1]
+    if len(m) != 2 or m[0] != shape[0] or m[1] != 1:
+        raise ValueError(f"the gate is {tuple(m)}, needs {tuple(shape)} or {(shape[0], 1)}")
+    return 1
 
 
 def _form(pair, name, shape):
     """(pointer, stride, scales) of an 8-bit matrix, (q, scales) as fp8_empty gives them."""
-    if pair is None:
-        return _NO_FORM
     q, scales = pair
     p, stride = _mat(q, name, _FP8, shape)
-    return p or 0, stride, _scales(scales, name, _blocks(shape[1]), shape[0]) or 0
+    return p or 0, stride, _scales(scales, name, -(-shape[1] // RS_FP8_BLOCK), shape[0]) or 0
 
 
 _NO_FORM = (0, 0, 0)
 
 
-def _operand(t, name, dtype, shape):
-    """(pointer, stride, scales) of a matrix, or of a kept one (q, scales)."""
-    if type(t) is not tuple:
-        p, stride = _mat(t, name, dtype, shape)
-        return p or 0, stride, 0
-    p, stride, scales = _form(t, name, shape)
-    if not scales:
+def _kept(pair, name, shape):
+    """The same of an operand, whose scales have to be there."""
+    got = _form(pair, name, shape)
+    if not got[2]:
         raise ValueError(f"{name} needs its scales")
-    return p, stride, scales
+    return got
 
 
-# the structures' fields packed at once: assigning them one by one takes a small call 3 us of its 14
-_SANDWICH, _SANDWICH_OUT, _SANDWICH_GRADS = struct.Struct("4i12Q"), struct.Struct("18Q"), struct.Struct("15Q")
+# The structures' fields, packed at once: a ctypes structure filled field by field takes a small call 3 us of its 14.
+_SANDWICH, _SANDWICH_OUT, _SANDWICH_GRADS = (struct.Struct(f).pack for f in ("4i12Q", "18Q", "15Q"))
 
 
-def _sandwich(x, r, gate, dtype, shape, post_weight, pre_weight, residual_scale):
+def _sandwich(x, r, gate, gate_cols, dtype, shape, post_weight, pre_weight, residual_scale):
+    """rs_sandwich's bytes."""
     rows, cols = shape
-    gate_cols = _gate_cols(gate, shape)
     f32 = torch.float32
-    px, sx, qx = _operand(x, "x", dtype, shape)
-    pr, sr, qr = _operand(r, "r", dtype, shape)
-    pz, sz, qz = _operand(gate, "gate", dtype, shape if gate_cols == cols else (rows, 1)) if gate_cols else _NO_FORM
-    return gate_cols, rs_sandwich.from_buffer_copy(_SANDWICH.pack(
-        rows, cols, _DTYPES[dtype], gate_cols, px, sx, qx, pr, sr, qr, pz, sz, qz,
-        0 if residual_scale is None else _vec(residual_scale, f32, cols, "residual_scale"),
-        _vec(post_weight, f32, cols, "post_weight") or 0, _vec(pre_weight, f32, cols, "pre_weight") or 0))
+    px, sx, qx = _kept(x, "x", shape) if type(x) is tuple else (*_mat(x, "x", dtype, shape), 0)
+    pr, sr, qr = _kept(r, "r", shape) if type(r) is tuple else (*_mat(r, "r", dtype, shape), 0)
+    pz, sz, qz = (_NO_FORM if gate_cols == 0 else _kept(gate, "gate", shape) if type(gate) is tuple else
+                  (*_mat(gate, "gate", dtype, shape if gate_cols == cols else (rows, 1)), 0))
+    return _SANDWICH(rows, cols, _DTYPES[dtype], gate_cols, px or 0, sx, qx, pr or 0, sr, qr, pz or 0, sz, qz,
+                     0 if residual_scale is None else _vec(residual_scale, f32, cols, "residual_scale"),
+                     _vec(post_weight, f32, cols, "post_weight") or 0, _vec(pre_weight, f32, cols, "pre_weight") or 0)
 
 
 def rs_sandwich_norm_fwd(x, r, post_weight, pre_weight, q=None, scales=None, gate=None, residual_scale=None, sum=None,
@@ -942,19 +939,23 @@ def rs_sandwich_norm_fwd(x, r, post_weight, pre_weight, q=None, scales=None, gat
     form of y = norm(sum) pre_weight.  x, r, sum, y [rows, cols] float32 / float16 / bfloat16 CUDA; gate [rows, cols] or
     [rows, 1] of the same type; weights and residual_scale float32 [cols]; rstd_r, rstd_s float32 [rows].  kept_x, kept_r
     and kept_gate, (q, scales) as fp8_empty(rows, cols) gives them, receive the operands in 8 bits for the backward."""
-    shape = rows, cols = x.shape
-    dt = x.dtype
+    shape = x.shape
+    rows = shape[0]
+    dt, f32 = x.dtype, torch.float32
     _dtype(x, "x")
-    f32 = torch.float32
-    _, block = _sandwich(x, r, gate, dt, shape, post_weight, pre_weight, residual_scale)
-    ps, ss = _mat(sum, "sum", dt, shape)
-    py, sy = _mat(y, "y", dt, shape)
-    form = _NO_FORM if q is None and scales is None else _form((q, scales), "q", shape)
-    kx, kr, kz = _form(kept_x, "kept_x", shape), _form(kept_r, "kept_r", shape), _form(kept_gate, "kept_gate", shape)
-    out = rs_sandwich_out.from_buffer_copy(_SANDWICH_OUT.pack(
-        ps or 0, ss, py or 0, sy, *form, *kx, *kr, *kz, _vec(rstd_r, f32, rows, "rstd_r") or 0,
-        _vec(rstd_s, f32, rows, "rstd_s") or 0))
-    _check("rs_sandwich_norm_fwd", lib().rs_sandwich_norm_fwd(block, eps, out, _stream(stream)))
+    block = _sandwich(x, r, gate, _gate_cols(gate, shape), dt, shape, post_weight, pre_weight, residual_scale)
+    ps, ss = (0, 0) if sum is None else _mat(sum, "sum", dt, shape)
+    py, sy = (0, 0) if y is None else _mat(y, "y", dt, shape)
+    out = _SANDWICH_OUT(
+        ps, ss, py, sy, *(_NO_FORM if q is None and scales is None else _form((q, scales), "q", shape)),
+        *(_NO_FORM if kept_x is None else _form(kept_x, "kept_x", shape)),
+        *(_NO_FORM if kept_r is None else _form(kept_r, "kept_r", shape)),
+        *(_NO_FORM if kept_gate is None else _form(kept_gate, "kept_gate", shape)),
+        0 if rstd_r is None else _vec(rstd_r, f32, rows, "rstd_r") or 0,
+        0 if rstd_s is None else _vec(rstd_s, f32, rows, "rstd_s") or 0)
+    code = lib().rs_sandwich_norm_fwd(block, eps, out, _stream(stream))
+    if code:
+        _check("rs_sandwich_norm_fwd", code)
 
 
 def rs_sandwich_norm_bwd_workspace_size(rows: int, cols: int) -> int:
@@ -967,22 +968,27 @@ def rs_sandwich_norm_bwd(x, r, post_weight, pre_weight, rstd_r, rstd_s, dL_dy, d
     """Gradients of rs_sandwich_norm_fwd.  x, r and gate: the forward's matrices, or what it kept of them, (q, scales);
     a gate of one a row always is the matrix.  The vectors' gradients and dL_dgate may be None."""
     shape = rows, cols = dL_dy.shape
-    dt = dL_dy.dtype
+    dt, f32 = dL_dy.dtype, torch.float32
     _dtype(dL_dy, "dL_dy")
-    f32 = torch.float32
-    gate_cols, block = _sandwich(x, r, gate, dt, shape, post_weight, pre_weight, residual_scale)
+    gate_cols = _gate_cols(gate, shape)
+    block = _sandwich(x, r, gate, gate_cols, dt, shape, post_weight, pre_weight, residual_scale)
     pg, sg = _mat(dL_dy, "dL_dy", dt, shape)
-    pu, su = _mat(dL_dsum, "dL_dsum", dt, shape)
+    pu, su = (0, 0) if dL_dsum is None else _mat(dL_dsum, "dL_dsum", dt, shape)
     px, sx = _mat(dL_dx, "dL_dx", dt, shape)
     pr, sr = _mat(dL_dr, "dL_dr", dt, shape)
-    pz, sz = _mat(dL_dgate, "dL_dgate", dt, shape if gate_cols == cols else (rows, gate_cols))
-    grads = rs_sandwich_grads.from_buffer_copy(_SANDWICH_GRADS.pack(
-        _vec(rstd_r, f32, rows, "rstd_r") or 0, _vec(rstd_s, f32, rows, "rstd_s") or 0, pg or 0, sg, pu or 0, su, px or 0, sx,
-        pr or 0, sr, pz or 0, sz, _vec(dL_dresidual_scale, f32, cols, "dL_dresidual_scale") or 0,
-        _vec(dL_dpost_weight, f32, cols, "dL_dpost_weight") or 0, _vec(dL_dpre_weight, f32, cols, "dL_dpre_weight") or 0))
-    _check("rs_sandwich_norm_bwd", lib().rs_sandwich_norm_bwd(
+    pz, sz = ((0, 0) if dL_dgate is None else
+              _mat(dL_dgate, "dL_dgate", dt, shape if gate_cols == cols else (rows, gate_cols)))
+    grads = _SANDWICH_GRADS(
+        _vec(rstd_r, f32, rows, "rstd_r") or 0, _vec(rstd_s, f32, rows, "rstd_s") or 0, pg, sg, pu, su, px or 0, sx,
+        pr or 0, sr, pz, sz,
+        0 if dL_dresidual_scale is None else _vec(dL_dresidual_scale, f32, cols, "dL_dresidual_scale"),
+        0 if dL_dpost_weight is None else _vec(dL_dpost_weight, f32, cols, "dL_dpost_weight"),
+        0 if dL_dpre_weight is None else _vec(dL_dpre_weight, f32, cols, "dL_dpre_weight"))
+    code = lib().rs_sandwich_norm_bwd(
         block, grads, _vec(workspace, torch.uint8, 0, "workspace"), 0 if workspace is None else workspace.numel(),
-        _stream(stream)))
+        _stream(stream))
+    if code:
+        _check("rs_sandwich_norm_bwd", code)
 
 
 def rs_quantize_fp8_relu8(x, relu, q=None, scales=None, qt=None, scales_t=None, stream=None):

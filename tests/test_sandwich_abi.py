@@ -10,6 +10,7 @@ from gaussian_splatting_tile_gb300 import build_lib, rs
 OK, P, Q = rs.RS_OK, 0x10000, 0x20000
 BAD, SMALL = rs.RS_ERR_INVALID_ARG, rs.RS_ERR_WORKSPACE
 ODD = 0x10001
+ref = ctypes.byref
 
 
 @pytest.fixture(scope="module")
@@ -33,11 +34,11 @@ BAD_BLOCKS = [dict(rows=-1), dict(cols=0), dict(cols=16385, x_stride=20000, r_st
 
 @pytest.mark.parametrize("change", BAD_BLOCKS)
 def test_operands_refused_both_ways(L, change):
-    out = rs.rs_sandwich_out(q=FORM)
-    b = rs.rs_sandwich(**(BLOCK | change))
+    out = ref(rs.rs_sandwich_out(q=FORM))
+    b = ref(rs.rs_sandwich(**(BLOCK | change)))
     assert L.rs_sandwich_norm_fwd(b, 1e-6, out, None) == BAD
-    grads = rs.rs_sandwich_grads(d_rstd_r=P, d_rstd_s=P, d_dL_dy=P, dy_stride=256, d_dL_dx=Q, dx_stride=256, d_dL_dr=P,
-                                 dr_stride=256)
+    grads = ref(rs.rs_sandwich_grads(d_rstd_r=P, d_rstd_s=P, d_dL_dy=P, dy_stride=256, d_dL_dx=Q, dx_stride=256, d_dL_dr=P,
+                                     dr_stride=256))
     assert L.rs_sandwich_norm_bwd(b, grads, None, 0, None) == BAD
 
 
@@ -45,15 +46,15 @@ def test_operands_refused_both_ways(L, change):
                                     dict(gate_stride=8), dict(d_r_scales=None), dict(d_x_scales=None),
                                     dict(d_gate_scales=None), dict(gate_cols=1), dict(d_x_scales=ODD)])
 def test_kept_operands_refused(L, change):
-    b = rs.rs_sandwich(**(KEPT | change))
-    grads = rs.rs_sandwich_grads(d_rstd_r=P, d_rstd_s=P, d_dL_dy=P, dy_stride=256, d_dL_dx=Q, dx_stride=256, d_dL_dr=P,
-                                 dr_stride=256)
+    b = ref(rs.rs_sandwich(**(KEPT | change)))
+    grads = ref(rs.rs_sandwich_grads(d_rstd_r=P, d_rstd_s=P, d_dL_dy=P, dy_stride=256, d_dL_dx=Q, dx_stride=256, d_dL_dr=P,
+                                     dr_stride=256))
     assert L.rs_sandwich_norm_bwd(b, grads, None, 0, None) == BAD
 
 
 def test_forward_refusals(L):
     def call(eps=1e-6, block=BLOCK, **out):
-        return L.rs_sandwich_norm_fwd(rs.rs_sandwich(**block), eps, rs.rs_sandwich_out(**({"q": FORM} | out)), None)
+        return L.rs_sandwich_norm_fwd(ref(rs.rs_sandwich(**block)), eps, ref(rs.rs_sandwich_out(**({"q": FORM} | out))), None)
 
     F = rs.rs_fp8_matrix
     for c in (dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(block=KEPT), dict(q=F()),
@@ -63,8 +64,8 @@ def test_forward_refusals(L):
               dict(d_y=P, y_stride=100), dict(d_rstd_r=ODD), dict(d_rstd_s=ODD),
               dict(block=BLOCK | dict(gate_cols=1), kept_gate=FORM), dict(block=BLOCK | dict(gate_cols=0), kept_gate=FORM)):
         assert call(**c) == BAD, c
-    assert L.rs_sandwich_norm_fwd(None, 1e-6, rs.rs_sandwich_out(q=FORM), None) == BAD
-    assert L.rs_sandwich_norm_fwd(rs.rs_sandwich(**BLOCK), 1e-6, None, None) == BAD
+    assert L.rs_sandwich_norm_fwd(None, 1e-6, ref(rs.rs_sandwich_out(q=FORM)), None) == BAD
+    assert L.rs_sandwich_norm_fwd(ref(rs.rs_sandwich(**BLOCK)), 1e-6, None, None) == BAD
     none = dict.fromkeys([k for k in BLOCK if k.startswith("d_")])
     assert call(block=BLOCK | none | dict(rows=0, gate_cols=0), q=F()) == OK
 
@@ -77,7 +78,7 @@ def test_backward_refusals(L):
                 d_dL_dr=Q, dr_stride=256, d_dL_dgate=0x30000, dgate_stride=256, d_dL_dpost_weight=P)
 
     def call(block=BLOCK, ws=P, bytes=need, **c):
-        return L.rs_sandwich_norm_bwd(rs.rs_sandwich(**block), rs.rs_sandwich_grads(**(base | c)), ws, bytes, None)
+        return L.rs_sandwich_norm_bwd(ref(rs.rs_sandwich(**block)), ref(rs.rs_sandwich_grads(**(base | c))), ws, bytes, None)
 
     for c in (dict(d_rstd_r=None), dict(d_rstd_s=ODD), dict(d_dL_dy=None), dict(dy_stride=255), dict(d_dL_dsum=ODD),
               dict(dsum_stride=1), dict(d_dL_dx=None), dict(dx_stride=300), dict(d_dL_dr=None), dict(d_dL_dr=P),
@@ -87,8 +88,8 @@ def test_backward_refusals(L):
               dict(ws=ODD)):
         assert call(**c) == BAD, c
     assert call(bytes=need - 1) == SMALL
-    assert L.rs_sandwich_norm_bwd(None, rs.rs_sandwich_grads(**base), P, need, None) == BAD
-    assert L.rs_sandwich_norm_bwd(rs.rs_sandwich(**BLOCK), None, P, need, None) == BAD
+    assert L.rs_sandwich_norm_bwd(None, ref(rs.rs_sandwich_grads(**base)), P, need, None) == BAD
+    assert L.rs_sandwich_norm_bwd(ref(rs.rs_sandwich(**BLOCK)), None, P, need, None) == BAD
     assert call(block=BLOCK | dict(rows=0), d_dL_dpost_weight=None) == OK
 
 
@@ -139,3 +140,19 @@ def test_binding_refuses_what_it_cannot_describe(L):
         rs.rs_transpose_fp8(x, w, x.t(), w)
     with pytest.raises(TypeError):
         rs.rs_quantize_fp8_relu8(x, x)
+
+
+def test_packed_structures_are_the_declared_ones():
+    names = lambda c: [n for n, _ in c._fields_]
+    count = lambda c: sum(3 if t is rs.rs_fp8_matrix else 1 for _, t in c._fields_)
+    for cls, pack, ints in ((rs.rs_sandwich, rs._SANDWICH, 4), (rs.rs_sandwich_out, rs._SANDWICH_OUT, 0),
+                            (rs.rs_sandwich_grads, rs._SANDWICH_GRADS, 0)):
+        values = list(range(1, count(cls) + 1))
+        raw = pack(*values)
+        assert len(raw) == ctypes.sizeof(cls)
+        got = cls.from_buffer_copy(raw)
+        flat = []
+        for n in names(cls):
+            v = getattr(got, n)
+            flat += [v.d_q, v.stride, v.d_scales] if isinstance(v, rs.rs_fp8_matrix) else [v]
+        assert flat == values
