@@ -171,77 +171,99 @@ __global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant
 // back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.  Through L1, where the
 // two halves of a float32 run's sectors meet (160,000 x 512 float32: 383 against 626 us past it).
 //
-// `bytes` of SIZE are read, the rest becomes zero.
+// With `bytes`, that many of SIZE are read and the rest becomes zero.
 template <int SIZE>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes = SIZE) {
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;"
+                 ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "n"(SIZE) : "memory");
+}
+template <int SIZE>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;"
                  ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "n"(SIZE), "r"(bytes) : "memory");
 }
 
+// Rows that are not on 16-byte boundaries come in words, neighbours' words by neighbouring threads: a warp's (a row's
+// sixteen threads') runs follow each other in memory, so their words do, and one more where 16-bit runs start in the
+// middle of a word.  A thread's run then was copied by others of its warp.  (Each thread its own run's words: 80,000 x
+// 1001 bf16 as stored 434 us, float32 894.)
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 struct Ring {
     static constexpr bool kWhole = MOVE != kAny;                               // runs on 16-byte boundaries
     static constexpr int kThreads = TPR < 128 ? 128 : TPR;
-    // A run's words: of 16 bytes, or of 4 with one more where it may start in the middle of one.
-    static constexpr int kWord = kWhole ? 16 : 4, kWords = kWhole ? int(sizeof(T)) / 2 : sizeof(T) == 2 ? 5 : 8;
-    static constexpr int kWide = (KEPT ? 2 : 5) * RUNS * kWords, kNarrow = KEPT ? 3 * RUNS : 0;
-    static constexpr int kStage = kThreads * (kWord * kWide + 8 * kNarrow);
+    static constexpr int kGroup = TPR < 32 ? TPR : 32, kGroups = kThreads / kGroup;
+    static constexpr int kWords = kWhole ? int(sizeof(T)) / 2 : 2 * int(sizeof(T));  // a thread's: of 16 bytes, or of 4
+    static constexpr int kGroupBytes = kGroup * (kWhole ? 16 : 4) * kWords + (kWhole || sizeof(T) == 4 ? 0 : 16);
+    static constexpr int kWide = (KEPT ? 2 : 5) * RUNS, kNarrow = KEPT ? 3 * RUNS : 0;  // runs of T, of bytes
+    static constexpr int kStage = kWide * kGroups * kGroupBytes + kNarrow * kThreads * 8;
     static constexpr int kStages = kStage <= 24 * 1024 ? 3 : 2;
     static constexpr int kBytes = kStages * kStage;
     static constexpr int kVectors = 3 * RUNS * TPR * 32;                       // behind the ring
     static constexpr int kShared = kBytes + kVectors;                          // what a block is launched with
     static_assert(kShared >= kThreads * 32 && kShared <= 226 * 1024, "room to join the rows' sums, and for the block");
     static constexpr int kBlocks = kThreads > 128 ? 1 : RUNS == 1 ? 3 : 2;   // an SM: registers
-    static __device__ __forceinline__ uint8_t* wide(uint8_t* ring, int stage, int u) {
-        return ring + stage * kStage + kNarrow * kThreads * 8 + (u * kThreads + int(threadIdx.x)) * kWord;
+    static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int run) {
+        return ring + stage * kStage + (run * kThreads + int(threadIdx.x)) * 8;
     }
-    static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int u) {
-        return ring + stage * kStage + (u * kThreads + int(threadIdx.x)) * 8;
+    // of the group: word w of its thread l at w kGroup + l (16 bytes each), or its words in order (4 each)
+    static __device__ __forceinline__ uint8_t* wide(uint8_t* ring, int stage, int run) {
+        return ring + stage * kStage + kNarrow * kThreads * 8 + (run * kGroups + int(threadIdx.x) / kGroup) * kGroupBytes;
     }
+    static __device__ __forceinline__ int lane() { return int(threadIdx.x) % kGroup; }
 };
 
-// One run of a matrix of T, of which `left` values exist (whole runs: all), on its way into the ring.  Of a 16-bit run
-// that starts in the middle of a word the whole word is read: it holds the value before, or what lies before the row.
+// One run of a matrix of T on its way into the ring.  p: where this thread's run starts; left: how many of its values
+// exist, not above zero where none does.  Of 16-bit rows the words at their ends are read whole: with the value before
+// the row.
 template <typename R, typename T>
 __device__ __forceinline__ void send(uint8_t* ring, int stage, int run, const T* p, int left) {
-    const int u = run * R::kWords;
+    uint8_t* to = R::wide(ring, stage, run);
+    const int l = R::lane();
     if constexpr (R::kWhole) {
+        if (left <= 0) return;
 #pragma unroll
-        for (int i = 0; i < R::kWords; ++i) copy_async<16>(R::wide(ring, stage, u + i), p + i * (16 / sizeof(T)));
+        for (int i = 0; i < R::kWords; ++i) copy_async<16>(to + (i * R::kGroup + l) * 16, p + i * (16 / sizeof(T)));
     } else {
+        left += 8 * l;  // of the group
+        if (left <= 0) return;
+        p -= 8 * l;
         const uint8_t* q = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
-        const int end = int(reinterpret_cast<const uint8_t*>(p) - q) + min(left, 8) * int(sizeof(T));
+        const int off = int(reinterpret_cast<const uint8_t*>(p) - q);
+        constexpr int kStep = R::kGroup * 4, kAll = R::kWords * kStep;
+        if (left > 8 * R::kGroup) {  // every word is the row's
 #pragma unroll
-        for (int i = 0; i < R::kWords; ++i) {
-            const int bytes = min(max(end - 4 * i, 0), 4);
-            copy_async<4>(R::wide(ring, stage, u + i), bytes > 0 ? q + 4 * i : q, bytes);
+            for (int i = 0; i < R::kWords; ++i) copy_async<4>(to + l * 4 + i * kStep, q + l * 4 + i * kStep);
+            if (off && l == 0) copy_async<4>(to + kAll, q + kAll);
+        } else {
+            const int end = off + left * int(sizeof(T));
+            const auto word = [&](int at) {
+                const int bytes = min(max(end - at, 0), 4);
+                copy_async<4>(to + at, bytes > 0 ? q + at : q, bytes);
+            };
+#pragma unroll
+            for (int i = 0; i < R::kWords; ++i) word(l * 4 + i * kStep);
+            if (sizeof(T) == 2 && l == 0) word(kAll);
         }
     }
 }
 // The same run out of it, zero where it is not `live`; p as it was sent from, for where in a word it starts.
 template <typename R, typename T>
 __device__ __forceinline__ void receive(uint8_t* ring, int stage, int run, const T* p, bool live, Run8<T>& v) {
-    const int u = run * R::kWords;
-    if constexpr (R::kWhole) {
-        float4 w[R::kWords];
+    const uint8_t* from = R::wide(ring, stage, run);
+    const int l = R::lane();
+    constexpr int kQuads = int(sizeof(T)) / 2;
+    uint4 w[kQuads];
 #pragma unroll
-        for (int i = 0; i < R::kWords; ++i)
-            w[i] = live ? *reinterpret_cast<const float4*>(R::wide(ring, stage, u + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        memcpy(&v, w, sizeof(w));
-    } else {
-        uint32_t w[R::kWords];
-#pragma unroll
-        for (int i = 0; i < R::kWords; ++i)
-            w[i] = live ? *reinterpret_cast<const uint32_t*>(R::wide(ring, stage, u + i)) : 0u;
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t shift = reinterpret_cast<uintptr_t>(p) & 2 ? 16 : 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], shift);
-            memcpy(&v, w, 16);
-        } else {
-            memcpy(&v, w, 32);
-        }
+    for (int i = 0; i < kQuads; ++i)
+        w[i] = live ? *reinterpret_cast<const uint4*>(from + (R::kWhole ? i * R::kGroup + l : l * kQuads + i) * 16)
+                    : make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (!R::kWhole && sizeof(T) == 2) {
+        const uint32_t last = live ? *reinterpret_cast<const uint32_t*>(from + (l + 1) * 16) : 0u;
+        const uint32_t shift = reinterpret_cast<uintptr_t>(p) & 2 ? 16 : 0;
+        w[0] = make_uint4(__funnelshift_r(w[0].x, w[0].y, shift), __funnelshift_r(w[0].y, w[0].z, shift),
+                          __funnelshift_r(w[0].z, w[0].w, shift), __funnelshift_r(w[0].w, last, shift));
     }
+    memcpy(&v, w, sizeof(w));
 }
 
 // A run of an operand: as it is stored, or its checkpoint's bytes and scale.
@@ -338,17 +360,19 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         return static_cast<const T*>(p) + row * stride + column(i);
     };
     const auto operand = [&](const Stored& s, long long row, int stage, int k, int i) {
-        if constexpr (KEPT)
-            copy_async<8>(R::narrow(ring, stage, k * RUNS + i),
-                          static_cast<const uint8_t*>(s.p) + row * s.stride + column(i), min(rest(i), 8));
-        else
+        if constexpr (KEPT) {
+            if (rest(i) > 0)
+                copy_async<8>(R::narrow(ring, stage, k * RUNS + i),
+                              static_cast<const uint8_t*>(s.p) + row * s.stride + column(i), min(rest(i), 8));
+        } else {
             send<R>(ring, stage, (2 + k) * RUNS + i, run_of(s.p, s.stride, row, i), rest(i));
+        }
     };
     const auto fetch = [&](long long row, int stage) {
         if (row < a.rows) {
 #pragma unroll
             for (int i = 0; i < RUNS; ++i) {
-                if (rest(i) <= 0) continue;
+                if (R::kWhole && rest(i) <= 0) continue;
                 operand(a.x, row, stage, 0, i);
                 operand(a.r, row, stage, 1, i);
                 if (element) operand(a.z, row, stage, 2, i);
@@ -368,8 +392,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         const long long row = base + sub;
         const bool in = row < a.rows;
         const RowNumbers<RUNS> next = numbers(row + step);
+        if constexpr (!R::kWhole) __syncwarp();   // the row before has been read by all that share its words
         fetch(row + (kStages - 1) * step, stage == 0 ? kStages - 1 : stage - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        if constexpr (!R::kWhole) __syncwarp();   // and this one's are there
         float row_e = 0.f, row_g = 1.f;
         if (a.gate == kRowGate) {
             row_e = gate_e(now.z);
