@@ -4,169 +4,6 @@ namespace rs {
 namespace {
 
 // ---------------------------------------------------------------- backward
-// Eight values of an operand as they are stored, or of its checkpoint.
-template <typename T, bool KEPT, bool VEC>
-struct Operand8 {
-    Run8<T> v;
-    __device__ __forceinline__ void load(const Stored& s, long long row, int, int c, int left) {
-        v.template load<VEC>(static_cast<const T*>(s.p) + row * s.stride + c, left, c > 0);
-    }
-    __device__ __forceinline__ float2 pair(int p) const { return v.pair(p); }
-};
-template <typename T, bool VEC>
-struct Operand8<T, true, VEC> {
-    Bytes8 v;
-    float scale;
-    __device__ __forceinline__ void load(const Stored& s, long long row, int rows, int c, int left) {
-        v.load(static_cast<const uint8_t*>(s.p) + row * s.stride + c, left);
-        scale = left > 0 ? s.scales[size_t(c / kBlock) * rows + row] : 0.f;
-    }
-    __device__ __forceinline__ float2 pair(int p) const {
-        const float2 f = v.pair(p);
-        return make_float2(f.x * scale, f.y * scale);
-    }
-};
-
-// Everything of eight columns that the two passes over a row need.
-template <typename T, bool KEPT, bool VEC>
-struct BwdRun {
-    Operand8<T, KEPT, VEC> x, r, z;
-    Run8<T> dy, ds;
-    __device__ __forceinline__ void load(const SandwichBwdArgs& a, long long row, int c, int left) {
-        x.load(a.x, row, a.rows, c, left);
-        r.load(a.r, row, a.rows, c, left);
-        if (a.gate == kElementGate) z.load(a.z, row, a.rows, c, left);
-        dy.template load<VEC>(static_cast<const T*>(a.dy) + row * a.dys + c, left, c > 0);
-        if (a.ds) ds.template load<VEC>(static_cast<const T*>(a.ds) + row * a.dss + c, left, c > 0);
-    }
-};
-struct BwdRow {
-    float rstd_r, rstd_s, e, g;       // e, g: of the row's gate (0, 1 without a gate)
-};
-struct BwdWeights { float post[8], pre[8], alpha[8]; };
-
-struct BwdValue { float x, rh, n, p, sh, t, e, g, dy, ds; };
-
-template <typename T, bool KEPT, bool VEC>
-__device__ __forceinline__ void values(const SandwichBwdArgs& a, const BwdRun<T, KEPT, VEC>& u, const BwdRow& w,
-                                       const BwdWeights& k, int p, BwdValue (&o)[2]) {
-    const float2 x = u.x.pair(p), r = u.r.pair(p), dy = u.dy.pair(p);
-    const float2 ds = a.ds ? u.ds.pair(p) : make_float2(0.f, 0.f);
-    const float2 z = a.gate == kElementGate ? u.z.pair(p) : make_float2(0.f, 0.f);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        BwdValue& v = o[j];
-        v.x = j ? x.y : x.x;
-        v.e = w.e;
-        v.g = w.g;
-        if (a.gate == kElementGate) {
-            v.e = gate_e(j ? z.y : z.x);
-            v.g = gate_of(v.e);
-        }
-        v.rh = (j ? r.y : r.x) * w.rstd_r;
-        v.n = v.rh * k.post[2 * p + j];
-        v.p = v.g * v.n;
-        v.sh = fmaf(v.g, v.n, a.alpha ? v.x * k.alpha[2 * p + j] : v.x) * w.rstd_s;
-        v.dy = j ? dy.y : dy.x;
-        v.t = v.dy * k.pre[2 * p + j];
-        v.ds = j ? ds.y : ds.x;
-    }
-}
-
-// Rows of more than 4096 columns: a block's row has more values than its registers hold, so it is read twice (the second
-// time from L2) and a thread's shares of the vectors' gradients stay in shared memory.  10,000 x 8192 bf16 509 us (2.1 TB/s):
-// sixteen warps an SM that wait for their loads.
-template <typename T, bool KEPT, bool VEC, int TPR, int RUNS>
-__global__ void __launch_bounds__(TPR) k_sandwich_bwd_wide(const __grid_constant__ SandwichBwdArgs a) {
-    RS_PDL_ENTER();
-    __shared__ float smem[2][TPR / 32 * 3];
-    extern __shared__ float shares[];        // [3][RUNS][8][TPR]
-    const int t = threadIdx.x;
-    int turn = 0;
-    const auto share = [&](int k, int i, int j) -> float& { return shares[((k * RUNS + i) * 8 + j) * TPR + t]; };
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int i = 0; i < RUNS; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) share(k, i, j) = 0.f;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        BwdRow w{a.rstd_r[row], a.rstd_s[row], 0.f, 1.f};
-        if (a.gate == kRowGate) {
-            w.e = gate_e(to_f(static_cast<const T*>(a.z.p)[row * a.z.stride]));
-            w.g = gate_of(w.e);
-        }
-        BwdRun<T, KEPT, VEC> u;
-        float sums[3] = {0.f, 0.f, 0.f};
-        BwdWeights k;
-        const auto load = [&](int c) {
-            const int left = a.cols - c;
-            u.load(a, row, c, left);
-            load8<float, VEC>(a.wpost + c, left, k.post);
-            load8<float, VEC>(a.wpre + c, left, k.pre);
-            if (a.alpha) load8<float, VEC>(a.alpha + c, left, k.alpha);
-        };
-#pragma unroll 1
-        for (int i = 0; i < RUNS; ++i) {
-            load((i * TPR + t) * 8);
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                BwdValue v[2];
-                values<T, KEPT, VEC>(a, u, w, k, p, v);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    sums[0] = fmaf(v[j].t, v[j].sh, sums[0]);
-                    sums[1] = fmaf(fmaf(w.rstd_s, v[j].t, v[j].ds), v[j].p, sums[1]);
-                    sums[2] = fmaf(v[j].sh, v[j].p, sums[2]);
-                }
-            }
-        }
-        row_sums<TPR>(sums, smem[turn ^= 1]);
-        const float c1 = w.rstd_s * (sums[0] * a.inv_cols);
-        const float dot = fmaf(-c1, sums[2], sums[1]);           // sum of ds p
-        const float c2 = dot * a.inv_cols;
-        if (a.gate == kRowGate && a.dz && t == 0)
-            static_cast<T*>(a.dz)[row * a.dzs] = from_f<T>(dot * (w.e * w.g));
-#pragma unroll 1
-        for (int i = 0; i < RUNS; ++i) {
-            const int c = (i * TPR + t) * 8, left = a.cols - c;
-            load(c);
-            float dx[8], dr[8], dz[8];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-                BwdValue v[2];
-                values<T, KEPT, VEC>(a, u, w, k, p, v);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int e = 2 * p + j;
-                    const float ds = fmaf(-c1, v[j].sh, fmaf(w.rstd_s, v[j].t, v[j].ds));
-                    const float dn = ds * v[j].g;
-                    share(0, i, e) = fmaf(v[j].dy, v[j].sh, share(0, i, e));
-                    share(1, i, e) = fmaf(dn, v[j].rh, share(1, i, e));
-                    share(2, i, e) = fmaf(ds, v[j].x, share(2, i, e));
-                    dx[e] = a.alpha ? ds * k.alpha[e] : ds;
-                    dr[e] = w.rstd_r * fmaf(-v[j].rh, c2, dn * k.post[e]);
-                    dz[e] = ds * v[j].p * (v[j].e * v[j].g);
-                }
-            }
-            if (left > 0) {
-                store8<T, VEC>(static_cast<T*>(a.dx) + row * a.dxs + c, left, dx);
-                store8<T, VEC>(static_cast<T*>(a.dr) + row * a.drs + c, left, dr);
-                if (a.gate == kElementGate && a.dz) store8<T, VEC>(static_cast<T*>(a.dz) + row * a.dzs + c, left, dz);
-            }
-        }
-    }
-    if (!a.part) return;
-    float* part = a.part + size_t(blockIdx.x) * 3 * a.cols;
-    for (int k = 0; k < 3; ++k)
-        for (int i = 0; i < RUNS; ++i)
-            for (int j = 0; j < 8; ++j) {
-                const int c = (i * TPR + t) * 8 + j;
-                if (c < a.cols) part[size_t(k) * a.cols + c] = share(k, i, j);
-            }
-}
-
-// ---- up to 4096 columns
 // The copies of a row's operands on their way: every thread copies its own runs into a place of its own and reads them
 // back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.  Through L1, where the
 // two halves of a float32 run's sectors meet (160,000 x 512 float32: 383 against 626 us past it).
@@ -286,6 +123,18 @@ struct RowNumbers {
 
 enum Vector { kPost, kPre, kAlpha };
 
+// ---- a cluster's CTAs
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// v to where p lies in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_there(float* p, int rank, float v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+}
+
 // A block takes every gridDim-th group of rows; a thread keeps the same columns throughout, so its shares of the
 // vectors' gradients stay in its registers and leave once per block, to be added up in a fixed order.
 //
@@ -295,7 +144,11 @@ enum Vector { kPost, kPre, kAlpha };
 // 372; eight columns a thread on two warps, without the ring, 385; five rows in flight instead of two the same.  190 us is
 // 5.6 TB/s, 83% of the copy's rate, and half of the instructions' rate; as stored 200 us (6.5 TB/s), float32 383 us (6.8
 // TB/s), 10,007 x 1000 float16 35 us, whose last two microseconds are the sums' launch.
-template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
+//
+// CL: a row is a cluster's of that many CTAs, 4096 columns each; they tell each other their sums through distributed
+// shared memory, one cluster barrier a row: 10,000 x 8192 bf16 from checkpoints 308 us (3.5 TB/s); one CTA that read such
+// a row twice and kept its shares in shared memory took 506.
+template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
     k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
     RS_PDL_ENTER();
@@ -303,8 +156,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
     constexpr bool VEC = MOVE != kAny, FULL = MOVE == kFull;
     constexpr int kThreads = R::kThreads, kRows = kThreads / TPR, kStages = R::kStages;
     __shared__ float smem[2][kThreads / 32 * 3];
+    __shared__ float cross[2][CL][3];
     extern __shared__ __align__(16) uint8_t ring[];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int rank = CL > 1 ? int(blockIdx.x) % CL : 0, c0 = rank * (TPR * RUNS * 8);
+    const unsigned cluster = blockIdx.x / CL, clusters = gridDim.x / CL;
+    const auto column = [&](int i) { return c0 + (i * TPR + t) * 8; };
     const bool element = a.gate == kElementGate;
     // The vectors, where their loads do not wait: halves of runs apart, so that neighbours hit different banks.
     float4* vectors = reinterpret_cast<float4*>(ring + R::kBytes);
@@ -320,12 +177,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
             for (int i = 0; i < RUNS; ++i) {
                 const float* v = k == kPost ? a.wpost : k == kPre ? a.wpre : a.alpha;
                 float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                if (v) load8<float, VEC>(v + (i * TPR + t) * 8, a.cols - (i * TPR + t) * 8, w);
+                if (v) load8<float, VEC>(v + column(i), a.cols - column(i), w);
                 vectors[(k * 2 * RUNS + i) * TPR + t] = make_float4(w[0], w[1], w[2], w[3]);
                 vectors[(k * 2 * RUNS + RUNS + i) * TPR + t] = make_float4(w[4], w[5], w[6], w[7]);
             }
     }
     __syncthreads();
+    if constexpr (CL > 1) cluster_sync();  // the others' memory is there
     float2 acc[3][RUNS][4];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -333,7 +191,6 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         for (int i = 0; i < RUNS; ++i)
 #pragma unroll
             for (int p = 0; p < 4; ++p) acc[k][i][p] = f2(0.f);
-    const auto column = [&](int i) { return (i * TPR + t) * 8; };
     // of a run: how many of its values exist
     const auto rest = [&](int i) {
         return FULL ? 8 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
@@ -382,13 +239,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    const long long step = (long long)gridDim.x * kRows;
-    const long long first = (long long)blockIdx.x * kRows + sub;
+    const long long step = (long long)clusters * kRows;
+    const long long first = (long long)cluster * kRows + sub;
     RowNumbers<RUNS> now = numbers(first);
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
     int stage = 0, turn = 0;
-    for (long long base = (long long)blockIdx.x * kRows; base < a.rows; base += step) {
+    for (long long base = (long long)cluster * kRows; base < a.rows; base += step) {
         const long long row = base + sub;
         const bool in = row < a.rows;
         const RowNumbers<RUNS> next = numbers(row + step);
@@ -457,10 +314,23 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         }
         float sums[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
         row_sums<TPR>(sums, smem[turn ^= 1]);
+        if constexpr (CL > 1) {
+            if (t < CL)
+#pragma unroll
+                for (int k = 0; k < 3; ++k) store_there(&cross[turn][rank][k], t, sums[k]);
+            __syncwarp();
+            cluster_sync();  // (the row after the next uses this memory again: all have read it by the next one's barrier)
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                sums[k] = cross[turn][0][k];
+#pragma unroll
+                for (int i = 1; i < CL; ++i) sums[k] += cross[turn][i][k];
+            }
+        }
         const float c1 = now.rstd_s * (sums[0] * a.inv_cols);
         const float dot = fmaf(-c1, sums[2], sums[1]);           // sum of ds p
         const float c2 = dot * a.inv_cols;
-        if (a.gate == kRowGate && a.dz && in && t == 0)
+        if (a.gate == kRowGate && a.dz && in && t == 0 && rank == 0)
             static_cast<T*>(a.dz)[row * a.dzs] = from_f<T>(dot * (row_e * row_g));
 #pragma unroll
         for (int i = 0; i < RUNS; ++i) {
@@ -492,7 +362,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         if (++stage == kStages) stage = 0;
     }
     if (!a.part) return;
-    float* part = a.part + size_t(blockIdx.x) * 3 * a.cols;
+    float* part = a.part + size_t(cluster) * 3 * a.cols;
     float2* comb = reinterpret_cast<float2*>(ring);              // no copy is on its way to it: no row is left
     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
@@ -542,53 +412,82 @@ __global__ void __launch_bounds__(1024) k_sandwich_sums(const float* __restrict_
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = s;
 }
 
-// Threads a row; two runs each from 129 to 4096 columns, beyond that the wide form on 512 threads.
+// Threads of a row in a CTA, two runs each from 129 columns on; CTAs of a row.
 int bwd_threads(int cols) {
-    if (cols > 4096) return 512;
     const int runs = ceil_div(cols, 8);
     for (int t = 16; t < 256; t *= 2)
         if (runs <= 2 * t) return t;
     return 256;
 }
-// The most blocks of a call; what it launches depends on types too.
+int bwd_ctas(int cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
+// The most blocks (clusters) of a call, each with a row of partial sums; what is launched depends on types too.
 int bwd_blocks(int rows, int cols) {
     const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1;
-    return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * (t <= 128 ? 3 : 1)));
+    return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * (t <= 128 ? 3 : 1) / bwd_ctas(cols)));
 }
 
+// How many clusters the GPU holds at once (a grid of more would run in two turns).
 template <typename K>
-cudaError_t bwd_launch(K kernel, unsigned grid, int threads, int smem, const SandwichBwdArgs& a, cudaStream_t s) {
-    if (smem > 47 * 1024) {  // with what is static, more than needs no leave
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+int clusters_at_once(K kernel, int cluster, int threads, int smem) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = cluster;
+    cfg.blockDim = threads;
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
+cudaError_t bwd(const SandwichBwdArgs& a, unsigned& parts, cudaStream_t s) {
+    using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
+    const auto kernel = k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS, CL>;
+    if (R::kShared > 47 * 1024) {  // with what is static, more than needs no leave
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, R::kShared);
         if (e != cudaSuccess) return e;
     }
-    return pdl_launch(kernel, grid, threads, smem, s, a);
-}
-
-template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
-cudaError_t bwd(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
-    using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
-    grid = unsigned(std::min(bwd_blocks(a.rows, a.cols), kSms * R::kBlocks));
-    return bwd_launch(k_sandwich_bwd<T, KEPT, MOVE, TPR, RUNS>, grid, R::kThreads, R::kShared, a, s);
-}
-template <typename T, bool KEPT, bool VEC, int RUNS>
-cudaError_t bwd_wide(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
-    grid = unsigned(bwd_blocks(a.rows, a.cols));
-    return bwd_launch(k_sandwich_bwd_wide<T, KEPT, VEC, 512, RUNS>, grid, 512, 3 * RUNS * 8 * 512 * 4, a, s);
+    int most = kSms * R::kBlocks;
+    if constexpr (CL > 1) {
+        static const int at_once = clusters_at_once(kernel, CL, R::kThreads, R::kShared);
+        if (at_once < 1) return cudaErrorInvalidConfiguration;
+        most = at_once;
+    }
+    parts = unsigned(std::min(bwd_blocks(a.rows, a.cols), most));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = parts * CL;
+    cfg.blockDim = R::kThreads;
+    cfg.dynamicSmemBytes = R::kShared;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CL;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CL > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename T, bool KEPT, Move MOVE>
-cudaError_t bwd_width(const SandwichBwdArgs& a, unsigned& grid, cudaStream_t s) {
-    if (a.cols > 8192) return bwd_wide<T, KEPT, MOVE != kAny, 4>(a, grid, s);
-    if (a.cols > 4096) return bwd_wide<T, KEPT, MOVE != kAny, 2>(a, grid, s);
+cudaError_t bwd_width(const SandwichBwdArgs& a, unsigned& parts, cudaStream_t s) {
+    switch (bwd_ctas(a.cols)) {
+        case 2: return bwd<T, KEPT, MOVE, 256, 2, 2>(a, parts, s);
+        case 4: return bwd<T, KEPT, MOVE, 256, 2, 4>(a, parts, s);
+    }
     switch (bwd_threads(a.cols)) {
         case 16:
-            return a.cols <= 128 ? bwd<T, KEPT, MOVE, 16, 1>(a, grid, s) : bwd<T, KEPT, MOVE, 16, 2>(a, grid, s);
-        case 32: return bwd<T, KEPT, MOVE, 32, 2>(a, grid, s);
-        case 64: return bwd<T, KEPT, MOVE, 64, 2>(a, grid, s);
-        case 128: return bwd<T, KEPT, MOVE, 128, 2>(a, grid, s);
+            return a.cols <= 128 ? bwd<T, KEPT, MOVE, 16, 1, 1>(a, parts, s) : bwd<T, KEPT, MOVE, 16, 2, 1>(a, parts, s);
+        case 32: return bwd<T, KEPT, MOVE, 32, 2, 1>(a, parts, s);
+        case 64: return bwd<T, KEPT, MOVE, 64, 2, 1>(a, parts, s);
+        case 128: return bwd<T, KEPT, MOVE, 128, 2, 1>(a, parts, s);
     }
-    return bwd<T, KEPT, MOVE, 256, 2>(a, grid, s);
+    return bwd<T, KEPT, MOVE, 256, 2, 1>(a, parts, s);
 }
 
 }  // namespace
@@ -649,20 +548,20 @@ int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grad
     const SandwichBwdArgs a{args_of(block), grads->d_rstd_r, grads->d_rstd_s, in[0].p, in[0].stride, in[1].p,
                             in[1].stride, out[0].p, out[0].stride, out[1].p, out[1].stride, out[2].p, out[2].stride,
                             any ? static_cast<float*>(d_workspace) : nullptr};
-    unsigned grid = 0;
+    unsigned parts = 0;
     cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
         // nothing asked, as in the forward, pays from checkpoints alone (160,000 x 512: 190 us, 196 asking; as stored 214
         // and 206)
         if (kept) {
-            if (!vec) return bwd_width<T, true, kAny>(a, grid, s);
-            return full_width(cols) ? bwd_width<T, true, kFull>(a, grid, s) : bwd_width<T, true, kRuns>(a, grid, s);
+            if (!vec) return bwd_width<T, true, kAny>(a, parts, s);
+            return full_width(cols) ? bwd_width<T, true, kFull>(a, parts, s) : bwd_width<T, true, kRuns>(a, parts, s);
         }
-        return vec ? bwd_width<T, false, kRuns>(a, grid, s) : bwd_width<T, false, kAny>(a, grid, s);
+        return vec ? bwd_width<T, false, kRuns>(a, parts, s) : bwd_width<T, false, kAny>(a, parts, s);
     });
     if (e == cudaSuccess && any)
         e = pdl_launch(k_sandwich_sums, dim3(ceil_div(cols, 32), 3), 1024, 0, s, static_cast<const float*>(a.part),
-                       int(grid), cols, Vectors{{vectors[0], vectors[1], vectors[2]}});
+                       int(parts), cols, Vectors{{vectors[0], vectors[1], vectors[2]}});
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
 

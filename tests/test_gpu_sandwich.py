@@ -203,7 +203,7 @@ def keep(b, o):
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
 @pytest.mark.parametrize("gate", ["none", "row", "element"])
-@pytest.mark.parametrize("rows,cols", SIZES + [(4001, 129), (1700, 512), (3000, 1000), (700, 2048), (400, 4096), (200, 16384)])
+@pytest.mark.parametrize("rows,cols", SIZES + [(4001, 129), (1700, 512), (3000, 1000), (700, 2048), (400, 4096), (200, 16384), (400, 8200), (50, 12288)])
 def test_backward(dt, gate, rows, cols):
     g = gen(rows * 7 + cols)
     for kept in (False, True):
