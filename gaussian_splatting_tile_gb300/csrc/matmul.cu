@@ -21,9 +21,9 @@
 //
 // An 8-bit result: with 256 columns a tile a reader holds a row's 128 sums of one block, so it settles the block's scale
 // by itself, and a pass out is 128 bytes a row.  160,000 x 512 x 512 58 us (a float32 result and its 8-bit form: 181),
-// bound as above: of the 25 that memory and products need each, the readers' way round leaves 43%.  Results by plain
-// stores instead of TMA and the fence before it 66; loads of 32 columns from tensor memory, which do not fit the registers,
-// 69.
+// bound by the readers: 40 for adding the blocks up, as above, and 18 for the way out, most of it the conversions (memory
+// and products need 25 each).  Results by plain stores instead of TMA and the fence before it 66; loads of 32 columns
+// from tensor memory, which do not fit the registers, 69.
 #include <cuda.h>
 
 #include <cfloat>

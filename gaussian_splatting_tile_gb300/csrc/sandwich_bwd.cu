@@ -170,20 +170,6 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
         w[0] = make_float2(lo.x, lo.y), w[1] = make_float2(lo.z, lo.w);
         w[2] = make_float2(hi.x, hi.y), w[3] = make_float2(hi.z, hi.w);
     };
-    if (sub == 0) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-#pragma unroll
-            for (int i = 0; i < RUNS; ++i) {
-                const float* v = k == kPost ? a.wpost : k == kPre ? a.wpre : a.alpha;
-                float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                if (v) load8<float, VEC>(v + column(i), a.cols - column(i), w);
-                vectors[(k * 2 * RUNS + i) * TPR + t] = make_float4(w[0], w[1], w[2], w[3]);
-                vectors[(k * 2 * RUNS + RUNS + i) * TPR + t] = make_float4(w[4], w[5], w[6], w[7]);
-            }
-    }
-    __syncthreads();
-    if constexpr (CL > 1) cluster_sync();  // the others' memory is there
     float2 acc[3][RUNS][4];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
@@ -244,6 +230,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
     RowNumbers<RUNS> now = numbers(first);
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) fetch(first + s * step, s);
+    if (sub == 0) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i) {
+                const float* v = k == kPost ? a.wpost : k == kPre ? a.wpre : a.alpha;
+                float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+                if (v) load8<float, VEC>(v + column(i), a.cols - column(i), w);
+                vectors[(k * 2 * RUNS + i) * TPR + t] = make_float4(w[0], w[1], w[2], w[3]);
+                vectors[(k * 2 * RUNS + RUNS + i) * TPR + t] = make_float4(w[4], w[5], w[6], w[7]);
+            }
+    }
+    __syncthreads();
+    if constexpr (CL > 1) cluster_sync();  // the others' memory is there
     int stage = 0, turn = 0;
     for (long long base = (long long)cluster * kRows; base < a.rows; base += step) {
         const long long row = base + sub;
