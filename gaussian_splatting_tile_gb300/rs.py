@@ -223,9 +223,13 @@ def _check(fn: str, code: int):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
+# the current device without a look at whether CUDA has been set up, which whoever has a CUDA tensor has seen to
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream):
     if stream is None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return stream.cuda_stream
 
 
@@ -747,14 +751,22 @@ def _dtype(t, name="tensor") -> int:
     return code
 
 
+_Tensor, _F32 = torch.Tensor, torch.float32
+
+
 def _mat(t, name, dtype, shape):
     """(pointer, row stride in elements) of a row-major CUDA matrix of `shape` (rows, columns); its rows may be apart."""
     if t is None:
         return None, 0
-    # the common case in one line: these checks are most of a small call's time
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        # a single row's stride is never followed: give one that the alignment rules allow
-        return t.data_ptr(), (shape[1] if shape[0] > 1 else (shape[1] + 15) // 16 * 16)
+    # the common cases in a few lines: these checks are most of a small call's time
+    if type(t) is _Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape:
+        rows, cols = shape
+        if t.is_contiguous():
+            # a single row's stride is never followed: give one that the alignment rules allow
+            return t.data_ptr(), (cols if rows > 1 else (cols + 15) // 16 * 16)
+        s0, s1 = t.stride()
+        if s1 == 1 and rows > 1:
+            return t.data_ptr(), s0
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype is not dtype and not (dtype is _FP8 and t.dtype is torch.uint8):
@@ -772,7 +784,7 @@ def _vec(t, dtype, numel: int, name: str):
     """Pointer of a contiguous CUDA tensor of at least `numel` elements."""
     if t is None:
         return None
-    if type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
+    if type(t) is _Tensor and t.is_cuda and t.dtype is dtype and t.is_contiguous() and t.numel() >= numel:
         return t.data_ptr()
     return _ptr(t, dtype, numel, name).value  # says what is wrong
 
@@ -792,6 +804,8 @@ def fp8_dequantize(q: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
 
 
 def _scales(t, name, blocks: int, rows: int):
+    if type(t) is _Tensor and t.is_cuda and t.dtype is _F32 and t.shape == (blocks, rows) and t.is_contiguous():
+        return t.data_ptr()
     if t is not None and t.shape != (blocks, rows):
         raise ValueError(f"{name} is {tuple(t.shape)}, needs {(blocks, rows)}")
     return _vec(t, torch.float32, 0, name)
