@@ -374,7 +374,7 @@ class WideAppearance:
         self.colors = torch.empty(3, n, dtype=torch.float32, device=dev)
         sizes = [(n, hidden, c), (n, c, hidden), (n, 3, c), (n, c, 3), (hidden, c, n), (c, hidden, n), (3, c, n)]
         if gate:
-            sizes += [(n, gates, c), (n, c, gates), (gates, c, n)]
+            sizes += [(n, gates, c), (n, c, gates), (gates, c, n), (c, gates, n)]
         need = max([rs.rs_matmul_fp8_workspace_size(*s) for s in sizes] +
                    [rs.rs_rms_norm_bwd_workspace_size(n, c), rs.rs_grad_norm_workspace_size(rs.RS_ADAM_MAX_SEGMENTS)])
         if checkpoints:
@@ -497,7 +497,11 @@ class WideAppearance:
                     undo(self.qgt[1])
                     self._product(self.qg, self.gates[b].qt, self.gates[b].st, self.dr)
                     self.dy.add_(self.dr)
-                    self._product(self.qgt, *self.qct, self.gates[b].dw)  # qct still holds the norm's output by columns
+                    dw = self.gates[b].dw  # qct still holds the norm's output by columns
+                    if dw.shape[0] == 1:  # as a column of many rows: one row's long contraction would run on few SMs
+                        self._product(self.qct, *self.qgt, dw.view(-1, 1))
+                    else:
+                        self._product(self.qgt, *self.qct, dw)
                 if not self.sandwich:
                     self._norm_backward(b, self.h[b], self.dh, undo)
             if self.sandwich:
