@@ -4,8 +4,9 @@ formulas, through the C ABI.
 Tolerances, with u = 2^-24 (float32's half ulp) and h = the half ulp of the stored type (2^-24, 2^-11, 2^-8):
  - a float32 sum in which no chain of additions is longer than L is within L u of its terms' magnitudes; a row's chains are at
    most 32 values a thread, 5 shuffles and 16 warps: 64 u covers them, 40 u the reciprocal root of such a sum of squares;
- - a gate's e = exp(-z) is off by at most (2 + 1.2 |z|) ulp (CUDA's bound for __expf), 2 (2 + 1.2 |z|) u; the quotient 1 / (1 + e)
-   by 2 ulp and the sum's rounding: (9 + 2.4 |z|) u of g, and twice that and a product for g e = 1 - g;
+ - a gate's e = 2^(-z log2 e): the constant and the product move the exponent by at most 1.5 |z| log2(e) u, so e by 1.5 |z| u,
+   and the power of two (PTX: within 2^-22.5) by 3 u; the reciprocal of 1 + e is off by an ulp, 2 u, and the sum's rounding:
+   less than (9 + 2.4 |z|) u of g, and of g e = 1 - g, where e counts twice, than (13 + 5 |z|) u;
  - what follows is each formula's operations, one u each, with the errors of what they take.
 Functions below carry a value and the bound on its error side by side."""
 import math
