@@ -37,7 +37,8 @@ struct Ring {
     static constexpr int kBytes = kStages * kStage;
     static constexpr int kVectors = 3 * RUNS * TPR * 32;                       // behind the ring
     static constexpr int kShared = kBytes + kVectors;                          // what a block is launched with
-    static_assert(kShared >= kThreads * 32 && kShared <= 226 * 1024, "room to join the rows' sums, and for the block");
+    static_assert((kThreads == TPR || kBytes >= 12 * RUNS * kThreads * 8) && kShared <= 226 * 1024,
+                  "room to join the rows' shares in the ring, and for the block");
     static constexpr int kBlocks = kThreads > 128 ? 1 : RUNS == 1 ? 3 : 2;   // an SM: registers
     static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int run) {
         return ring + stage * kStage + (run * kThreads + int(threadIdx.x)) * 8;
@@ -363,33 +364,40 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TP
     }
     if (!a.part) return;
     float* part = a.part + size_t(cluster) * 3 * a.cols;
-    float2* comb = reinterpret_cast<float2*>(ring);              // no copy is on its way to it: no row is left
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    const auto leave = [&](int k, int i, int p, float2 v) {
+        const int c = column(i) + 2 * p;
+        if (c < a.cols) part[size_t(k) * a.cols + c] = v.x;
+        if (c + 1 < a.cols) part[size_t(k) * a.cols + c + 1] = v.y;
+    };
+    if constexpr (kRows == 1) {
 #pragma unroll
-    for (int k = 0; k < 3; ++k)
+        for (int k = 0; k < 3; ++k)
 #pragma unroll
-        for (int i = 0; i < RUNS; ++i) {
-            if constexpr (kRows > 1) {
-                __syncthreads();
+            for (int i = 0; i < RUNS; ++i)
 #pragma unroll
-                for (int p = 0; p < 4; ++p) comb[p * kThreads + threadIdx.x] = acc[k][i][p];
-                __syncthreads();
-                if (sub == 0)
+                for (int p = 0; p < 4; ++p) leave(k, i, p, acc[k][i][p]);
+    } else {  // the rows' threads join their shares, each some of them
+        float2* comb = reinterpret_cast<float2*>(ring);  // no copy is on its way to it: no row is left
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
 #pragma unroll
-                    for (int p = 0; p < 4; ++p)
-                        for (int o = 1; o < kRows; ++o) {
-                            const float2 v = comb[p * kThreads + o * TPR + t];
-                            acc[k][i][p] = make_float2(acc[k][i][p].x + v.x, acc[k][i][p].y + v.y);
-                        }
+        for (int k = 0; k < 3; ++k)
+#pragma unroll
+            for (int i = 0; i < RUNS; ++i)
+#pragma unroll
+                for (int p = 0; p < 4; ++p) comb[((k * RUNS + i) * 4 + p) * kThreads + threadIdx.x] = acc[k][i][p];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 12 * RUNS; ++n) {
+            if (n % kRows != sub) continue;
+            float2 v = comb[n * kThreads + t];
+            for (int o = 1; o < kRows; ++o) {
+                const float2 w = comb[n * kThreads + o * TPR + t];
+                v = make_float2(v.x + w.x, v.y + w.y);
             }
-            if (sub == 0)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    const int c = column(i) + 2 * p;
-                    if (c < a.cols) part[size_t(k) * a.cols + c] = acc[k][i][p].x;
-                    if (c + 1 < a.cols) part[size_t(k) * a.cols + c + 1] = acc[k][i][p].y;
-                }
+            leave(n / (4 * RUNS), n / 4 % RUNS, n % 4, v);
         }
+    }
 }
 
 struct Vectors { float* out[3]; };
