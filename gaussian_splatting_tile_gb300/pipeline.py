@@ -309,7 +309,8 @@ class WideAppearance:
 
     checkpoints: what the forward keeps for the backward is kept in 8 bits: the norms' and relus' outputs, which the
     products read in that form anyway, and a sandwich block's operands, from which its backward then starts (a block of the
-    plain kind keeps its residual stream in `dtype`).  The forward's colours are the same."""
+    plain kind keeps its residual stream in `dtype`).  The colours stay the same with float32 activations; in 16 bits the
+    hidden layer's are no longer rounded to those before they are to 8."""
 
     def __init__(self, features: torch.Tensor, hidden: int, blocks: int = 2, dtype=torch.bfloat16, seed: int = 0,
                  sandwich: bool = False, gate: str | None = None, checkpoints: bool = False):
