@@ -6,7 +6,7 @@
 //
 // Measured: 160,000 x 512 bf16 both forms 60 us (5.4 TB/s), through a relu 85 us (5.8 TB/s), float32 5.9 TB/s; 128 x 128
 // forms both ways round of 8192 x 8192 float32 68 us (5.9 TB/s), bf16 51 us (5.2 TB/s), of 2048 x 2048 10 us, the launch.
-// Through a relu kept in 8 bits 160,000 x 512 bf16 67 us (6.1 TB/s); 80,000 x 1001, rows between words, 133 us (3.1 TB/s).
+// Through a relu kept in 8 bits 160,000 x 512 bf16 67 us (6.1 TB/s); 80,000 x 1001, rows between words, 120 us (3.4 TB/s).
 #include "wide.cuh"
 
 namespace rs {

@@ -137,20 +137,23 @@ struct PackedRun8 {
             w = make_uint4(h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16);
         }
     }
-    // The same at any even address, without a way of its own for a row's first and last run: every aligned word that
-    // holds one of the values is read whole, with the value before or after it.
+    // The same at any even address, without a way of its own for a row's first run: where that starts in the middle of a
+    // word, the value before it is read with it.  Nothing behind the row is.
     __device__ __forceinline__ void load_words(const T* p, int left) {
         const uint32_t* q = reinterpret_cast<const uint32_t*>(reinterpret_cast<uintptr_t>(p) & ~uintptr_t(3));
-        const int off = int(reinterpret_cast<uintptr_t>(p) & 2), end = off + 2 * min(left, 8);
+        const auto half = [&](int i) { return uint32_t(*reinterpret_cast<const uint16_t*>(q + i)); };
+        const int off = int(reinterpret_cast<uintptr_t>(p) & 2), end = left > 0 ? off + 2 * min(left, 8) : 0;
         uint32_t r[5];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) r[i] = left > 0 && 4 * i < end ? q[i] : 0u;
+        for (int i = 0; i < 4; ++i) r[i] = 4 * i + 4 <= end ? q[i] : 0u;
+        r[4] = end == 18 ? half(4) : 0u;
+        if (end < 16 && end & 2) {  // the row ends in the middle of a word
+            const uint32_t last = half(end >> 2);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[i] = i == end >> 2 ? last : r[i];
+        }
         w = make_uint4(__funnelshift_r(r[0], r[1], 8 * off), __funnelshift_r(r[1], r[2], 8 * off),
                        __funnelshift_r(r[2], r[3], 8 * off), __funnelshift_r(r[3], r[4], 8 * off));
-        if (left < 8) {
-            const auto keep = [&](uint32_t x, int i) { return left > i + 1 ? x : left > i ? x & 0xffffu : 0u; };
-            w = make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
-        }
     }
     static __device__ __forceinline__ uint32_t kept(uint32_t x, uint32_t u) {
         return x & ~__hle2_mask(*reinterpret_cast<const T2*>(&u), T2{T(0.f), T(0.f)});

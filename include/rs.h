@@ -549,8 +549,8 @@ typedef struct rs_fp8_matrix {
  *
  * x, r and an element's gate are matrices of `dtype`, or (in the backward alone) the 8-bit forms
  * that the forward kept: then d_x_scales, d_r_scales and, for an element's gate, d_gate_scales are
- * their scales; all of them or none.  A gate a row is always of `dtype`.  (16-bit rows that do not
- * start on words are read in whole words: the value before a row and the one after it too.)
+ * their scales; all of them or none.  A gate a row is always of `dtype`.  (Where a 16-bit
+ * row starts in the middle of a word, the value before it is read with it.)
  * 1 <= cols <= RS_NORM_MAX_COLS; rows = 0 is valid. */
 typedef struct rs_sandwich {
     int32_t rows, cols;
@@ -630,8 +630,8 @@ int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grad
 /* rs_quantize_fp8 through a relu whose output was kept in 8 bits: d_relu [rows][cols] are e4m3 bytes
  * (rows on 16-byte boundaries); x counts as zero where they hold a value <= 0.  (A positive value
  * that was rounded to zero when it was kept counts as zero here too, as it did in the products that
- * read it.)  Scales do not matter and are not asked for.  16-bit rows of x that do not start on words
- * are read in whole words. */
+ * read it.)  Scales do not matter and are not asked for.  Where a 16-bit row of x starts in the
+ * middle of a word, the value before it is read with it. */
 int rs_quantize_fp8_relu8(int32_t rows, int32_t cols, int32_t dtype, const void* d_x, size_t x_stride,
                           const uint8_t* d_relu, size_t relu_stride, uint8_t* d_q, size_t q_stride,
                           float* d_scales, uint8_t* d_qt, size_t qt_stride, float* d_scales_t, void* stream);
