@@ -182,20 +182,33 @@ cudaError_t fwd(const SandwichFwdArgs& a, cudaStream_t s) {
     return pdl_launch(k_sandwich_fwd<T, MOVE, TPR, RUNS>, ceil_div(a.rows, kRows), TPR < 128 ? 128 : TPR, 0, s, a);
 }
 
-// Two runs a thread from 129 columns on, on as few threads as they fit (512 columns on 64 threads with one run each: 384
-// against 243 us, with the arithmetic one by one).  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
-template <typename T, Move MOVE>
-cudaError_t fwd_width(const SandwichFwdArgs& a, cudaStream_t s) {
-    const int runs = ceil_div(a.cols, 8);
-    if (runs <= 16) return fwd<T, MOVE, 16, 1>(a, s);
-    if (runs <= 32) return fwd<T, MOVE, 16, 2>(a, s);
-    if (runs <= 64) return fwd<T, MOVE, 32, 2>(a, s);
-    if (runs <= 128) return fwd<T, MOVE, 64, 2>(a, s);
-    if (runs <= 256) return fwd<T, MOVE, 128, 2>(a, s);
-    if (runs <= 512) return fwd<T, MOVE, 256, 2>(a, s);
-    if (runs <= 1024) return fwd<T, MOVE, 512, 2>(a, s);
-    return fwd<T, MOVE, 512, 4>(a, s);
+template <typename T, int TPR, int RUNS>
+cudaError_t fwd_moved(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
+    if (!vec) return fwd<T, kAny, TPR, RUNS>(a, s);
+    return a.cols == 8 * TPR * RUNS ? fwd<T, kFull, TPR, RUNS>(a, s) : fwd<T, kRuns, TPR, RUNS>(a, s);
 }
+
+// Two or three runs a thread from 129 columns on, on as few threads as they fit (512 columns on 64 threads with one run
+// each: 384 against 243 us, with the arithmetic one by one; 100,000 x 768 bf16 on 32 threads with three 151 us, on 64 with
+// two, of which a quarter are idle, 217).  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
+template <typename T>
+cudaError_t fwd_width(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
+    const int runs = ceil_div(a.cols, 8);
+    if (runs <= 16) return fwd_moved<T, 16, 1>(a, vec, s);
+    if (runs <= 32) return fwd_moved<T, 16, 2>(a, vec, s);
+    if (runs <= 48) return fwd_moved<T, 16, 3>(a, vec, s);
+    if (runs <= 64) return fwd_moved<T, 32, 2>(a, vec, s);
+    if (runs <= 96) return fwd_moved<T, 32, 3>(a, vec, s);
+    if (runs <= 128) return fwd_moved<T, 64, 2>(a, vec, s);
+    if (runs <= 192) return fwd_moved<T, 64, 3>(a, vec, s);
+    if (runs <= 256) return fwd_moved<T, 128, 2>(a, vec, s);
+    if (runs <= 384) return fwd_moved<T, 128, 3>(a, vec, s);
+    if (runs <= 512) return fwd_moved<T, 256, 2>(a, vec, s);
+    if (runs <= 768) return fwd_moved<T, 256, 3>(a, vec, s);
+    if (runs <= 1024) return fwd_moved<T, 512, 2>(a, vec, s);
+    return fwd_moved<T, 512, 4>(a, vec, s);
+}
+
 }  // namespace
 }  // namespace rs
 
@@ -232,8 +245,7 @@ int rs_sandwich_norm_fwd(const rs_sandwich* block, float eps, const rs_sandwich_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = with_dtype(dtype, [&](auto v) {
         using T = decltype(v);
-        if (!vec) return fwd_width<T, kAny>(a, s);
-        return full_width(cols) ? fwd_width<T, kFull>(a, s) : fwd_width<T, kRuns>(a, s);
+        return fwd_width<T>(a, vec, s);
     });
     return e == cudaSuccess ? RS_OK : RS_ERR_CUDA;
 }
