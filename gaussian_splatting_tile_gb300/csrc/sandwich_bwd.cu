@@ -27,7 +27,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 struct Ring {
     static constexpr bool kWhole = MOVE != kAny;                               // runs on 16-byte boundaries
-    static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+    static constexpr int kThreads = block_threads(TPR);
     static constexpr int kGroup = TPR < 32 ? TPR : 32, kGroups = kThreads / kGroup;
     static constexpr int kWords = kWhole ? int(sizeof(T)) / 2 : 2 * int(sizeof(T));  // a thread's: of 16 bytes, or of 4
     static constexpr int kGroupBytes = kGroup * (kWhole ? 16 : 4) * kWords + (kWhole || sizeof(T) == 4 ? 0 : 16);
@@ -39,7 +39,7 @@ struct Ring {
     static constexpr int kShared = kBytes + kVectors;                          // what a block is launched with
     static_assert((kThreads == TPR || kBytes >= 12 * RUNS * kThreads * 8) && kShared <= 226 * 1024,
                   "room to join the rows' shares in the ring, and for the block");
-    static constexpr int kBlocks = kThreads > 128 ? 1 : RUNS == 1 ? 3 : 2;   // an SM: registers
+    static constexpr int kBlocks = RUNS == 1 ? 384 / kThreads : kThreads > 128 ? 1 : 2;   // an SM: registers
     static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int run) {
         return ring + stage * kStage + (run * kThreads + int(threadIdx.x)) * 8;
     }
@@ -51,8 +51,8 @@ struct Ring {
 };
 
 // One run of a matrix of T on its way into the ring.  p: where this thread's run starts; left: how many of its values
-// exist, not above zero where none does.  Of 16-bit rows the words at their ends are read whole: with the value before
-// the row.
+// exist, not above zero where none does.  Where a 16-bit row starts in the middle of a word, the value before it is read
+// with it.
 template <typename R, typename T>
 __device__ __forceinline__ void send(uint8_t* ring, int stage, int run, const T* p, int left) {
     uint8_t* to = R::wide(ring, stage, run);
@@ -150,7 +150,7 @@ __device__ __forceinline__ void store_there(float* p, int rank, float v) {
 // shared memory, one cluster barrier a row: 10,000 x 8192 bf16 from checkpoints 308 us (3.5 TB/s); one CTA that read such
 // a row twice and kept its shares in shared memory took 506.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
+__global__ void __launch_bounds__(block_threads(TPR), (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
     k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
     RS_PDL_ENTER();
     using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
@@ -420,18 +420,32 @@ __global__ void __launch_bounds__(1024) k_sandwich_sums(const float* __restrict_
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = s;
 }
 
-// Threads of a row in a CTA, two runs each from 129 columns on; CTAs of a row.
-int bwd_threads(int cols) {
+// Threads of a row in a CTA and runs of each; CTAs of a row.  Two runs a thread; in 16 bits, for widths that would leave
+// a quarter of those idle or more, one run on three quarters of the threads instead (100,000 x 768 bf16 from checkpoints
+// on 96 threads 194 us, on 64 with two runs 237; float32 as stored 456, 362 with two).
+struct Shape { int threads, runs; };
+Shape bwd_shape(int cols, bool f32) {
     const int runs = ceil_div(cols, 8);
-    for (int t = 16; t < 256; t *= 2)
-        if (runs <= 2 * t) return t;
-    return 256;
+    if (runs <= 16) return {16, 1};
+    if (runs <= 32) return {16, 2};
+    if (runs <= 64) return {32, 2};
+    if (runs <= 96 && !f32) return {96, 1};
+    if (runs <= 128) return {64, 2};
+    if (runs <= 192 && !f32) return {192, 1};
+    if (runs <= 256) return {128, 2};
+    if (runs <= 384 && !f32) return {384, 1};
+    return {256, 2};
 }
 int bwd_ctas(int cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
-// The most blocks (clusters) of a call, each with a row of partial sums; what is launched depends on types too.
+// The most blocks (clusters) of a call, each with a row of partial sums, whatever its type.
 int bwd_blocks(int rows, int cols) {
-    const int t = bwd_threads(cols), rows_a_block = t < 128 ? 128 / t : 1;
-    return std::max(1, std::min(ceil_div(rows, rows_a_block), kSms * (t <= 128 ? 3 : 1) / bwd_ctas(cols)));
+    int most = 1;
+    for (const bool f32 : {false, true}) {
+        const Shape p = bwd_shape(cols, f32);
+        const int threads = block_threads(p.threads), per = p.runs == 1 ? 384 / threads : threads > 128 ? 1 : 2;
+        most = std::max(most, std::min(ceil_div(rows, threads / p.threads), kSms * per / bwd_ctas(cols)));
+    }
+    return most;
 }
 
 // How many clusters the GPU holds at once (a grid of more would run in two turns).
@@ -463,9 +477,9 @@ cudaError_t bwd(const SandwichBwdArgs& a, unsigned& parts, cudaStream_t s) {
     if constexpr (CL > 1) {
         static const int at_once = clusters_at_once(kernel, CL, R::kThreads, R::kShared);
         if (at_once < 1) return cudaErrorInvalidConfiguration;
-        most = at_once;
+        most = std::min(at_once, kSms / CL);
     }
-    parts = unsigned(std::min(bwd_blocks(a.rows, a.cols), most));
+    parts = unsigned(std::min(ceil_div(a.rows, R::kThreads / TPR), most));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = parts * CL;
     cfg.blockDim = R::kThreads;
@@ -488,9 +502,16 @@ cudaError_t bwd_width(const SandwichBwdArgs& a, unsigned& parts, cudaStream_t s)
         case 2: return bwd<T, KEPT, MOVE, 256, 2, 2>(a, parts, s);
         case 4: return bwd<T, KEPT, MOVE, 256, 2, 4>(a, parts, s);
     }
-    switch (bwd_threads(a.cols)) {
-        case 16:
-            return a.cols <= 128 ? bwd<T, KEPT, MOVE, 16, 1, 1>(a, parts, s) : bwd<T, KEPT, MOVE, 16, 2, 1>(a, parts, s);
+    const Shape p = bwd_shape(a.cols, sizeof(T) == 4);
+    if constexpr (sizeof(T) == 2) {
+        switch (p.threads) {
+            case 96: return bwd<T, KEPT, MOVE, 96, 1, 1>(a, parts, s);
+            case 192: return bwd<T, KEPT, MOVE, 192, 1, 1>(a, parts, s);
+            case 384: return bwd<T, KEPT, MOVE, 384, 1, 1>(a, parts, s);
+        }
+    }
+    switch (p.threads) {
+        case 16: return p.runs == 1 ? bwd<T, KEPT, MOVE, 16, 1, 1>(a, parts, s) : bwd<T, KEPT, MOVE, 16, 2, 1>(a, parts, s);
         case 32: return bwd<T, KEPT, MOVE, 32, 2, 1>(a, parts, s);
         case 64: return bwd<T, KEPT, MOVE, 64, 2, 1>(a, parts, s);
         case 128: return bwd<T, KEPT, MOVE, 128, 2, 1>(a, parts, s);
@@ -563,7 +584,9 @@ int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grad
         // and 206)
         if (kept) {
             if (!vec) return bwd_width<T, true, kAny>(a, parts, s);
-            return full_width(cols) ? bwd_width<T, true, kFull>(a, parts, s) : bwd_width<T, true, kRuns>(a, parts, s);
+            const Shape p = bwd_shape(cols, dtype == RS_F32);
+            return cols == 8 * p.threads * p.runs * bwd_ctas(cols) ? bwd_width<T, true, kFull>(a, parts, s)
+                                                                   : bwd_width<T, true, kRuns>(a, parts, s);
         }
         return vec ? bwd_width<T, false, kRuns>(a, parts, s) : bwd_width<T, false, kAny>(a, parts, s);
     });

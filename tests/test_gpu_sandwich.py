@@ -24,7 +24,8 @@ DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
 HALF_ULP = {"f32": U, "f16": 2.0 ** -11, "bf16": 2.0 ** -8}
 TINY = {"f32": 2.0 ** -126, "f16": 2.0 ** -24, "bf16": 2.0 ** -126}      # half of a subnormal step, or what is flushed
 SIZES = [(1, 1), (3, 7), (130, 64), (5, 127), (9, 128), (33, 129), (1, 256), (70, 257), (17, 512), (5, 777), (300, 1000),
-         (2, 1025), (9, 2048), (3, 2050), (4, 4096), (3, 4104), (2, 8192), (3, 8193), (2, 16384)]
+         (2, 1025), (9, 2048), (3, 2050), (4, 4096), (3, 4104), (2, 8192), (3, 8193), (2, 16384), (41, 384), (37, 600),
+         (37, 601), (700, 768), (9, 1203), (400, 1536), (4, 2601), (300, 3000)]
 
 
 @pytest.fixture(scope="module", autouse=True)
