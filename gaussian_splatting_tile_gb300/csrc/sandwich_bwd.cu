@@ -51,14 +51,13 @@ struct Ring {
 };
 
 // One run of a matrix of T on its way into the ring.  p: where this thread's run starts; left: how many of its values
-// exist, not above zero where none does.  Where a 16-bit row starts in the middle of a word, the value before it is read
+// exist, not above zero where none does (whole runs are sent where they exist alone).  Where a 16-bit row starts in the middle of a word, the value before it is read
 // with it.
 template <typename R, typename T>
 __device__ __forceinline__ void send(uint8_t* ring, int stage, int run, const T* p, int left) {
     uint8_t* to = R::wide(ring, stage, run);
     const int l = R::lane();
     if constexpr (R::kWhole) {
-        if (left <= 0) return;
 #pragma unroll
         for (int i = 0; i < R::kWords; ++i) copy_async<16>(to + (i * R::kGroup + l) * 16, p + i * (16 / sizeof(T)));
     } else {
@@ -178,10 +177,10 @@ __global__ void __launch_bounds__(block_threads(TPR), (Ring<T, KEPT, MOVE, TPR, 
         for (int i = 0; i < RUNS; ++i)
 #pragma unroll
             for (int p = 0; p < 4; ++p) acc[k][i][p] = f2(0.f);
-    // of a run: how many of its values exist
-    const auto rest = [&](int i) {
-        return FULL ? 8 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
-    };
+    // Of a run: how many of its values exist.  Widths are given to threads so that only the last run may lack some, but in a
+    // cluster any.
+    const auto left_of = [&](int i) { return MOVE == kAny ? a.cols - column(i) : column(i) < a.cols ? 8 : 0; };
+    const auto rest = [&](int i) { return FULL || (CL == 1 && i + 1 < RUNS) ? 8 : left_of(i); };
     const auto numbers = [&](long long row) {
         RowNumbers<RUNS> n{};
         if (row >= a.rows) return n;
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(block_threads(TPR), (Ring<T, KEPT, MOVE, TPR, 
                 copy_async<8>(R::narrow(ring, stage, k * RUNS + i),
                               static_cast<const uint8_t*>(s.p) + row * s.stride + column(i), min(rest(i), 8));
         } else {
-            send<R>(ring, stage, (2 + k) * RUNS + i, run_of(s.p, s.stride, row, i), rest(i));
+            send<R>(ring, stage, (2 + k) * RUNS + i, run_of(s.p, s.stride, row, i), left_of(i));
         }
     };
     const auto fetch = [&](long long row, int stage) {
@@ -220,8 +219,8 @@ __global__ void __launch_bounds__(block_threads(TPR), (Ring<T, KEPT, MOVE, TPR, 
                 operand(a.x, row, stage, 0, i);
                 operand(a.r, row, stage, 1, i);
                 if (element) operand(a.z, row, stage, 2, i);
-                send<R>(ring, stage, i, run_of(a.dy, a.dys, row, i), rest(i));
-                if (a.ds) send<R>(ring, stage, RUNS + i, run_of(a.ds, a.dss, row, i), rest(i));
+                send<R>(ring, stage, i, run_of(a.dy, a.dys, row, i), left_of(i));
+                if (a.ds) send<R>(ring, stage, RUNS + i, run_of(a.ds, a.dss, row, i), left_of(i));
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");

@@ -38,7 +38,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int left, const float2 (&
 // in pairs; two operands' or three operands' maxima travel together.  That took 250,000 x 512 bf16, gated, operands kept,
 // from 384 us (103 instructions a value) to 243 (60; 6.4 TB/s, 94% of the copy's rate).  float32 160,000 x 512 233 us
 // (7.1 TB/s); 80,000 x 1000 bf16 194 us (5.0 TB/s: three of a row's 128 runs are empty, and rows of two warps wait for each
-// other); 80,000 x 1001, between words, 257 us.  One row costs the call, 10 us.
+// other); 80,000 x 1001, between words, 247 us.  One row costs the call, 10 us.
 template <typename T, Move MOVE, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __grid_constant__ SandwichFwdArgs a) {
     RS_PDL_ENTER();
@@ -54,9 +54,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
     const T* r = static_cast<const T*>(a.r.p) + at * a.r.stride;
     const T* z = a.gate ? static_cast<const T*>(a.z.p) + at * a.z.stride : nullptr;
     const auto column = [&](int i) { return (i * TPR + t) * 8; };
-    // of a run: how many of its values exist
+    // Of a run: how many of its values exist.  Widths are given to threads so that only the last runs may lack some (with
+    // four, the last two); threads without a row take the first one's, and store nothing.
+    const auto whole = [&](int i) { return FULL || (RUNS < 4 && i + 1 < RUNS); };
     const auto rest = [&](int i) {
-        return FULL ? 8 : !in ? 0 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
+        return whole(i) ? 8 : !in ? 0 : MOVE == kRuns ? (column(i) < a.cols ? 8 : 0) : a.cols - column(i);
     };
     Run8<T> xv[RUNS], rv[RUNS], zv[RUNS];
     const auto load = [&](Run8<T>& v, const T* p, int i) {
@@ -101,7 +103,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
                 constexpr int kEach = 16 / kKept;
                 const int c = column(i), first = (3 * i + k) * kEach;
                 const float by = __shfl_sync(0xffffffffu, inv, first, 16);
-                if (of == first && in && (FULL || c - of * 8 < a.cols))
+                if (of == first && in && (whole(i) || c - of * 8 < a.cols))
                     f.scales[size_t(c / kBlock) * a.rows + row] = scale;
                 const float2 w[4] = {v[i].pair(0), v[i].pair(1), v[i].pair(2), v[i].pair(3)};
                 if (in && rest(i) > 0) store_e4m3(f.q + row * f.stride + c, rest(i), w, by);
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
         constexpr int kEach = 16 / kForms;
         const int c = column(i);
         const float by = __shfl_sync(0xffffffffu, inv, i * kEach, 16);
-        if (of == i * kEach && in && (FULL || c - of * 8 < a.cols)) a.q.scales[size_t(c / kBlock) * a.rows + row] = scale;
+        if (of == i * kEach && in && (whole(i) || c - of * 8 < a.cols)) a.q.scales[size_t(c / kBlock) * a.rows + row] = scale;
         if (in && rest(i) > 0) store_e4m3(a.q.q + row * a.q.stride + c, rest(i), v[i], by);
     }
 }
@@ -190,7 +192,7 @@ cudaError_t fwd_moved(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
 
 // Two or three runs a thread from 129 columns on, on as few threads as they fit (512 columns on 64 threads with one run
 // each: 384 against 243 us, with the arithmetic one by one; 100,000 x 768 bf16 on 32 threads with three 151 us, on 64 with
-// two, of which a quarter are idle, 217).  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
+// two, of which a quarter are idle, 217).  125,000 x 640 192 us, 223 asking of every run whether it exists.  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
 template <typename T>
 cudaError_t fwd_width(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
     const int runs = ceil_div(a.cols, 8);
