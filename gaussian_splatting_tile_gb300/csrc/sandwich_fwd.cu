@@ -192,7 +192,8 @@ cudaError_t fwd_moved(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
 
 // Two or three runs a thread from 129 columns on, on as few threads as they fit (512 columns on 64 threads with one run
 // each: 384 against 243 us, with the arithmetic one by one; 100,000 x 768 bf16 on 32 threads with three 151 us, on 64 with
-// two, of which a quarter are idle, 217).  125,000 x 640 192 us, 223 asking of every run whether it exists.  kFull, where nothing asks: 250,000 x 512 243 us, 273 as kRuns.
+// two, of which a quarter are idle, 217).  125,000 x 640 192 us, 223 where every run asked whether it exists; kFull, where
+// none does: 250,000 x 512 243 us, 273 as kRuns.
 template <typename T>
 cudaError_t fwd_width(const SandwichFwdArgs& a, bool vec, cudaStream_t s) {
     const int runs = ceil_div(a.cols, 8);
