@@ -51,8 +51,8 @@ struct Ring {
 };
 
 // One run of a matrix of T on its way into the ring.  p: where this thread's run starts; left: how many of its values
-// exist, not above zero where none does (whole runs are sent where they exist alone).  Where a 16-bit row starts in the middle of a word, the value before it is read
-// with it.
+// exist, not above zero where none does (whole runs are sent where they exist alone).  Where a 16-bit row starts in the
+// middle of a word, the value before it is read with it.
 template <typename R, typename T>
 __device__ __forceinline__ void send(uint8_t* ring, int stage, int run, const T* p, int left) {
     uint8_t* to = R::wide(ring, stage, run);
