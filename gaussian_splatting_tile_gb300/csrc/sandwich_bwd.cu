@@ -447,9 +447,10 @@ int bwd_blocks(int rows, int cols) {
     return most;
 }
 
-// How many clusters the GPU holds at once (a grid of more would run in two turns).
+// How many clusters the GPU holds at once (a grid of more would run in two turns).  Asked in every call: the answer is the
+// current device's, and a question that failed once may not decide later calls.
 template <typename K>
-int clusters_at_once(K kernel, int cluster, int threads, int smem) {
+cudaError_t clusters_at_once(K kernel, int cluster, int threads, int smem, int& n) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = cluster;
     cfg.blockDim = threads;
@@ -460,8 +461,8 @@ int clusters_at_once(K kernel, int cluster, int threads, int smem) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    int n = 0;
-    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+    n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
 }
 
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
@@ -474,7 +475,9 @@ cudaError_t bwd(const SandwichBwdArgs& a, unsigned& parts, cudaStream_t s) {
     }
     int most = kSms * R::kBlocks;
     if constexpr (CL > 1) {
-        static const int at_once = clusters_at_once(kernel, CL, R::kThreads, R::kShared);
+        int at_once;
+        const cudaError_t e = clusters_at_once(kernel, CL, R::kThreads, R::kShared, at_once);
+        if (e != cudaSuccess) return e;
         if (at_once < 1) return cudaErrorInvalidConfiguration;
         most = std::min(at_once, kSms / CL);
     }
