@@ -922,9 +922,9 @@ _NO_FORM = (0, 0, 0)
 
 
 def _kept(pair, name, shape):
-    """The same of an operand, whose scales have to be there."""
+    """The same of an operand, whose scales have to be there (without rows they lie nowhere)."""
     got = _form(pair, name, shape)
-    if not got[2]:
+    if pair[1] is None:
         raise ValueError(f"{name} needs its scales")
     return got
 
