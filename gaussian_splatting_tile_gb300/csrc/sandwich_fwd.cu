@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __
         for (int i = 0; i < RUNS; ++i) {
             m[3 * i] = max_abs8(xv[i]);
             m[3 * i + 1] = max_abs8(rv[i]);
-            if (a.kz.q) m[3 * i + 2] = max_abs8(zv[i]);
+            // gates beyond that become the largest 8-bit value
+            if (a.kz.q) m[3 * i + 2] = fminf(max_abs8(zv[i]), kGateEnd);
         }
         max_over_16(m, of);
         block_scale(m[0], scale, inv);

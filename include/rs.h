@@ -572,7 +572,8 @@ typedef struct rs_sandwich {
 
 /* What the forward writes; every pointer may be NULL, but not both d_y and q.d_q.  d_sum and d_y
  * receive s and y in the block's type; kept_x, kept_r and kept_gate (an element's gate only) the
- * 8-bit forms of the operands, for the backward.  d_rstd_r and d_rstd_s [rows] are the backward's
+ * 8-bit forms of the operands, for the backward; a gate's is that of max(-80, min(z, 80)), beyond
+ * which it is as good as shut or open, so that an infinite one leaves its block the others.  d_rstd_r and d_rstd_s [rows] are the backward's
  * statistics.  d_sum may be d_x or d_r (same stride).  Nothing else may overlap. */
 typedef struct rs_sandwich_out {
     void* d_sum;

@@ -1,4 +1,7 @@
-"""The sandwich norm where its operands come to an end: no rows."""
+"""The sandwich norm where its operands come to an end: no rows, gates that are shut or wide open, kept in 8 bits.
+Tolerances are those of test_gpu_sandwich."""
+import math
+
 import pytest
 import torch
 
@@ -40,3 +43,42 @@ def test_networks_of_no_gaussians(options):
     for p, g in net.parameters():
         assert bool((g == 0).all()) and bool(torch.isfinite(p).all())
     assert float(net.norm) == 0
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [300, 301, 4200])
+def test_gates_at_the_ends_from_checkpoints(dt, cols):
+    """A gate beyond 80 either way is as good as shut or open and is kept as 80, so that neither an infinity nor a type's lowest
+    value takes the other gates of its block of 128 along."""
+    g = S.gen(cols)
+    b = S.Block(g, 12, cols, dt)
+    low, high = torch.finfo(S.DT[dt]).min, torch.finfo(S.DT[dt]).max
+    b.gate[1], b.gate[2], b.gate[3] = -math.inf, math.inf, low
+    b.gate[4, 7], b.gate[5, 130], b.gate[6, 299] = -math.inf, math.inf, low
+    b.gate[7, ::2], b.gate[8, 5], b.gate[9, 5], b.gate[9, 6] = high, 79.5, 80, -80.5
+    b.gate[10, 3], b.gate[10, 4] = 1000, -1000
+    o = b.forward(kept=True)
+    held = b.gate.clamp(-80, 80)
+    want = rs.fp8_empty(b.rows, cols)
+    rs.rs_quantize_fp8(held, *want)
+    assert torch.equal(o["kept_gate"][0].view(torch.uint8), want[0].view(torch.uint8))
+    assert torch.equal(o["kept_gate"][1], want[1])
+    z = b.gate
+    S.keep(b, o)
+    back = rs.fp8_dequantize(*b.gate)
+    # a block's largest gate comes back to two roundings of its scale, the others to half an e4m3 step
+    assert bool(((back - held.float()).abs() <= held.float().abs() / 16 * (1 + 2 ** -20) + 80 / 448 * 2.0 ** -10).all())
+    dy, dsum = S.grads_of(g, b)
+    got = S.check_backward(b, o, dy, dsum)
+    assert all(bool(torch.isfinite(t.float()).all()) for t in got)
+    shut = (z < -80).float()
+    assert bool((got[2].float() * shut).abs().max() < 1e-28)
+
+
+def test_a_gate_that_is_no_number_stays_one():
+    g = S.gen(11)
+    b = S.Block(g, 3, 300, "bf16")
+    b.gate[1, 5] = math.nan
+    o = b.forward(kept=True)
+    z = rs.fp8_dequantize(*o["kept_gate"])
+    assert int(torch.isnan(z).sum()) == 1 and math.isnan(float(z[1, 5]))
