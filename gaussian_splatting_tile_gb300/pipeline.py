@@ -366,8 +366,10 @@ class WideAppearance:
         self.qc, self.qct = q8(n, c), q8(c, n)
         self.qh, self.qht = q8(n, hidden), q8(hidden, n)
         self.q3, self.q3t = q8(n, 3), q8(3, n)
-        self.r, self.dh, self.dy, self.du = e(n, c), e(n, c), e(n, c), e(n, hidden)
-        if sandwich:
+        self.dh, self.dy, self.du = e(n, c), e(n, c), e(n, hidden)
+        if not sandwich:
+            self.r = e(n, c)
+        else:
             self.dr = e(n, c)
             if gate:
                 self.dgate, self.qg, self.qgt = e(n, gates), q8(n, gates), q8(gates, n)
@@ -507,8 +509,7 @@ class WideAppearance:
                     self._norm_backward(b, self.h[b], self.dh, undo)
             if self.sandwich:
                 x = self.h[0]
-                if self.checkpoints:  # the stream has moved on: the features once more
-                    x = self.r
+                if self.checkpoints:  # the stream has moved on, and is not read again: the features once more
                     x.copy_(self.features)
                 self._norm_backward(0, x, self.dh if last else None, undo)
             if down is None:
