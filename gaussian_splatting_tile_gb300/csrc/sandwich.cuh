@@ -12,6 +12,7 @@
 // so that one pass over the row gives all three sums.
 #pragma once
 
+#include "sandwich_plan.h"
 #include "wide.cuh"
 
 namespace rs {
@@ -72,9 +73,6 @@ __device__ __forceinline__ float gate_of(float e) {
 __device__ __forceinline__ float2 gate_e(float2 z) { return make_float2(gate_e(z.x), gate_e(z.y)); }
 __device__ __forceinline__ float2 gate_of(float2 e) { return make_float2(gate_of(e.x), gate_of(e.y)); }
 
-// Threads of a block whose rows are TPR threads each: as many rows as 128 hold, one at least.
-__host__ __device__ constexpr int block_threads(int tpr) { return tpr < 128 ? 128 / tpr * tpr : tpr; }
-
 // A barrier of the TPR threads of a row, in a block of THREADS.  Two rows of 64 do not wait for each other.  (The
 // barriers' numbers stand in the code: with a number from a register a block holds all sixteen, and few blocks fit an
 // SM: 80,000 x 1000 bf16 forward 286 us, with one barrier for both rows 203.)
@@ -97,7 +95,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float* smem) {
         if ((threadIdx.x & 31) == 0)
 #pragma unroll
             for (int k = 0; k < N; ++k) smem[(threadIdx.x >> 5) * N + k] = v[k];
-        row_barrier<TPR, block_threads(TPR)>();
+        row_barrier<TPR, kBlockThreads<TPR>>();
         const float* mine = smem + threadIdx.x / TPR * kWarps * N;
 #pragma unroll
         for (int k = 0; k < N; ++k) {

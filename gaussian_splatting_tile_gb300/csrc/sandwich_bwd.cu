@@ -27,7 +27,7 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 struct Ring {
     static constexpr bool kWhole = MOVE != kAny;                               // runs on 16-byte boundaries
-    static constexpr int kThreads = block_threads(TPR);
+    static constexpr int kThreads = kBlockThreads<TPR>;
     static constexpr int kGroup = TPR < 32 ? TPR : 32, kGroups = kThreads / kGroup;
     static constexpr int kWords = kWhole ? int(sizeof(T)) / 2 : 2 * int(sizeof(T));  // a thread's: of 16 bytes, or of 4
     static constexpr int kGroupBytes = kGroup * (kWhole ? 16 : 4) * kWords + (kWhole || sizeof(T) == 4 ? 0 : 16);
@@ -39,7 +39,7 @@ struct Ring {
     static constexpr int kShared = kBytes + kVectors;                          // what a block is launched with
     static_assert((kThreads == TPR || kBytes >= 12 * RUNS * kThreads * 8) && kShared <= 226 * 1024,
                   "room to join the rows' shares in the ring, and for the block");
-    static constexpr int kBlocks = RUNS == 1 ? 384 / kThreads : kThreads > 128 ? 1 : 2;   // an SM: registers
+    static constexpr int kBlocks = bwd_resident(kThreads, RUNS);                // on an SM
     static __device__ __forceinline__ uint8_t* narrow(uint8_t* ring, int stage, int run) {
         return ring + stage * kStage + (run * kThreads + int(threadIdx.x)) * 8;
     }
@@ -149,7 +149,7 @@ __device__ __forceinline__ void store_there(float* p, int rank, float v) {
 // shared memory, one cluster barrier a row: 10,000 x 8192 bf16 from checkpoints 308 us (3.5 TB/s); one CTA that read such
 // a row twice and kept its shares in shared memory took 506.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
-__global__ void __launch_bounds__(block_threads(TPR), (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
+__global__ void __launch_bounds__(kBlockThreads<TPR>, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))
     k_sandwich_bwd(const __grid_constant__ SandwichBwdArgs a) {
     RS_PDL_ENTER();
     using R = Ring<T, KEPT, MOVE, TPR, RUNS>;
@@ -419,34 +419,6 @@ __global__ void __launch_bounds__(1024) k_sandwich_sums(const float* __restrict_
     if ((threadIdx.x & 31) == 0 && oc < cols) out[oc] = s;
 }
 
-// Threads of a row in a CTA and runs of each; CTAs of a row.  Two runs a thread; in 16 bits, for widths that would leave
-// a quarter of those idle or more, one run on three quarters of the threads instead (100,000 x 768 bf16 from checkpoints
-// on 96 threads 194 us, on 64 with two runs 237; float32 as stored 456, 362 with two).
-struct Shape { int threads, runs; };
-Shape bwd_shape(int cols, bool f32) {
-    const int runs = ceil_div(cols, 8);
-    if (runs <= 16) return {16, 1};
-    if (runs <= 32) return {16, 2};
-    if (runs <= 64) return {32, 2};
-    if (runs <= 96 && !f32) return {96, 1};
-    if (runs <= 128) return {64, 2};
-    if (runs <= 192 && !f32) return {192, 1};
-    if (runs <= 256) return {128, 2};
-    if (runs <= 384 && !f32) return {384, 1};
-    return {256, 2};
-}
-int bwd_ctas(int cols) { return cols <= 4096 ? 1 : cols <= 8192 ? 2 : 4; }
-// The most blocks (clusters) of a call, each with a row of partial sums, whatever its type.
-int bwd_blocks(int rows, int cols) {
-    int most = 1;
-    for (const bool f32 : {false, true}) {
-        const Shape p = bwd_shape(cols, f32);
-        const int threads = block_threads(p.threads), per = p.runs == 1 ? 384 / threads : threads > 128 ? 1 : 2;
-        most = std::max(most, std::min(ceil_div(rows, threads / p.threads), kSms * per / bwd_ctas(cols)));
-    }
-    return most;
-}
-
 // How many clusters the GPU holds at once (a grid of more would run in two turns).  Asked in every call: the answer is the
 // current device's, and a question that failed once may not decide later calls.
 template <typename K>
@@ -528,7 +500,8 @@ extern "C" {
 
 size_t rs_sandwich_norm_bwd_workspace_size(int32_t rows, int32_t cols) {
     if (rows < 0 || cols < 1 || cols > RS_NORM_MAX_COLS) return 0;
-    return size_t(rs::bwd_blocks(rows, cols)) * 3 * cols * sizeof(float);
+    const int blocks = std::max({1, rs::bwd_blocks(rows, cols, false), rs::bwd_blocks(rows, cols, true)});  // whatever the type
+    return size_t(blocks) * 3 * cols * sizeof(float);
 }
 
 int rs_sandwich_norm_bwd(const rs_sandwich* block, const rs_sandwich_grads* grads, void* d_workspace,
