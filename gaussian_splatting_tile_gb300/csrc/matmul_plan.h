@@ -61,11 +61,13 @@ inline Plan plan_matmul(int m, int n, int k) {
 // 256 columns a tile, unsplit.  Otherwise the result goes to the workspace in float32 and from there to 8 bits, in two
 // more launches at most.
 //  - From 65 rows on alone, unless the plan splits a contraction of more than 16 blocks: 160,000 x 512 x 512 58 against
-//    181 us, x 128 x 512 32 against 53, 1000 x 512 x 512 6.8 against 9.0 in a graph, 256 x 2048 x 2048 12.8 against 18.6;
-//    the other way 512 x 256 x 9300 37 against 19.
-//  - Fewer rows alone up to 8 blocks, where a call saves the host a launch: 37 x 1001 x 777 11.8 against 17.4 us, 1 x
-//    1024 x 1024 11.0 against 15.8 (in a graph 8.4 against 5.4); beyond, the rows kernel is worth two launches: 64 x 4096
-//    x 4096 20 against 16.
+//    180 us, x 128 x 512 31 against 53, 1000 x 512 x 512 6.6 against 8.8 in a graph, 256 x 2048 x 2048 12.3 against 16.6;
+//    the other way 512 x 256 x 9300 36 against 17.
+//  - Fewer rows alone up to 8 blocks, where a call costs the host 10 us instead of 14 to 16.  On the GPU, in a graph, that
+//    is right from about 37 rows on (37 x 1001 x 777 7.8 against 12.4 us, 64 x 4096 x 512 6.7 against 13.8), either way at
+//    16 (1024 x 1024 8.2 against 6.7, 1001 x 777 7.7 against 9.3) and wrong for one (1024 x 1024 8.3 against 5.5, 4096 x
+//    512 6.5 against 5.8).  Beyond 8 blocks the rows kernel is worth two launches: 64 x 4096 x 4096 19.4 against 14.4, in
+//    a graph 18.8 against 11.7.
 inline bool direct_8bit(int m, int n, int k) {
     const int blocks = ceil_div(k, kBlock);
     if (m <= 64) return blocks <= 8;

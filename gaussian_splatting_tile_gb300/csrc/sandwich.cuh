@@ -54,9 +54,10 @@ struct SandwichBwdArgs : SandwichArgs {
 constexpr int kNoGate = 0, kRowGate = 1, kElementGate = 2;
 
 // exp(-z) of a gate, held below exp(80) so that g = 1 / (1 + e) and 1 - g = e g are numbers whatever z is (NaN stays):
-// gates below 1.8e-35 count as that.  The forward keeps z within 80 of zero, too, so that a gate's infinity or a type's
-// lowest value is no block's largest magnitude: that would leave the block's other gates no bits, or NaN.  2^x and 1 / x to within two of their last bits, without the steps that would carry
-// results below 2^-126: e near zero adds nothing to 1, and 1 + e is at most 2^116.
+// gates below 1.8e-35 count as that.  (The forward keeps z within 80 of zero, too, so that an infinity or a type's lowest
+// value is no block's largest magnitude: that would leave the block's other gates no bits, or NaN.)  2^x and 1 / x to
+// within two of their last bits, without the steps that would carry results below 2^-126: e near zero adds nothing to 1,
+// and 1 + e is at most 2^116.
 constexpr float kGateEnd = 80.f;
 __device__ __forceinline__ float gate_e(float z) {
     constexpr float kLog2E = 1.44269504f;

@@ -4,9 +4,10 @@ namespace rs {
 namespace {
 
 // ---------------------------------------------------------------- backward
-// The copies of a row's operands on their way: every thread copies its own runs into a place of its own and reads them
-// back itself, so the ring needs no barrier.  Two rows are in flight for each that is worked on.  Through L1, where the
-// two halves of a float32 run's sectors meet (160,000 x 512 float32: 383 against 626 us past it).
+// The copies of a row's operands on their way.  Of rows on 16-byte boundaries every thread copies its own runs into a
+// place of its own and reads them back itself, so the ring needs no barrier.  One or two rows are in flight for each that
+// is worked on: two stages, or three where a stage is at most 24 KB.  Through L1, where the two halves of a float32 run's
+// sectors meet (160,000 x 512 float32: 382 against 626 us past it).
 //
 // With `bytes`, that many of SIZE are read and the rest becomes zero.
 template <int SIZE>
@@ -22,8 +23,9 @@ __device__ __forceinline__ void copy_async(void* dst, const void* src, int bytes
 
 // Rows that are not on 16-byte boundaries come in words, neighbours' words by neighbouring threads: a warp's (a row's
 // sixteen threads') runs follow each other in memory, so their words do, and one more where 16-bit runs start in the
-// middle of a word.  A thread's run then was copied by others of its warp.  (Each thread its own run's words: 80,000 x
-// 1001 bf16 as stored 434 us, float32 894.)
+// middle of a word.  A thread's run then was copied by others of its warp, so the warp meets before it copies over a stage
+// and before it reads one.  (80,000 x 1001 bf16 as stored 382 us, float32 655; each thread its own run's words 434 and
+// 894.)
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS>
 struct Ring {
     static constexpr bool kWhole = MOVE != kAny;                               // runs on 16-byte boundaries
@@ -142,11 +144,12 @@ __device__ __forceinline__ void store_there(float* p, int rank, float v) {
 // warps on an SM; the ring keeps memory busy all the same, and the vectors wait in shared memory, since eight warps do not
 // hide loads from L1 (160,000 x 512 from checkpoints 190 against 256 us).  Measured there: three blocks an SM with spills
 // 372; eight columns a thread on two warps, without the ring, 385; five rows in flight instead of two the same.  190 us is
-// 5.6 TB/s, 83% of the copy's rate, and half of the instructions' rate; as stored 200 us (6.5 TB/s), float32 383 us (6.8
-// TB/s), 10,007 x 1000 float16 35 us, whose last two microseconds are the sums' launch.
+// 5.7 TB/s, 83% of the copy's rate, and half of the instructions' rate; as stored 200 us (6.6 TB/s), float32 382 us (6.9
+// TB/s), 10,007 x 1000 float16 35 us.  The vectors' gradients are 5 to 6 us of that: the partial sums' way out and the
+// launch that adds them up (without them 29.5 and 183 us; 37 x 1001 float32 in a graph 5.3 of 7.4).
 //
 // CL: a row is a cluster's of that many CTAs, 4096 columns each; they tell each other their sums through distributed
-// shared memory, one cluster barrier a row: 10,000 x 8192 bf16 from checkpoints 308 us (3.5 TB/s); one CTA that read such
+// shared memory, one cluster barrier a row: 10,000 x 8192 bf16 from checkpoints 306 us (3.5 TB/s); one CTA that read such
 // a row twice and kept its shares in shared memory took 506.
 template <typename T, bool KEPT, Move MOVE, int TPR, int RUNS, int CL>
 __global__ void __launch_bounds__(kBlockThreads<TPR>, (Ring<T, KEPT, MOVE, TPR, RUNS>::kBlocks))

@@ -37,8 +37,9 @@ __device__ __forceinline__ void store_e4m3(uint8_t* p, int left, const float2 (&
 // over the row, maxima, quotients), and a row of up to 512 values then is a warp's own, without a barrier; arithmetic is
 // in pairs; two operands' or three operands' maxima travel together.  That took 250,000 x 512 bf16, gated, operands kept,
 // from 384 us (103 instructions a value) to 243 (60; 6.4 TB/s, 94% of the copy's rate).  float32 160,000 x 512 233 us
-// (7.1 TB/s); 80,000 x 1000 bf16 194 us (5.0 TB/s: three of a row's 128 runs are empty, and rows of two warps wait for each
-// other); 80,000 x 1001, between words, 247 us.  One row costs the call, 10 us.
+// (7.1 TB/s); 80,000 x 1000 bf16 199 us (4.9 TB/s: three of a row's 128 runs are empty, and rows of two warps wait for each
+// other); 80,000 x 1001, between words, 248 us.  One row costs the call, 10 us, and 3 in a graph; 4099 x 777 float16,
+// between words, 13 and 12.
 template <typename T, Move MOVE, int TPR, int RUNS>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_sandwich_fwd(const __grid_constant__ SandwichFwdArgs a) {
     RS_PDL_ENTER();

@@ -390,7 +390,7 @@ class WideAppearance:
         self.steps = torch.zeros(1, dtype=torch.int32, device=dev)  # taken so far: skipped ones do not count
 
     def kept_bytes(self) -> int:
-        """Bytes of activations that live from the forward to the backward."""
+        """Bytes of the matrices that hold activations from the forward on (what blocks share counts once)."""
         blocks = len(self.up)
         rows = [*self.h[:blocks + 1], *self.rstd]
         rows += [t for pair in (*self.yq, *self.uq) for t in pair] if self.checkpoints else [*self.y, *self.u]

@@ -952,7 +952,8 @@ def rs_sandwich_norm_fwd(x, r, post_weight, pre_weight, q=None, scales=None, gat
     """The end of a residual block: sum = residual_scale x + sigmoid(gate) norm(r) post_weight, and q, scales = the 8-bit
     form of y = norm(sum) pre_weight.  x, r, sum, y [rows, cols] float32 / float16 / bfloat16 CUDA; gate [rows, cols] or
     [rows, 1] of the same type; weights and residual_scale float32 [cols]; rstd_r, rstd_s float32 [rows].  kept_x, kept_r
-    and kept_gate, (q, scales) as fp8_empty(rows, cols) gives them, receive the operands in 8 bits for the backward."""
+    and kept_gate, (q, scales) as fp8_empty(rows, cols) gives them, receive the operands in 8 bits for the backward (gates
+    within 80 of zero)."""
     shape = x.shape
     rows = shape[0]
     dt, f32 = x.dtype, torch.float32

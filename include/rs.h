@@ -544,8 +544,10 @@ typedef struct rs_fp8_matrix {
  *   s = residual_scale x + g rh post_weight,
  *   rstd_s = 1 / sqrt(mean(s^2) + eps),  y = s rstd_s pre_weight, and q = the 8-bit form of y.
  * gate_cols: 0 (no gate, g = 1; d_gate is not read), 1 (one gate a row: z [rows][1]) or cols (one
- * an element).  A gate below 2^-115 counts as exp(-80).  Weights and residual_scale [cols] are
- * float32; residual_scale may be NULL (1).  The norm is taken of the sum before its rounding.
+ * an element).  A gate below exp(-80), 1.8e-35, counts as that, and a 1 - g below 2^-126 as 0;
+ * otherwise g is within (9 + 2.4 |z|) 2^-24 of its value and 1 - g within (13 + 5 |z|) 2^-24.
+ * Weights and residual_scale [cols] are float32; residual_scale may be NULL (1).  The norm is taken
+ * of the sum before its rounding.
  *
  * x, r and an element's gate are matrices of `dtype`, or (in the backward alone) the 8-bit forms
  * that the forward kept: then d_x_scales, d_r_scales and, for an element's gate, d_gate_scales are
@@ -647,10 +649,9 @@ int rs_transpose_fp8(int32_t rows, int32_t cols, const uint8_t* d_q, size_t q_st
 /* rs_matmul_fp8 with its result in 8 bits: d_q [m][n] with d_scales [ceil(n / 128)][m], the 8-bit
  * form of the float32 sums (after the relu, where asked for), ready to be the next product's
  * operand and to be kept for the backward.  (The sums' roundings may be other ones than
- * rs_matmul_fp8's for the same sizes.)  k = 0 gives the form of zeros.  The result must not overlap
- * an operand.  Operands, relu and
- * errors as rs_matmul_fp8; d_workspace: rs_matmul_fp8_q_workspace_size bytes (0: none needed, may
- * be NULL). */
+ * rs_matmul_fp8's for the same sizes; they are the same from call to call.)  k = 0 gives the form
+ * of zeros.  The result must not overlap an operand.  Operands, relu and errors as rs_matmul_fp8;
+ * d_workspace: rs_matmul_fp8_q_workspace_size bytes (0: none needed, may be NULL). */
 size_t rs_matmul_fp8_q_workspace_size(int32_t m, int32_t n, int32_t k);
 int rs_matmul_fp8_q(int32_t m, int32_t n, int32_t k, const uint8_t* d_a, size_t a_stride,
                     const float* d_a_scales, const uint8_t* d_b, size_t b_stride, const float* d_b_scales,

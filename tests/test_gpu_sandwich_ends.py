@@ -46,7 +46,7 @@ def test_networks_of_no_gaussians(options):
 
 
 @pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
-@pytest.mark.parametrize("cols", [300, 301, 4200])
+@pytest.mark.parametrize("cols", [300, 301, 512, 4200])
 def test_gates_at_the_ends_from_checkpoints(dt, cols):
     """A gate beyond 80 either way is as good as shut or open and is kept as 80, so that neither an infinity nor a type's lowest
     value takes the other gates of its block of 128 along."""
